@@ -62,10 +62,10 @@ def listed():
         _linear("linear-64x24576x4096-heads", 64, 24576, 4096, "bf16", "bf16", "silu", True, 4096),
         # odd sizes: rows and columns that end inside a tile
         _linear("linear-333x5001x2112-gelu", 333, 5001, 2112, "bf16", "f32", "gelu", True, 0),
-        # the 8-bit output projection of one sequence's positions
+        # the 8-bit output projection of one sequence's positions, float32 logits
         _linear("linear-7x128256x4096-e4m3", 7, 128256, 4096, "e4m3", "f32", "none", False, 0),
-        # the 8-bit output projection of the headline round
-        _linear("linear-448x128256x4096-e4m3", 448, 128256, 4096, "e4m3", "f32", "none", False, 0),
+        # the 8-bit output projection of the headline round, whose logits are bfloat16
+        _linear("linear-448x128256x4096-e4m3", 448, 128256, 4096, "e4m3", "bf16", "none", False, 0),
         # one decoded token of one sequence: latency
         _adjust("adjust-b1-v32000-step", 1, 0, 32000, "f32", "step", 512, True, 4, False),
         # the headline round's target rows: penalties over histories, the drafts before each position counted
