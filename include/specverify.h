@@ -68,7 +68,20 @@ typedef enum {
   SV_ERR_WORKSPACE = -6  /* scratch could not be provided                         */
 } sv_status;
 
-typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
+typedef enum {
+  SV_F32 = 0,
+  SV_BF16 = 1,
+  SV_E4M3 = 2 /* 8 bits, OCP e4m3 (no infinities): sv_rms_norm's output, sv_linear's operands */
+} sv_dtype;
+
+/* Activations of sv_linear's epilogue. */
+typedef enum {
+  SV_ACT_NONE = 0,
+  SV_ACT_RELU = 1,     /* max(v, 0)                                            */
+  SV_ACT_SILU = 2,     /* v / (1 + exp(-v))                                    */
+  SV_ACT_GELU = 3,     /* v (1 + erf(v / sqrt 2)) / 2                          */
+  SV_ACT_GELU_TANH = 4 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2    */
+} sv_activation;
 
 #define SV_MAX_K 64
 #define SV_MAX_V 2097152 /* 256 chunks of 8192 logits per row */
@@ -77,6 +90,9 @@ typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
  * call with B <= 64, K <= 6 and V <= 128256, in any mode and dtype; a call
  * whose scratch would not fit returns SV_ERR_WORKSPACE. */
 #define SV_NOALLOC_SCRATCH_BYTES (32 << 20)
+#define SV_MAX_NORM_D 65536         /* widest row of sv_rms_norm              */
+#define SV_MAX_LINEAR_K 65536       /* longest sum of sv_linear               */
+#define SV_MAX_HISTORY (1 << 27)    /* tokens per sequence, sv_adjust_logits  */
 /* sv_init flag: also size the stream's buffer of projection logits for
  * sv_spec_verify_lmhead. */
 #define SV_INIT_LMHEAD 1
@@ -396,6 +412,144 @@ int sv_spec_verify_lmhead(const void* hidden_target, const void* weight_target,
                           double* out_p, double* out_q, double* out_z,
                           int32_t B, int32_t K, int32_t V,
                           int32_t d_target, int32_t d_draft, void* stream);
+
+/*
+ * sv_rms_norm - root-mean-square norm with the residual's addition: the step
+ * that makes the hidden states the output projection takes.
+ *   h = x + residual        (h = x without a residual)
+ *   out_j = h_j * weight_j / sqrt(mean_j(h_j^2) + eps)
+ * All sums and products are float32; out is rounded once to its type, and h
+ * to x's type where out_residual asks for it (the norm uses the unrounded h).
+ * With out_dtype SV_E4M3 each row has its scale: out_scale = max(max_j |out_j|
+ * / 448, FLT_MIN), and out_j / out_scale is what is rounded (to nearest, ties
+ * to even) and stored; the row is out * out_scale.
+ *
+ * x            [rows, d] dtype (SV_F32 or SV_BF16), device
+ * residual     [rows, d] dtype, device, or NULL
+ * weight       [d] dtype, device
+ * out          [rows, d] out_dtype (SV_F32, SV_BF16 or SV_E4M3), device
+ * out_scale    [rows] float32, device (SV_E4M3 only; otherwise unused)
+ * out_residual [rows, d] dtype, device, or NULL: receives h (needs residual)
+ * eps          finite, above 0
+ *
+ * out and out_residual may each be x or residual itself (the same pointer and
+ * type: in place); any other overlap of an output with another argument is
+ * SV_ERR_PARAM.  Every element must be aligned to its type; 16-byte aligned
+ * rows take the vectorised path.  A row whose sum of squares is not finite in
+ * float32 (one that holds a NaN or an infinity, for one) comes out all NaN, its
+ * scale too.  1 <= d <= SV_MAX_NORM_D (else SV_ERR_SHAPE).  rows == 0 does
+ * nothing.  Nothing is allocated and no scratch is used, so calls on any
+ * streams may overlap and be captured.
+ */
+int sv_rms_norm(const void* x, const void* residual, const void* weight, float eps, void* out, float* out_scale,
+                void* out_residual, int32_t rows, int32_t d, int32_t dtype, int32_t out_dtype, void* stream);
+
+/*
+ * sv_linear - matrix product with bias, activation and residual in its
+ * epilogue:
+ *   out[m, n] = act(x_scale[m] * weight_scale[n] * sum_k x[m, k] weight[n, k]
+ *                   + bias[n]) + residual[m, n mod residual_cols]
+ * Draft heads on the target's hidden states are such products (several heads
+ * in one call: their weights stacked along n, one residual of K columns shared
+ * by all: residual_cols = K, N = heads * K), and so is the output projection
+ * in 8 bits, whose weight reads are half of sv_lm_logits's.  Products are
+ * exact in float32, the sums and the epilogue are float32, and out is rounded
+ * once.
+ *
+ * x             [M, K] dtype (SV_BF16 or SV_E4M3), device, 16-byte aligned
+ * weight        [N, K] dtype, device, 16-byte aligned
+ * x_scale       [M] float32, weight_scale [N] float32, device: SV_E4M3 only
+ *               (unused for SV_BF16, where the scales are 1)
+ * bias          [N] out_dtype, device, or NULL
+ * residual      [M, residual_cols] out_dtype, device, or NULL; residual_cols
+ *               divides N (unused without a residual)
+ * out           [M, N] out_dtype (SV_F32 or SV_BF16), device (any alignment of
+ *               its type)
+ * activation    sv_activation
+ *
+ * K is a multiple of 64 in [64, SV_MAX_LINEAR_K], N >= 1, M >= 0 (else
+ * SV_ERR_SHAPE); M == 0 does nothing.  out may be the residual itself when
+ * residual_cols == N; any other overlap of out with another argument is
+ * SV_ERR_PARAM.  Infinite sums have no defined activation.  Nothing is
+ * allocated and no scratch is used.
+ */
+int sv_linear(const void* x, const void* weight, const float* x_scale, const float* weight_scale, const void* bias,
+              const void* residual, void* out, int32_t M, int32_t N, int32_t K, int32_t residual_cols,
+              int32_t activation, int32_t dtype, int32_t out_dtype, void* stream);
+
+/*
+ * sv_adjust_logits - penalties for repeated tokens, biases and grammar masks,
+ * applied to the logits before temperature and the filters (page
+ * www.gsyq.cn/news/428210 section 3.3 asks for the same repetition penalty on
+ * the target and the draft: call it on the draft's rows before sv_sample and
+ * on the target's and the draft's rows before sv_spec_verify).  For token j of a
+ * row that stands after the sequence's history and `s` of its drafts, with
+ * c_j = the number of times j occurs in the history behind the prompt and in
+ * those drafts:
+ *   l = logit_j
+ *   l = l > 0 ? l / repetition : l * repetition   if c_j > 0 or j is in the
+ *                                                 prompt
+ *   l = l - frequency * c_j - presence            if c_j > 0
+ *   l = l + every bias listed for j, in its order
+ *   l = -inf                                      if the row's mask forbids j
+ * in float32, rounded once.  Logits that none of these touches keep their
+ * bits.  Row i of a sequence has s = drafts_seen + i.
+ *
+ * logits       [B, R, V] dtype (SV_F32 or SV_BF16), device
+ * out_logits   the same shape and type, device; may be logits itself (in
+ *              place: only the logits that change are written)
+ * history      [B, history_cap] int32, device: the prompt, then the tokens
+ *              accepted so far (NULL if history_cap == 0)
+ * history_len  [B] int32, device, or NULL (history_cap): tokens in use, taken
+ *              as within [0, history_cap]
+ * prompt_len   [B] int32, device, or NULL (0): the first tokens that are the
+ *              prompt, taken as within [0, history_len]
+ * draft_tokens [B, K] int32, device (NULL if K == 0: no drafts are counted)
+ * repetition   [B] float32 above 0, device, or NULL (1)
+ * frequency, presence  [B] float32, device, or NULL (0)
+ * cu_bias      [B + 1] int32 offsets, device, or NULL (no biases): sequence
+ *              b's biases are the entries cu_bias[b] .. cu_bias[b + 1] - 1 of
+ * bias_tokens, bias_values  [num_bias] int32 and float32, device (finite, or
+ *              -inf to ban a token); offsets outside [0, num_bias] are taken
+ *              as its ends
+ * mask         [mask_rows, ceil(V / 32)] 32-bit words, device, or NULL: bit j
+ *              % 32 of word j / 32 is 1 where token j is allowed
+ * mask_index   [B * R] int32, device: each row's row of mask; a row whose index
+ *              lies outside [0, mask_rows) is not masked.  NULL: row r has mask
+ *              row r (mask_rows == B * R)
+ *
+ * Tokens outside [0, V), in any list, are ignored.  A row whose mask allows
+ * nothing comes out all -inf, which verification and sampling report as a row
+ * without a distribution.  Target rows of a round: R = K + 1, drafts_seen 0;
+ * its draft rows: R = K, drafts_seen 0; one row while drafting token i: R = 1,
+ * drafts_seen = i.  K <= SV_MAX_K, drafts_seen + R - 1 <= K unless K == 0 (then
+ * drafts_seen is 0), history_cap <= SV_MAX_HISTORY (else SV_ERR_SHAPE).  Overlap of out_logits with anything but
+ * logits itself is SV_ERR_PARAM.  Nothing is allocated and no scratch is used.
+ */
+int sv_adjust_logits(const void* logits, void* out_logits, const int32_t* history, const int32_t* history_len,
+                     const int32_t* prompt_len, const int32_t* draft_tokens, const float* repetition,
+                     const float* frequency, const float* presence, const int32_t* cu_bias,
+                     const int32_t* bias_tokens, const float* bias_values, const uint32_t* mask,
+                     const int32_t* mask_index, int32_t B, int32_t R, int32_t K, int32_t drafts_seen,
+                     int32_t history_cap, int32_t num_bias, int32_t mask_rows, int32_t V, int32_t dtype, void* stream);
+
+/*
+ * sv_adjust_logits_ragged - sv_adjust_logits on the packed rows of
+ * sv_spec_verify_ragged: sequence b has K_b = cu_num_draft[b + 1] -
+ * cu_num_draft[b] drafts from draft_tokens[cu_num_draft[b]], and K_b +
+ * bonus_rows rows from row cu_num_draft[b] + b * bonus_rows (bonus_rows 1: the
+ * target's rows; 0: the draft's).  Its row i has seen i drafts.  Host values as
+ * for sv_spec_verify_ragged.  Offsets that describe no packing (cu[0] != 0, a
+ * K_b < 0 or > max_k, or cu[B] != total_draft): no row is written, and the call
+ * still returns SV_OK (the verification of the same batch writes sentinels).
+ */
+int sv_adjust_logits_ragged(const void* logits, void* out_logits, const int32_t* history, const int32_t* history_len,
+                            const int32_t* prompt_len, const int32_t* draft_tokens, const int32_t* cu_num_draft,
+                            const float* repetition, const float* frequency, const float* presence,
+                            const int32_t* cu_bias, const int32_t* bias_tokens, const float* bias_values,
+                            const uint32_t* mask, const int32_t* mask_index, int32_t B, int32_t total_draft,
+                            int32_t max_k, int32_t bonus_rows, int32_t history_cap, int32_t num_bias,
+                            int32_t mask_rows, int32_t V, int32_t dtype, void* stream);
 
 /*
  * sv_read_floor - measurement aid, not part of the verification: reads the

@@ -9,3 +9,4 @@ from .dynamic_k import DynamicK  # noqa: F401
 from .lmhead import lm_logits, verify_lmhead  # noqa: F401
 from .near_tie import classify, classify_sample, at_risk, MATCH, FLAGGED, FAIL  # noqa: F401
 from .rate import DrawTables  # noqa: F401
+from . import last_layer  # noqa: F401

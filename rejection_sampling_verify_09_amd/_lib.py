@@ -16,7 +16,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 
 SV_OK, SV_ERR_NULL, SV_ERR_SHAPE, SV_ERR_DTYPE, SV_ERR_PARAM, SV_ERR_HIP, SV_ERR_WORKSPACE = 0, -1, -2, -3, -4, -5, -6
-SV_F32, SV_BF16 = 0, 1
+SV_F32, SV_BF16, SV_E4M3 = 0, 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 SV_MAX_K = 64
 SV_INIT_LMHEAD = 1
 SV_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -58,6 +59,14 @@ def lib() -> ctypes.CDLL:
         L.sv_spec_verify_lmhead.argtypes = [vp, vp, vp, vp, vp, vp, f32, i32, f32, vp, vp, vp, vp, vp, i32, i32, i32,
                                             i32, i32, vp]
         L.sv_spec_verify_lmhead.restype = ctypes.c_int
+        L.sv_rms_norm.argtypes = [vp, vp, vp, f32, vp, vp, vp, i32, i32, i32, i32, vp]
+        L.sv_rms_norm.restype = ctypes.c_int
+        L.sv_linear.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp]
+        L.sv_linear.restype = ctypes.c_int
+        L.sv_adjust_logits.argtypes = [vp] * 14 + [i32] * 9 + [vp]
+        L.sv_adjust_logits.restype = ctypes.c_int
+        L.sv_adjust_logits_ragged.argtypes = [vp] * 15 + [i32] * 9 + [vp]
+        L.sv_adjust_logits_ragged.restype = ctypes.c_int
         L.sv_dynk_create.argtypes = [i32, i32, ctypes.c_double, ctypes.c_double, i32, i32, i32]
         L.sv_dynk_create.restype = vp
         L.sv_dynk_observe.argtypes = [vp, vp, vp, vp]
@@ -408,6 +417,231 @@ def spec_verify_lmhead(hidden_target: torch.Tensor, weight_target: torch.Tensor,
     if debug:
         return out_tokens, out_n, dict(p=out_p, q=out_q, z=out_z)
     return out_tokens, out_n
+
+
+_CODES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float8_e4m3fn: SV_E4M3}
+
+
+def _code(dtype: torch.dtype, name: str, allowed) -> int:
+    if dtype not in allowed:
+        raise TypeError(f"{name} must be one of {', '.join(str(t) for t in allowed)}, got {dtype}")
+    return _CODES[dtype]
+
+
+def _arg(t: torch.Tensor | None, name: str, dtype, shape, like: torch.Tensor):
+    """Pointer of an optional tensor of this type and shape, on the device of ``like``."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    return _dev(t, name)
+
+
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An output tensor, its memory kept until the work on ``stream`` is done."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None and t.is_cuda:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream)))
+    return t
+
+
+def _on_current_device(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+             out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+             out_scale: torch.Tensor | None = None, out_residual: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norm of the last dimension with the residual's
+    addition: h = x + residual, out = h * weight / sqrt(mean(h^2) + eps).
+
+    x [..., d] float32 or bfloat16, weight [d] and residual [..., d] of x's
+    type; out_dtype float32, bfloat16 (x's type by default) or float8_e4m3fn
+    (then with one float32 scale per row: the row is out * out_scale).
+    Returns (out, out_scale [...] or None, h rounded to x's type or None
+    without a residual).  out and out_residual may be x or residual (in
+    place)."""
+    code = _code(x.dtype, "x", (torch.float32, torch.bfloat16))
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    ocode = _code(out_dtype, "out_dtype", (torch.float32, torch.bfloat16, torch.float8_e4m3fn))
+    if x.dim() < 1 or weight.dim() != 1 or x.shape[-1] != weight.shape[0] or weight.shape[0] < 1:
+        raise ValueError("x must be [..., d] and weight [d]")
+    d = weight.shape[0]
+    rows = x.numel() // d
+    wp = _arg(weight, "weight", x.dtype, (d,), x)
+    rp = _arg(residual, "residual", x.dtype, x.shape, x)
+    if residual is None and out_residual is not None:
+        raise ValueError("out_residual needs a residual")
+    if ocode != SV_E4M3 and out_scale is not None:
+        raise ValueError("out_scale goes with out_dtype float8_e4m3fn")
+    op = _arg(out, "out", out_dtype, x.shape, x)
+    sp = _arg(out_scale, "out_scale", torch.float32, x.shape[:-1], x)
+    hp = _arg(out_residual, "out_residual", x.dtype, x.shape, x)
+    _on_current_device(x, "x")
+    if out is None:
+        out = _new(x.shape, out_dtype, x, stream)
+        op = out.data_ptr()
+    if ocode == SV_E4M3 and out_scale is None:
+        out_scale = _new(x.shape[:-1], torch.float32, x, stream)
+        sp = out_scale.data_ptr()
+    if residual is not None and out_residual is None:
+        out_residual = _new(x.shape, x.dtype, x, stream)
+        hp = out_residual.data_ptr()
+    st = lib().sv_rms_norm(_dev(x, "x"), rp, wp, float(eps), op, sp, hp, rows, d, code, ocode, _stream(stream))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "sv_rms_norm")
+    return out, out_scale, out_residual
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+           residual: torch.Tensor | None = None, activation: str = "none", x_scale: torch.Tensor | None = None,
+           weight_scale: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+           out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """act(x_scale * weight_scale * (x weight^T) + bias) + residual.
+
+    x [..., K] and weight [N, K], both bfloat16, or both float8_e4m3fn with
+    x_scale [...] and weight_scale [N] float32; bias [N] and residual
+    [..., R] of out_dtype (float32 or bfloat16), R dividing N: output column n
+    adds residual column n mod R (several draft heads stacked along N share
+    one residual).  activation: "none", "relu", "silu", "gelu" or "gelu_tanh".
+    Returns out [..., N]."""
+    code = _code(x.dtype, "x", (torch.bfloat16, torch.float8_e4m3fn))
+    ocode = _code(out_dtype, "out_dtype", (torch.float32, torch.bfloat16))
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
+    if x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[1] or weight.shape[1] < 1:
+        raise ValueError("x must be [..., K] and weight [N, K]")
+    N, K = weight.shape
+    M = x.numel() // K
+    lead = tuple(x.shape[:-1])
+    if (code == SV_E4M3) != (x_scale is not None) or (code == SV_E4M3) != (weight_scale is not None):
+        raise ValueError("x_scale and weight_scale go with float8_e4m3fn operands")
+    wp = _arg(weight, "weight", x.dtype, (N, K), x)
+    xsp = _arg(x_scale, "x_scale", torch.float32, lead, x)
+    wsp = _arg(weight_scale, "weight_scale", torch.float32, (N,), x)
+    bp = _arg(bias, "bias", out_dtype, (N,), x)
+    R = 0
+    if residual is not None:
+        R = residual.shape[-1] if residual.dim() else 0
+        if R < 1 or N % R != 0:
+            raise ValueError("residual must be [..., R] with R dividing N")
+    rp = _arg(residual, "residual", out_dtype, lead + (R,), x)
+    op = _arg(out, "out", out_dtype, lead + (N,), x)
+    _on_current_device(x, "x")
+    if out is None:
+        out = _new(lead + (N,), out_dtype, x, stream)
+        op = out.data_ptr()
+    st = lib().sv_linear(_dev(x, "x"), wp, xsp, wsp, bp, rp, op, M, N, K, R, ACTIVATIONS[activation], code, ocode,
+                         _stream(stream))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "sv_linear")
+    return out
+
+
+def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, history_len: torch.Tensor | None = None,
+                  prompt_len: torch.Tensor | None = None, draft_tokens: torch.Tensor | None = None,
+                  drafts_seen: int = 0, repetition_penalty: torch.Tensor | None = None,
+                  frequency_penalty: torch.Tensor | None = None, presence_penalty: torch.Tensor | None = None,
+                  bias: tuple | None = None, mask: torch.Tensor | None = None,
+                  mask_index: torch.Tensor | None = None, cu_num_draft: torch.Tensor | None = None,
+                  max_k: int | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Penalties for repeated tokens, biases and grammar masks on logits.
+
+    logits [B, R, V] (row i of a sequence stands after its first drafts_seen
+    + i drafts; draft_tokens [B, K] int32), [B, V] (one row each), or, with
+    cu_num_draft [B + 1] and max_k, the packed rows of spec_verify_ragged: [N +
+    B, V] target rows or [N, V] draft rows (draft_tokens [N] int32).
+    float32 or bfloat16.
+
+    history [B, cap] int32, history_len [B] (cap by default), prompt_len [B]
+    (0 by default): the prompt, then the tokens accepted so far.
+    repetition_penalty (prompt, history and drafts), frequency_penalty and
+    presence_penalty (history behind the prompt, and drafts): [B] float32.
+    bias: (cu_bias [B + 1] int32, tokens int32, values float32).  mask
+    [mask_rows, ceil(V / 32)] int32, bit j % 32 of word j / 32 set where token j
+    is allowed; mask_index [rows] int32, each row's row of mask (outside of it:
+    not masked).  Returns out; out=logits adjusts in place."""
+    code = _code(logits.dtype, "logits", (torch.float32, torch.bfloat16))
+    i32, f32 = torch.int32, torch.float32
+    if logits.dim() not in (2, 3):
+        raise ValueError("logits must be [B, R, V] or [rows, V]")
+    V = logits.shape[-1]
+    if V < 1:
+        raise ValueError("logits must have a vocabulary")
+    rows = logits.numel() // V
+    K = N = bonus = R = 0
+    if cu_num_draft is not None:
+        if logits.dim() != 2 or cu_num_draft.dim() != 1 or cu_num_draft.shape[0] < 1 or max_k is None or drafts_seen:
+            raise ValueError("a ragged batch has logits [rows, V], cu_num_draft [B + 1], max_k and no drafts_seen")
+        B = cu_num_draft.shape[0] - 1
+        N = 0 if draft_tokens is None else draft_tokens.numel()
+        if rows not in (N, N + B):
+            raise ValueError("logits must be [N + B, V] (target rows) or [N, V] (draft rows) for N draft_tokens")
+        bonus = 1 if rows == N + B else 0
+        xp = _arg(draft_tokens, "draft_tokens", i32, (N,), logits)
+        cp = _arg(cu_num_draft, "cu_num_draft", i32, (B + 1,), logits)
+    else:
+        B = logits.shape[0]
+        R = logits.shape[1] if logits.dim() == 3 else 1
+        if draft_tokens is not None:
+            if draft_tokens.dim() != 2:
+                raise ValueError("draft_tokens must be [B, K]")
+            K = draft_tokens.shape[1]
+        xp = _arg(draft_tokens, "draft_tokens", i32, (B, K), logits)
+    cap = 0
+    if history is not None:
+        if history.dim() != 2:
+            raise ValueError("history must be [B, cap]")
+        cap = history.shape[1]
+    elif history_len is not None or prompt_len is not None:
+        raise ValueError("history_len and prompt_len go with a history")
+    hp = _arg(history, "history", i32, (B, cap), logits)
+    hl = _arg(history_len, "history_len", i32, (B,), logits)
+    pl = _arg(prompt_len, "prompt_len", i32, (B,), logits)
+    rp = _arg(repetition_penalty, "repetition_penalty", f32, (B,), logits)
+    fp = _arg(frequency_penalty, "frequency_penalty", f32, (B,), logits)
+    pp = _arg(presence_penalty, "presence_penalty", f32, (B,), logits)
+    cb = bt = bv = None
+    nb = 0
+    if bias is not None:
+        cu_bias, btok, bval = bias
+        nb = btok.numel()
+        cb = _arg(cu_bias, "cu_bias", i32, (B + 1,), logits)
+        bt = _arg(btok, "bias tokens", i32, (nb,), logits)
+        bv = _arg(bval, "bias values", f32, (nb,), logits)
+    mrows = 0
+    if mask is not None:
+        mrows = mask.shape[0] if mask.dim() == 2 else -1
+        if mask_index is None and mrows != rows:
+            raise ValueError("mask must have a row for each row of logits, unless mask_index says which")
+    elif mask_index is not None:
+        raise ValueError("mask_index goes with a mask")
+    mp = _arg(mask, "mask", i32, (mrows, (V + 31) // 32), logits)
+    mi = _arg(mask_index, "mask_index", i32, (rows,), logits)
+    op = _arg(out, "out", logits.dtype, logits.shape, logits)
+    _on_current_device(logits, "logits")
+    if out is None:
+        out = _new(logits.shape, logits.dtype, logits, stream)
+        op = out.data_ptr()
+    lp, s = _dev(logits, "logits"), _stream(stream)
+    if cu_num_draft is not None:
+        st = lib().sv_adjust_logits_ragged(lp, op, hp, hl, pl, xp, cp, rp, fp, pp, cb, bt, bv, mp, mi, B, N, int(max_k),
+                                           bonus, cap, nb, mrows, V, code, s)
+        what = "sv_adjust_logits_ragged"
+    else:
+        st = lib().sv_adjust_logits(lp, op, hp, hl, pl, xp, rp, fp, pp, cb, bt, bv, mp, mi, B, R, K, int(drafts_seen), cap,
+                                    nb, mrows, V, code, s)
+        what = "sv_adjust_logits"
+    if st != SV_OK:
+        raise SpecVerifyError(st, what)
+    return out
 
 
 class DraftLengthController:
