@@ -437,7 +437,8 @@ int sv_spec_verify_lmhead(const void* hidden_target, const void* weight_target,
  * SV_ERR_PARAM.  Every element must be aligned to its type; 16-byte aligned
  * rows take the vectorised path.  A row whose sum of squares is not finite in
  * float32 (one that holds a NaN or an infinity, for one) comes out all NaN, its
- * scale too.  1 <= d <= SV_MAX_NORM_D (else SV_ERR_SHAPE).  rows == 0 does
+ * scale too.  1 <= d <= SV_MAX_NORM_D, and rows * min(1024, d / 8 in whole
+ * waves) threads within one launch (else SV_ERR_SHAPE).  rows == 0 does
  * nothing.  Nothing is allocated and no scratch is used, so calls on any
  * streams may overlap and be captured.
  */
@@ -489,10 +490,11 @@ int sv_linear(const void* x, const void* weight, const float* x_scale, const flo
  *   l = logit_j
  *   l = l > 0 ? l / repetition : l * repetition   if c_j > 0 or j is in the
  *                                                 prompt
- *   l = l - frequency * c_j - presence            if c_j > 0
+ *   l = l - (frequency * c_j + presence)          if c_j > 0
  *   l = l + every bias listed for j, in its order
  *   l = -inf                                      if the row's mask forbids j
- * in float32, rounded once.  Logits that none of these touches keep their
+ * in float32 (l / repetition as a product with the rounded reciprocal), rounded
+ * once.  Logits that none of these touches keep their
  * bits.  Row i of a sequence has s = drafts_seen + i.
  *
  * logits       [B, R, V] dtype (SV_F32 or SV_BF16), device

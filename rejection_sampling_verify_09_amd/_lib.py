@@ -124,7 +124,8 @@ def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without building the stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -428,32 +429,34 @@ def _code(dtype: torch.dtype, name: str, allowed) -> int:
     return _CODES[dtype]
 
 
-def _arg(t: torch.Tensor | None, name: str, dtype, shape, like: torch.Tensor):
-    """Pointer of an optional tensor of this type and shape, on the device of ``like``."""
+def _arg(t: torch.Tensor | None, name: str, dtype, shape, dev: int):
+    """Pointer of an optional contiguous tensor of this type and shape on device ``dev`` (-1: not a device)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
-    return _dev(t, name)
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a device tensor" + (f" on cuda:{dev}" if dev >= 0 else ""))
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """An output tensor, its memory kept until the work on ``stream`` is done."""
     t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None and t.is_cuda:
+    if stream is not None:
         t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream)))
     return t
 
 
-def _on_current_device(t: torch.Tensor, name: str) -> None:
-    if not t.is_cuda:
+def _on_current_device(dev: int, name: str) -> None:
+    if dev < 0:
         raise ValueError(f"{name} must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -475,16 +478,18 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
         raise ValueError("x must be [..., d] and weight [d]")
     d = weight.shape[0]
     rows = x.numel() // d
-    wp = _arg(weight, "weight", x.dtype, (d,), x)
-    rp = _arg(residual, "residual", x.dtype, x.shape, x)
+    dev = x.get_device()
+    wp = _arg(weight, "weight", x.dtype, (d,), dev)
+    rp = _arg(residual, "residual", x.dtype, x.shape, dev)
     if residual is None and out_residual is not None:
         raise ValueError("out_residual needs a residual")
     if ocode != SV_E4M3 and out_scale is not None:
         raise ValueError("out_scale goes with out_dtype float8_e4m3fn")
-    op = _arg(out, "out", out_dtype, x.shape, x)
-    sp = _arg(out_scale, "out_scale", torch.float32, x.shape[:-1], x)
-    hp = _arg(out_residual, "out_residual", x.dtype, x.shape, x)
-    _on_current_device(x, "x")
+    op = _arg(out, "out", out_dtype, x.shape, dev)
+    sp = _arg(out_scale, "out_scale", torch.float32, x.shape[:-1], dev)
+    hp = _arg(out_residual, "out_residual", x.dtype, x.shape, dev)
+    xp = _arg(x, "x", x.dtype, x.shape, dev)
+    _on_current_device(dev, "x")
     if out is None:
         out = _new(x.shape, out_dtype, x, stream)
         op = out.data_ptr()
@@ -494,7 +499,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     if residual is not None and out_residual is None:
         out_residual = _new(x.shape, x.dtype, x, stream)
         hp = out_residual.data_ptr()
-    st = lib().sv_rms_norm(_dev(x, "x"), rp, wp, float(eps), op, sp, hp, rows, d, code, ocode, _stream(stream))
+    st = lib().sv_rms_norm(xp, rp, wp, float(eps), op, sp, hp, rows, d, code, ocode, _stream(stream))
     if st != SV_OK:
         raise SpecVerifyError(st, "sv_rms_norm")
     return out, out_scale, out_residual
@@ -520,25 +525,27 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
         raise ValueError("x must be [..., K] and weight [N, K]")
     N, K = weight.shape
     M = x.numel() // K
-    lead = tuple(x.shape[:-1])
+    lead = x.shape[:-1]
+    dev = x.get_device()
     if (code == SV_E4M3) != (x_scale is not None) or (code == SV_E4M3) != (weight_scale is not None):
         raise ValueError("x_scale and weight_scale go with float8_e4m3fn operands")
-    wp = _arg(weight, "weight", x.dtype, (N, K), x)
-    xsp = _arg(x_scale, "x_scale", torch.float32, lead, x)
-    wsp = _arg(weight_scale, "weight_scale", torch.float32, (N,), x)
-    bp = _arg(bias, "bias", out_dtype, (N,), x)
+    wp = _arg(weight, "weight", x.dtype, (N, K), dev)
+    xsp = _arg(x_scale, "x_scale", torch.float32, lead, dev)
+    wsp = _arg(weight_scale, "weight_scale", torch.float32, (N,), dev)
+    bp = _arg(bias, "bias", out_dtype, (N,), dev)
     R = 0
     if residual is not None:
         R = residual.shape[-1] if residual.dim() else 0
         if R < 1 or N % R != 0:
             raise ValueError("residual must be [..., R] with R dividing N")
-    rp = _arg(residual, "residual", out_dtype, lead + (R,), x)
-    op = _arg(out, "out", out_dtype, lead + (N,), x)
-    _on_current_device(x, "x")
+    rp = _arg(residual, "residual", out_dtype, lead + (R,), dev)
+    op = _arg(out, "out", out_dtype, lead + (N,), dev)
+    xp = _arg(x, "x", x.dtype, x.shape, dev)
+    _on_current_device(dev, "x")
     if out is None:
         out = _new(lead + (N,), out_dtype, x, stream)
         op = out.data_ptr()
-    st = lib().sv_linear(_dev(x, "x"), wp, xsp, wsp, bp, rp, op, M, N, K, R, ACTIVATIONS[activation], code, ocode,
+    st = lib().sv_linear(xp, wp, xsp, wsp, bp, rp, op, M, N, K, R, ACTIVATIONS[activation], code, ocode,
                          _stream(stream))
     if st != SV_OK:
         raise SpecVerifyError(st, "sv_linear")
@@ -576,6 +583,7 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
     if V < 1:
         raise ValueError("logits must have a vocabulary")
     rows = logits.numel() // V
+    dev = logits.get_device()
     K = N = bonus = R = 0
     if cu_num_draft is not None:
         if logits.dim() != 2 or cu_num_draft.dim() != 1 or cu_num_draft.shape[0] < 1 or max_k is None or drafts_seen:
@@ -585,8 +593,8 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
         if rows not in (N, N + B):
             raise ValueError("logits must be [N + B, V] (target rows) or [N, V] (draft rows) for N draft_tokens")
         bonus = 1 if rows == N + B else 0
-        xp = _arg(draft_tokens, "draft_tokens", i32, (N,), logits)
-        cp = _arg(cu_num_draft, "cu_num_draft", i32, (B + 1,), logits)
+        xp = _arg(draft_tokens, "draft_tokens", i32, (N,), dev)
+        cp = _arg(cu_num_draft, "cu_num_draft", i32, (B + 1,), dev)
     else:
         B = logits.shape[0]
         R = logits.shape[1] if logits.dim() == 3 else 1
@@ -594,7 +602,7 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
             if draft_tokens.dim() != 2:
                 raise ValueError("draft_tokens must be [B, K]")
             K = draft_tokens.shape[1]
-        xp = _arg(draft_tokens, "draft_tokens", i32, (B, K), logits)
+        xp = _arg(draft_tokens, "draft_tokens", i32, (B, K), dev)
     cap = 0
     if history is not None:
         if history.dim() != 2:
@@ -602,20 +610,20 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
         cap = history.shape[1]
     elif history_len is not None or prompt_len is not None:
         raise ValueError("history_len and prompt_len go with a history")
-    hp = _arg(history, "history", i32, (B, cap), logits)
-    hl = _arg(history_len, "history_len", i32, (B,), logits)
-    pl = _arg(prompt_len, "prompt_len", i32, (B,), logits)
-    rp = _arg(repetition_penalty, "repetition_penalty", f32, (B,), logits)
-    fp = _arg(frequency_penalty, "frequency_penalty", f32, (B,), logits)
-    pp = _arg(presence_penalty, "presence_penalty", f32, (B,), logits)
+    hp = _arg(history, "history", i32, (B, cap), dev)
+    hl = _arg(history_len, "history_len", i32, (B,), dev)
+    pl = _arg(prompt_len, "prompt_len", i32, (B,), dev)
+    rp = _arg(repetition_penalty, "repetition_penalty", f32, (B,), dev)
+    fp = _arg(frequency_penalty, "frequency_penalty", f32, (B,), dev)
+    pp = _arg(presence_penalty, "presence_penalty", f32, (B,), dev)
     cb = bt = bv = None
     nb = 0
     if bias is not None:
         cu_bias, btok, bval = bias
         nb = btok.numel()
-        cb = _arg(cu_bias, "cu_bias", i32, (B + 1,), logits)
-        bt = _arg(btok, "bias tokens", i32, (nb,), logits)
-        bv = _arg(bval, "bias values", f32, (nb,), logits)
+        cb = _arg(cu_bias, "cu_bias", i32, (B + 1,), dev)
+        bt = _arg(btok, "bias tokens", i32, (nb,), dev)
+        bv = _arg(bval, "bias values", f32, (nb,), dev)
     mrows = 0
     if mask is not None:
         mrows = mask.shape[0] if mask.dim() == 2 else -1
@@ -623,14 +631,15 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
             raise ValueError("mask must have a row for each row of logits, unless mask_index says which")
     elif mask_index is not None:
         raise ValueError("mask_index goes with a mask")
-    mp = _arg(mask, "mask", i32, (mrows, (V + 31) // 32), logits)
-    mi = _arg(mask_index, "mask_index", i32, (rows,), logits)
-    op = _arg(out, "out", logits.dtype, logits.shape, logits)
-    _on_current_device(logits, "logits")
+    mp = _arg(mask, "mask", i32, (mrows, (V + 31) // 32), dev)
+    mi = _arg(mask_index, "mask_index", i32, (rows,), dev)
+    op = _arg(out, "out", logits.dtype, logits.shape, dev)
+    lp = _arg(logits, "logits", logits.dtype, logits.shape, dev)
+    _on_current_device(dev, "logits")
     if out is None:
         out = _new(logits.shape, logits.dtype, logits, stream)
         op = out.data_ptr()
-    lp, s = _dev(logits, "logits"), _stream(stream)
+    s = _stream(stream)
     if cu_num_draft is not None:
         st = lib().sv_adjust_logits_ragged(lp, op, hp, hl, pl, xp, cp, rp, fp, pp, cb, bt, bv, mp, mi, B, N, int(max_k),
                                            bonus, cap, nb, mrows, V, code, s)

@@ -24,6 +24,7 @@ def norm(x=P(0), res=P(1), w=P(2), eps=1e-6, out=P(3), scale=P(4), hres=P(5), ro
 
 @pytest.mark.parametrize("kw,code", [
     (dict(rows=-1), L.SV_ERR_SHAPE), (dict(d=0), L.SV_ERR_SHAPE), (dict(d=65537), L.SV_ERR_SHAPE),
+    (dict(rows=1 << 23, d=8192), L.SV_ERR_SHAPE),  # more threads than one launch holds
     (dict(dt=L.SV_E4M3), L.SV_ERR_DTYPE), (dict(dt=7), L.SV_ERR_DTYPE), (dict(odt=3), L.SV_ERR_DTYPE),
     (dict(eps=0.0), L.SV_ERR_PARAM), (dict(eps=-1.0), L.SV_ERR_PARAM), (dict(eps=math.nan), L.SV_ERR_PARAM),
     (dict(eps=math.inf), L.SV_ERR_PARAM),
