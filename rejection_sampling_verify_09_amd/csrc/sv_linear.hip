@@ -2,26 +2,33 @@
 //   out[m, n] = act(sx[m] sw[n] sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n mod R]
 // on the matrix cores, for bfloat16 operands or e4m3 operands with a float32
 // scale per row.  Products of two bfloat16 values are exact in float32 and are
-// summed in float32 (v_mfma_f32_32x32x16_bf16); the epilogue is float32 too,
+// summed in float32 (v_mfma_f32_16x16x32_bf16); the epilogue is float32 too,
 // rounded once.
 //
-// The 8-bit matrix instructions (v_mfma_f32_32x32x64_f8f6f4, twice the
+// The 8-bit matrix instructions (v_mfma_f32_16x16x128_f8f6f4, twice the
 // bfloat16 rate) keep their accumulators in float32 but form the sums of a
 // few products with fewer bits: measured on normal values, 1.5e-5 of the
 // result (2-norm), whatever the length of the sum and with every 8-bit form.
-// That lies 100 times below the half step of a bfloat16 output (2^-9 of the
-// value on average) and is used there; for a float32 output the operands are
-// converted to bfloat16 (exactly: 4 significant bits) and multiplied as such,
-// which measures 8e-8.
+// That lies 100 times below the rounding of a bfloat16 output and is used
+// there; for a float32 output the operands are converted to bfloat16 (exactly:
+// 4 significant bits) and multiplied as such, which measures 8e-8.
+//
+// Two kernels: linear_rows_kernel for up to 16 rows, which streams the weight
+// from memory into registers, and linear_tile_kernel, whose tiles launch_linear
+// chooses.  In both the weight is the matrix instruction's first operand, so
+// that a lane holds four consecutive columns of the output.
 #include "sv_ops.hpp"
 #include "specverify.h"
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
 
 namespace sv {
 
 namespace {
 
 typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 bf16x8;
-typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
 typedef __attribute__((__vector_size__(8 * sizeof(int)))) int i32x8;
 
 enum Act : int { A_NONE = 0, A_RELU = 1, A_SILU = 2, A_GELU = 3, A_GELU_TANH = 4 };
@@ -56,20 +63,6 @@ __device__ __forceinline__ float load_o(const void* p, size_t i) {
   return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
 }
 
-// out[m, n] from its sum
-template <int IN, int OUT>
-__device__ __forceinline__ void put(const LinArgs& a, int m, int n, float v) {
-  if (IN == T_E4M3) v = v * a.sx[m] * a.sw[n];
-  if (a.bias) v += load_o<OUT>(a.bias, n);
-  v = activate(v, a.act);
-  if (a.res) v += load_o<OUT>(a.res, (size_t)m * a.R + n % a.R);
-  const size_t at = (size_t)m * a.N + n;
-  if (OUT == T_F32)
-    static_cast<float*>(a.out)[at] = v;
-  else
-    static_cast<uint16_t*>(a.out)[at] = to_bf16(v);
-}
-
 // Eight e4m3 values as bfloat16 (exact).
 __device__ __forceinline__ bf16x8 widen8(uint2 v) {
   bf16x2 p[4];
@@ -80,69 +73,447 @@ __device__ __forceinline__ bf16x8 widen8(uint2 v) {
   return __builtin_bit_cast(bf16x8, p);
 }
 
-constexpr int LROW = 144;  // LDS bytes of a staged row: 128 of data, 16 of padding
+// How the sums are formed: bfloat16 operands; e4m3 operands on the 8-bit
+// instructions (bfloat16 output); e4m3 operands widened to bfloat16 (float32
+// output).
+enum Mode : int { L_BF16 = 0, L_F8 = 1, L_F8W = 2 };
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
 
-// 64 x 64 tile, 4 waves of 32 x 32, k blocks of 128 bytes.
-template <int IN, int OUT>
-__global__ void __launch_bounds__(256) linear_kernel(LinArgs a) {
-  __shared__ __attribute__((aligned(16))) char xs[64 * LROW];
-  __shared__ __attribute__((aligned(16))) char ws[64 * LROW];
-  const int nt = blockIdx.x / a.mtiles, mt = blockIdx.x - nt * a.mtiles;
-  const int m0 = mt * 64, n0 = nt * 64;
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6, h = lane >> 5, l32 = lane & 31;
-  const int kbytes = a.K * (IN == T_BF16 ? 2 : 1);
-  f32x16 acc;
+typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
+
+// A 16-row fragment of 128 bytes of k: lane l holds row l % 16 and, of its 128
+// bytes, the 16-byte chunks l / 16 and 4 + l / 16, in both operands.
+typedef i32x8 Frag;
+__device__ __forceinline__ Frag frag(const i32x4& a, const i32x4& b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+template <int I>
+__device__ __forceinline__ i32x4 half(const Frag& f) {
+  return __builtin_shufflevector(f, f, 4 * I, 4 * I + 1, 4 * I + 2, 4 * I + 3);
+}
+
+// Products of a (rows of the result) and NB fragments b (columns), added to c.
+template <int MODE, int NB>
+__device__ __forceinline__ void mma16(f32x4 (&c)[NB], const Frag& x, const Frag (&w)[NB]) {
+  if (MODE == L_F8) {
 #pragma unroll
-  for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
-  for (int k0 = 0; k0 < kbytes; k0 += 128) {
-    const int nb = min(128, kbytes - k0);  // 128, or 64 in the last block of e4m3 operands
+    for (int j = 0; j < NB; ++j) c[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[j], x, c[j], 0, 0, 0, 0, 0, 0);
+  } else if (MODE == L_BF16) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 32 * i + (t >> 3), c = t & 7;
-      if (16 * c < nb) {
-        *reinterpret_cast<uint4*>(xs + r * LROW + 16 * c) =
-            *reinterpret_cast<const uint4*>(a.x + (size_t)min(m0 + r, a.M - 1) * kbytes + k0 + 16 * c);
-        *reinterpret_cast<uint4*>(ws + r * LROW + 16 * c) =
-            *reinterpret_cast<const uint4*>(a.w + (size_t)min(n0 + r, a.N - 1) * kbytes + k0 + 16 * c);
-      }
+    for (int j = 0; j < NB; ++j)
+      c[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, half<0>(w[j])), __builtin_bit_cast(bf16x8, half<0>(x)), c[j], 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      c[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, half<1>(w[j])), __builtin_bit_cast(bf16x8, half<1>(x)), c[j], 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bf16x8 xv = widen8(make_uint2((uint32_t)x[2 * i], (uint32_t)x[2 * i + 1]));
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        c[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(make_uint2((uint32_t)w[j][2 * i], (uint32_t)w[j][2 * i + 1])), xv, c[j], 0, 0, 0);
     }
-    __syncthreads();
-    const char* xa = xs + (32 * (w >> 1) + l32) * LROW;
-    const char* wa = ws + (32 * (w & 1) + l32) * LROW;
-    if (IN == T_BF16) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(xa + 32 * s + 16 * h),
-                                                      *reinterpret_cast<const bf16x8*>(wa + 32 * s + 16 * h), acc, 0, 0, 0);
-    } else if (OUT == T_F32) {
-      for (int s = 0; s < nb / 16; ++s)
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8(*reinterpret_cast<const uint2*>(xa + 16 * s + 8 * h)),
-                                                      widen8(*reinterpret_cast<const uint2*>(wa + 16 * s + 8 * h)), acc, 0, 0, 0);
-    } else {
-      for (int s = 0; s < nb / 64; ++s) {
-        const i32x8 xf = *reinterpret_cast<const i32x8*>(xa + 64 * s + 32 * h);
-        const i32x8 wf = *reinterpret_cast<const i32x8*>(wa + 64 * s + 32 * h);
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xf, wf, acc, 0, 0, 0, 127, 0, 127);
-      }
-    }
-    __syncthreads();
-  }
-  // lane (h, l32), accumulator r: row 8 (r / 4) + 4 h + r % 4, column l32
-  const int n = n0 + 32 * (w & 1) + l32;
-  if (n >= a.N) return;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int m = m0 + 32 * (w >> 1) + 8 * (r >> 2) + 4 * h + (r & 3);
-    if (m < a.M) put<IN, OUT>(a, m, n, acc[r]);
   }
 }
 
+// A 16-byte buffer load, zeros where `in` is false (an offset past every buffer).
+__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t r, int off, int soff, bool in) {
+  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, in ? off : 0x7FFFFF00, in ? soff : 0, 0));
+}
+
+// The epilogue of four columns n .. n + 3 (n a multiple of 4), those below N:
+// what depends on the columns alone is read once for all rows.
 template <int IN, int OUT>
-hipError_t launch_linear(LinArgs a, hipStream_t s) {
-  a.mtiles = (a.M + 63) / 64;
-  a.ntiles = (a.N + 63) / 64;
-  hipLaunchKernelGGL((linear_kernel<IN, OUT>), dim3((unsigned)a.mtiles * (unsigned)a.ntiles), dim3(256), 0, s, a);
+struct Cols {
+  float sw[4], bias[4];
+  int n, nv, rc;
+  __device__ __forceinline__ Cols(const LinArgs& a, int n_) : n(n_), nv(min(4, a.N - n_)), rc(a.res ? n_ % a.R : 0) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      sw[r] = IN == T_E4M3 && r < nv ? a.sw[n + r] : 1.0f;
+      bias[r] = a.bias && r < nv ? load_o<OUT>(a.bias, n + r) : 0.0f;
+    }
+  }
+  __device__ __forceinline__ void put(const LinArgs& a, int m, const f32x4& s, float sx) const {
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      v[r] = IN == T_E4M3 ? s[r] * sx * sw[r] : s[r];
+      if (a.bias) v[r] += bias[r];
+    }
+    if (a.act != A_NONE) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = activate(v[r], a.act);
+    }
+    if (a.res) {
+      int c = rc;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r < nv) v[r] += load_o<OUT>(a.res, (size_t)m * a.R + c);
+        c = c + 1 == a.R ? 0 : c + 1;
+      }
+    }
+    const size_t at = (size_t)m * a.N + n;
+    if (nv == 4) {
+      // rows may start at any element: the hardware splits a store where it crosses
+      if (OUT == T_F32) {
+        const float4 q = make_float4(v[0], v[1], v[2], v[3]);
+        __builtin_memcpy(static_cast<float*>(a.out) + at, &q, 16);
+      } else {
+        const uint2 q = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        __builtin_memcpy(static_cast<uint16_t*>(a.out) + at, &q, 8);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < nv) {
+          if (OUT == T_F32)
+            static_cast<float*>(a.out)[at + r] = v[r];
+          else
+            static_cast<uint16_t*>(a.out)[at + r] = to_bf16(v[r]);
+        }
+    }
+  }
+};
+
+// Few rows: a workgroup owns 16 MT rows and 16 NT columns of the output, its W
+// waves take turns over the 128-byte steps of k, D of them in flight in
+// registers, straight from memory; the waves' sums are added in LDS.  Bound by
+// the weight's bytes: 1 x 4096 x 4096 bfloat16 takes 8.6 us on the device (3.9
+// TB/s, the launch and the first loads' way included), 1 x 128256 x 4096 e4m3
+// 90 us (5.8 TB/s).
+template <int MODE, int OUT, int NT, int MT, int W, int D>
+__global__ void __launch_bounds__(64 * W) linear_rows_kernel(LinArgs a) {
+  constexpr int IN = MODE == L_BF16 ? T_BF16 : T_E4M3;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  f32x4* part = reinterpret_cast<f32x4*>(smem);  // [W][MT * NT * 64]
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int nt0 = blockIdx.x / a.mtiles, mt0 = blockIdx.x - nt0 * a.mtiles;
+  const int m0 = mt0 * 16 * MT, n0 = nt0 * 16 * NT;
+  const int kbytes = a.K * (IN == T_BF16 ? 2 : 1);
+  const int steps = (kbytes + 127) / 128;
+  // buffer loads that end at the last valid row: rows past it read as zeros
+  const auto rx = wave_rsrc(a.x + (size_t)m0 * kbytes, min(16 * MT, a.M - m0) * kbytes);
+  const auto rw = wave_rsrc(a.w + (size_t)n0 * kbytes, min(16 * NT, a.N - n0) * kbytes);
+  const int off = l16 * kbytes + 16 * g;
+  Frag xf[D][MT], wf[D][NT];
+  auto load = [&](Frag (&x)[MT], Frag (&wt)[NT], int step) {
+    const int k0 = step * 128;
+    const bool whole = IN == T_BF16 || k0 + 64 < kbytes;  // the last 64 bytes of k may stand alone
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      wt[j] = frag(load16(rw, off + j * 16 * kbytes, k0, true), load16(rw, off + j * 16 * kbytes, k0 + 64, whole));
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      x[j] = frag(load16(rx, off + j * 16 * kbytes, k0, true), load16(rx, off + j * 16 * kbytes, k0 + 64, whole));
+  };
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (w + d * W < steps) load(xf[d], wf[d], w + d * W);
+  for (int s = w; s < steps; s += D * W) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (s + d * W < steps) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) mma16<MODE>(acc[i], xf[d][i], wf[d]);
+        if (s + (d + D) * W < steps) load(xf[d], wf[d], s + (d + D) * W);
+      }
+    }
+  }
+  // lane l of block (i, j) holds row 16 i + l % 16, columns 16 j + 4 (l / 16) + 0 .. 3
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[(w * MT * NT + i * NT + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  for (int q = t; q < MT * NT * 64; q += 64 * W) {
+    // four threads along each 16-column block, its row's blocks next
+    const int c = q & 3, j = (q >> 2) % NT, row = (q >> 2) / NT;
+    const int m = m0 + row, n = n0 + 16 * j + 4 * c;
+    if (m >= a.M || n >= a.N) continue;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < W; ++k) v += part[(k * MT * NT + (row >> 4) * NT + j) * 64 + 16 * c + (row & 15)];
+    Cols<IN, OUT>(a, n).put(a, m, v, IN == T_E4M3 ? a.sx[m] : 1.0f);
+  }
+}
+
+template <int MODE, int OUT, int NT, int MT, int W, int D>
+hipError_t launch_rows(LinArgs a, hipStream_t s) {
+  a.mtiles = (a.M + 16 * MT - 1) / (16 * MT);
+  a.ntiles = (a.N + 16 * NT - 1) / (16 * NT);
+  const size_t lds = (size_t)W * MT * NT * 64 * sizeof(f32x4);
+  hipLaunchKernelGGL((linear_rows_kernel<MODE, OUT, NT, MT, W, D>), dim3((unsigned)a.mtiles * (unsigned)a.ntiles),
+                     dim3(64 * W), lds, s, a);
   return hipGetLastError();
+}
+
+constexpr int tile_eb(int mb, int wm) { return mb * wm < 4 ? mb : 4 / wm; }  // 16-row blocks per pass of the epilogue
+constexpr int lcm2(int a, int b) { return a % b == 0 ? a : b % a == 0 ? b : a * b; }  // of such small numbers
+constexpr int lcm3(int a, int b, int c) { return lcm2(lcm2(a, b), c); }
+constexpr int LIN_XCD = 8;  // XCDs the workgroup ids are dealt over
+
+// More rows: a workgroup owns TM = 16 MB WM rows and TN = 16 NB WN columns; WM
+// x WN waves share it, 16 MB x 16 NB each, and WK such groups take turns over
+// the 128-byte steps of k, WK steps a round (their sums are added in LDS).
+// Both operands go through LDS, loaded as whole 128-byte lines, eight rows a
+// load: a fragment's own layout, 16 rows across neighbouring lanes, keeps the
+// address unit four times as long (64 against 16 cycles a load), which held
+// an earlier form with the weight straight in registers at 243 us where this
+// one takes 233 (448 x 128256 x 4096, e4m3 to bfloat16), and at 23.5 us where
+// this one takes 18 (333 x 5001 x 2112).
+//
+// What bounds the largest tile (224 x 256, k blocks of 128 bytes, 8 waves, one
+// workgroup a compute unit): its rounds take about 1.4 us, 1.0 of them the
+// matrix instructions' at the clock they leave the chip, the rest LDS traffic
+// (112 KB of rows, 64 KB of weights read, 60 KB written a round) that overlaps
+// them in part.  1.95 PFLOP/s e4m3, 1.07 PFLOP/s bfloat16 at 448 x 128256 x 4096
+// (the library's product: 1.60 and 0.87).
+template <int MODE, int OUT, int MB, int NB, int WM, int WN, int WK, int D>
+__global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs a) {
+  constexpr int IN = MODE == L_BF16 ? T_BF16 : T_E4M3;
+  constexpr int TM = 16 * MB * WM, TN = 16 * NB * WN, NTH = 64 * WM * WN * WK;
+  constexpr int CX = (WK * TM * 8 + NTH - 1) / NTH, CW = (WK * TN * 8 + NTH - 1) / NTH;  // 16-byte chunks a thread stages
+  constexpr int EB = tile_eb(MB, WM), PITCH = TN + 4;
+  extern __shared__ __attribute__((aligned(16))) char smem[];  // [3][WK][TM][128] of x, [2][WK][TN][128] of the weight; then the sums
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wn = w % WN, wm = w / WN % WM, wk = w / (WN * WM);
+  const int l16 = lane & 15, g = lane >> 4;
+  // the row tiles of one panel of columns are consecutive tiles of one XCD
+  const int q = blockIdx.x % LIN_XCD * (gridDim.x / LIN_XCD) + blockIdx.x / LIN_XCD;
+  if (q >= a.mtiles * a.ntiles) return;
+  const int nt0 = q / a.mtiles, m0 = (q - nt0 * a.mtiles) * TM, n0 = nt0 * TN;
+  const int kbytes = a.K * (IN == T_BF16 ? 2 : 1);
+  const int steps = (kbytes + 127) / 128, rounds = (steps + WK - 1) / WK;
+  // buffer loads that end at the last valid row: rows past it read as zeros
+  const auto rx = wave_rsrc(a.x + (size_t)m0 * kbytes, min(TM, a.M - m0) * kbytes);
+  const auto rw = wave_rsrc(a.w + (size_t)n0 * kbytes, min(TN, a.N - n0) * kbytes);
+
+  // byte of chunk c, row r of a staged block: the 16 rows that are read at once
+  // lie in 16 different 16-byte columns of the banks
+  auto at = [](int r, int c) { return r * 128 + 16 * (c ^ ((r >> 1) & 7)); };
+  // Past the end of k both operands read as zeros.  Every load is issued on
+  // every path, so that the waits count exactly.
+  auto load = [&](uint4& v, __amdgpu_buffer_rsrc_t rs, int rows, int i, int round) {
+    const int e = t + i * NTH, row = e >> 3, c = e & 7, r = row % rows;
+    const int k = (round * WK + row / rows) * 128 + 16 * c;
+    v = __builtin_bit_cast(uint4, load16(rs, r * kbytes + k, 0, k < kbytes));
+  };
+  auto store = [&](const uint4& v, char* stage, int rows, int n, int i) {
+    const int e = t + i * NTH, row = e >> 3, c = e & 7;
+    if (n * NTH == WK * rows * 8 || row < WK * rows) *reinterpret_cast<uint4*>(stage + at(row, c)) = v;
+  };
+  char* const ws = smem + 3 * WK * TM * 128;
+  auto read = [&](const char* p, int i) {
+    return frag(*reinterpret_cast<const i32x4*>(p + at(16 * i + l16, g)), *reinterpret_cast<const i32x4*>(p + at(16 * i + l16, 4 + g)));
+  };
+  auto getx = [&](int stage, int i) { return read(smem + (stage * WK + wk) * TM * 128 + wm * MB * 2048, i); };
+  auto getw = [&](int stage, int j) { return read(ws + (stage * WK + wk) * TN * 128 + wn * NB * 2048, j); };
+  f32x4 acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // Round r multiplies its stage while the next one is whole and the one after
+  // is written, so the first fragments of a round are read before the barrier
+  // that ends the one before, and no wave waits at its start.
+  uint4 xr[CX], wr[D][CW];
+  Frag wf[NB];
+  // stages 0 and 1 of both; the registers then hold round 2 (and for the
+  // weight D - 1 rounds more)
+#pragma unroll
+  for (int i = 0; i < CX; ++i) load(xr[i], rx, TM, i, 0);
+#pragma unroll
+  for (int s = 0; s < D; ++s)
+#pragma unroll
+    for (int i = 0; i < CW; ++i) load(wr[s][i], rw, TN, i, s);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int i = 0; i < CX; ++i) {
+      store(xr[i], smem + s * WK * TM * 128, TM, CX, i);
+      load(xr[i], rx, TM, i, s + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < CW; ++i) {
+      store(wr[s % D][i], ws + s * WK * TN * 128, TN, CW, i);
+      load(wr[s % D][i], rw, TN, i, s + D);
+    }
+  }
+  __syncthreads();
+  constexpr int AH = MB > 1 ? 2 : 1;  // fragments of x ahead of the one that is multiplied
+  constexpr int UN = lcm2(2, MB % AH ? AH : 1);
+  static_assert(UN % D == 0, "the rings close together");
+  Frag xf[AH];
+#pragma unroll
+  for (int k = 0; k < NB; ++k) wf[k] = getw(0, k);
+#pragma unroll
+  for (int i = 0; i < AH; ++i) xf[i] = getx(0, i);
+  __syncthreads();  // round 0 writes the weight's stage 0
+  int st = 0;  // the round's stage of x
+  for (int r = 0;;) {
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int st1 = st == 2 ? 0 : st + 1, st2 = st == 0 ? 2 : st - 1;
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const int x = (u * MB + i) % AH;
+        mma16<MODE>(acc[i], xf[x], wf);
+        xf[x] = i + AH < MB ? getx(st, i + AH) : getx(st1, (i + AH) % MB);
+        // spread over the round: the stages of the round after the next, and
+        // the loads that follow them into the registers they leave
+#pragma unroll
+        for (int k = 0; k < CW; ++k)
+          if (k * MB / CW == i) {
+            store(wr[u % D][k], ws + u % 2 * WK * TN * 128, TN, CW, k);
+            load(wr[u % D][k], rw, TN, k, r + 2 + D);
+          }
+#pragma unroll
+        for (int k = 0; k < CX; ++k)
+          if ((2 * k + 1) * MB / (2 * CX) == i) {
+            store(xr[k], smem + st2 * WK * TM * 128, TM, CX, k);
+            load(xr[k], rx, TM, k, r + 3);
+          }
+        if (MB > 4) __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) wf[k] = getw((u + 1) % 2, k);
+      __syncthreads();
+      st = st1;
+      if (++r == rounds) goto done;
+    }
+  }
+done:
+  // Lane l of block (i, j) holds row 16 i + l % 16, columns 16 j + 4 (l / 16)
+  // + 0 .. 3.  Through LDS, EB blocks of rows at a time: there the groups' sums
+  // are added, in order, and the rows are stored whole, a thread having four
+  // columns and every RS-th row.
+  float* tile = reinterpret_cast<float*>(smem);
+  float* sxs = tile + WM * 16 * EB * PITCH;  // the rows' scales
+  constexpr int RS = NTH / (TN / 4);
+  const int ncol = nt0 * TN + t % (TN / 4) * 4;
+  const Cols<IN, OUT> cols(a, min(ncol, a.N - 1));
+  __syncthreads();  // the fragments read ahead
+  if (IN == T_E4M3)
+    for (int i = t; i < min(TM, a.M - m0); i += NTH) sxs[i] = a.sx[m0 + i];
+  float* mine = tile + (wm * 16 * EB + l16) * PITCH + wn * 16 * NB + 4 * g;
+#pragma unroll
+  for (int ib = 0; ib < MB; ib += EB) {
+    const int rows = 16 * min(EB, MB - ib);  // of each of the WM parts
+#pragma unroll
+    for (int k = 0; k < WK; ++k) {
+      if (WK == 1 || wk == k) {
+#pragma unroll
+        for (int i = 0; i < EB; ++i)
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            if (ib + i >= MB) continue;
+            f32x4* p = reinterpret_cast<f32x4*>(mine + 16 * i * PITCH + 16 * j);
+            *p = k == 0 ? acc[ib + i][j] : *p + acc[ib + i][j];
+          }
+      }
+      __syncthreads();
+    }
+    if (ncol < a.N) {
+#pragma unroll 4
+      for (int e = t / (TN / 4); e < WM * rows; e += RS) {
+        const int p = WM == 1 ? 0 : e / rows, r = e - p * rows, m = p * 16 * MB + 16 * ib + r;  // row of the tile
+        if (m0 + m < a.M)
+          cols.put(a, m0 + m, *reinterpret_cast<const f32x4*>(tile + (p * 16 * EB + r) * PITCH + t % (TN / 4) * 4),
+                   IN == T_E4M3 ? sxs[m] : 1.0f);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <int MODE, int OUT, int MB, int NB, int WM, int WN, int WK, int D>
+hipError_t launch_tile(LinArgs a, hipStream_t s) {
+  constexpr int TM = 16 * MB * WM, TN = 16 * NB * WN;
+  constexpr int lds = std::max(3 * WK * TM * 128 + 2 * WK * TN * 128, (16 * WM * tile_eb(MB, WM) * (TN + 4) + TM) * 4);
+  static_assert(lds <= 160 * 1024, "LDS of a compute unit");
+  a.mtiles = (a.M + TM - 1) / TM;
+  a.ntiles = (a.N + TN - 1) / TN;
+  // the limit is raised once per device (twice from racing first calls is harmless)
+  static std::atomic<bool> raised[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return hipErrorInvalidDevice;
+  if (!raised[dev].load(std::memory_order_acquire)) {
+    const hipError_t e = hipFuncSetAttribute((const void*)linear_tile_kernel<MODE, OUT, MB, NB, WM, WN, WK, D>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    raised[dev].store(true, std::memory_order_release);
+  }
+  const unsigned grid = ((unsigned)a.mtiles * (unsigned)a.ntiles + LIN_XCD - 1) / LIN_XCD * LIN_XCD;
+  hipLaunchKernelGGL((linear_tile_kernel<MODE, OUT, MB, NB, WM, WN, WK, D>), dim3(grid), dim3(64 * WM * WN * WK), lds, s, a);
+  return hipGetLastError();
+}
+
+// The tiles to choose from: rows, columns, steps of k a round, workgroups a
+// compute unit holds, and the time of a round in nanoseconds, alone on its
+// compute unit (lat) and among others (thr), fitted to bfloat16 products of 32
+// to 1024 rows.  8-bit operands keep the order.
+struct TileCost {
+  int tm, tn, wk, per_cu;
+  float lat, thr;
+};
+constexpr TileCost kTiles[] = {
+    {32, 32, 4, 2, 530.0f, 450.0f},  {32, 64, 4, 1, 770.0f, 770.0f},    {64, 64, 2, 2, 550.0f, 490.0f},
+    {64, 128, 2, 1, 720.0f, 900.0f}, {128, 128, 1, 2, 600.0f, 590.0f},  {128, 256, 1, 1, 850.0f, 1050.0f},
+    {192, 256, 1, 1, 1150.0f, 1360.0f}, {224, 256, 1, 1, 1300.0f, 1570.0f},
+};
+
+// The tile with the least estimated time: its rounds, times the tiles that
+// follow one another on a compute unit.  Measured against each of them on 29
+// shapes and three type combinations, the choice is the fastest or within 6%
+// of it; 64 x 64 everywhere, for one, takes twice as long at 448 x 128256 x
+// 4096 (856 against 442 us), and 224 x 256 five times as long at 128 x 4096 x
+// 4096 (84 against 17 us).
+int pick_tile(int64_t M, int64_t N, int64_t steps) {
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < (int)(sizeof kTiles / sizeof *kTiles); ++i) {
+    const TileCost& c = kTiles[i];
+    const double tiles = (double)(((M + c.tm - 1) / c.tm) * ((N + c.tn - 1) / c.tn));
+    const double turns = std::max(1.0, std::ceil(tiles / (256.0 / c.per_cu)) / c.per_cu);
+    const double ns = (double)((steps + c.wk - 1) / c.wk) * std::max((double)c.lat, turns * c.thr);
+    if (i == 0 || ns < least) {
+      least = ns;
+      best = i;
+    }
+  }
+  return best;
+}
+
+template <int MODE, int OUT>
+hipError_t launch_linear(LinArgs a, hipStream_t s) {
+  if (a.M <= 16) {
+    // Up to 8192 columns are at most 512 workgroups of 16 columns, whose eight
+    // waves share k (1 x 4096 x 4096 bfloat16: 9.3 us, 13 us with 32 columns and
+    // four waves, 10.6 us with the smallest tile).  Longer weights: 32 columns
+    // for e4m3 (1 x 128256 x 4096: 90 us either way, 7 rows to float32: 93
+    // against 98 us), and tiles for more than 8 rows, which share the rows of x
+    // (16 x 128256 x 2048 bfloat16: 95 against 102 us, 8-bit: 51 against 57).
+    if (a.N <= 8192 || (a.M <= 8 && MODE == L_BF16)) return launch_rows<MODE, OUT, 1, 1, 8, 4>(a, s);
+    if (a.M <= 8) return launch_rows<MODE, OUT, 2, 1, 4, 4>(a, s);
+    return launch_tile<MODE, OUT, 1, 1, 1, 4, 2, 2>(a, s);
+  }
+  const int kbytes = a.K * (MODE == L_BF16 ? 2 : 1);
+  switch (pick_tile(a.M, a.N, (kbytes + 127) / 128)) {
+    case 0: return launch_tile<MODE, OUT, 2, 1, 1, 2, 4, 2>(a, s);
+    case 1: return launch_tile<MODE, OUT, 2, 2, 1, 2, 4, 2>(a, s);
+    case 2: return launch_tile<MODE, OUT, 2, 2, 2, 2, 2, 2>(a, s);
+    case 3: return launch_tile<MODE, OUT, 4, 2, 1, 4, 2, 2>(a, s);
+    case 4: return launch_tile<MODE, OUT, 4, 4, 2, 2, 1, 2>(a, s);
+    case 5: return launch_tile<MODE, OUT, 4, 4, 2, 4, 1, 2>(a, s);
+    case 6: return launch_tile<MODE, OUT, 6, 4, 2, 4, 1, 2>(a, s);
+    default: return launch_tile<MODE, OUT, 7, 4, 2, 4, 1, 1>(a, s);
+  }
 }
 
 }  // namespace
@@ -188,7 +559,7 @@ extern "C" int sv_linear(const void* x, const void* weight, const float* x_scale
   a.act = activation;
   hipStream_t s = (hipStream_t)stream;
   const hipError_t e = dtype == SV_BF16
-                           ? (out_dtype == SV_F32 ? launch_linear<T_BF16, T_F32>(a, s) : launch_linear<T_BF16, T_BF16>(a, s))
-                           : (out_dtype == SV_F32 ? launch_linear<T_E4M3, T_F32>(a, s) : launch_linear<T_E4M3, T_BF16>(a, s));
+                           ? (out_dtype == SV_F32 ? launch_linear<L_BF16, T_F32>(a, s) : launch_linear<L_BF16, T_BF16>(a, s))
+                           : (out_dtype == SV_F32 ? launch_linear<L_F8W, T_F32>(a, s) : launch_linear<L_F8, T_BF16>(a, s));
   return e == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
