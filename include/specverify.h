@@ -92,7 +92,7 @@ typedef enum {
 #define SV_NOALLOC_SCRATCH_BYTES (32 << 20)
 #define SV_MAX_NORM_D 65536         /* widest row of sv_rms_norm              */
 #define SV_MAX_LINEAR_K 65536       /* longest sum of sv_linear               */
-#define SV_MAX_HISTORY (1 << 27)    /* tokens per sequence, sv_adjust_logits  */
+#define SV_MAX_HISTORY (1 << 21)    /* tokens per sequence, sv_adjust_logits  */
 /* sv_init flag: also size the stream's buffer of projection logits for
  * sv_spec_verify_lmhead. */
 #define SV_INIT_LMHEAD 1

@@ -54,7 +54,11 @@ struct AdjArgs {
 
 // Table entry: occurrences in the low bits, and what else is known of the token.
 constexpr uint32_t E_PROMPT = 1u << 31, E_DRAFT = 1u << 30, E_BIAS = 1u << 29, E_BIASES = 1u << 28;
-constexpr uint32_t E_COUNT = E_BIASES - 1;
+constexpr int E_SHIFT = 22;  // six bits: of a drafted token, the first draft that is it
+constexpr uint32_t E_COUNT = (1u << E_SHIFT) - 1;
+static_assert(SV_MAX_HISTORY <= E_COUNT && MAX_K <= 64, "counts and drafts fit an entry");
+constexpr int BIAS_LDS = 1024;  // a sequence's biases held in LDS (at most 16 a thread)
+constexpr uint16_t NONE = 0xFFFFu;
 constexpr int ADJ_MAX_WG = 1024, ADJ_EPT = 8;  // a thread has 8 tokens of the slice
 
 // What a sequence's c occurrences of a token take off its logit.
@@ -149,8 +153,12 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   const int t = threadIdx.x, nt = blockDim.x, S = nt * ADJ_EPT;
   uint32_t* tab = smem;                                           // [S]
   uint32_t* bt = smem + S;                                        // [S] with biases: index of the token's first, then the sum
-  uint16_t* list = reinterpret_cast<uint16_t*>(smem + (a.cub ? 2 : 1) * S);  // [S] in place: tokens of nonzero entries
-  __shared__ int32_t xs[MAX_K];                                   // the sequence's drafts
+  float* bvals = reinterpret_cast<float*>(smem + 2 * S);          // [BIAS_LDS] with biases: their values,
+  uint16_t* btoks = reinterpret_cast<uint16_t*>(bvals + BIAS_LDS);  // [BIAS_LDS] their tokens in the slice
+  uint16_t* bnext = btoks + BIAS_LDS;                             // [BIAS_LDS] and another of the same token
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + (a.cub ? 2 * S + 2 * BIAS_LDS : S));  // [S] in place: tokens of nonzero entries
+  __shared__ int32_t xs[MAX_K];                                   // the sequence's drafts,
+  __shared__ uint64_t same[MAX_K];                                // and which of them are the same token
   __shared__ int32_t nlist;
   const int b = blockIdx.x / a.nslices, sl = blockIdx.x - b * a.nslices;
   const int v0 = sl * S, vn = min(S, a.V - v0);
@@ -266,52 +274,106 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
           for (int k = 0; k < 4; ++k) count(i + 4 * u * nt + k, q[u][k]);
       }
     }
-    for (int i = t; i < nd; i += nt) {
-      xs[i] = a.drafts[d0 + i];
-      const uint32_t j = (uint32_t)xs[i] - (uint32_t)v0;
-      if (j < (uint32_t)vn) touch(j, atomicOr(&tab[j], E_DRAFT));
+    if (t < nd) xs[t] = a.drafts[d0 + t];
+    __syncthreads();
+    if (t < nd) {
+      uint64_t m = 0;
+      for (int k = 0; k < nd; ++k) m |= (uint64_t)(xs[k] == xs[t]) << k;
+      same[t] = m;
+      const uint32_t j = (uint32_t)xs[t] - (uint32_t)v0;
+      if (j < (uint32_t)vn && !(m & ((1ull << t) - 1))) touch(j, atomicOr(&tab[j], E_DRAFT | (uint32_t)t << E_SHIFT));
     }
   }
   if (a.cub) {
     // several biases of one token are added in the order they are listed, by
-    // the thread of the first
-    auto each = [&](auto&& f) {
-      if (i0 + t < i1) f(i0 + t, btok0, (uint32_t)btok0 - (uint32_t)v0);
-      for (int i = i0 + t + nt; i < i1; i += nt) f(i, a.btok[i], (uint32_t)a.btok[i] - (uint32_t)v0);
-    };
-    each([&](int i, int32_t, uint32_t j) {
-      if (j >= (uint32_t)vn) return;
-      atomicMin(&bt[j], (uint32_t)i);
-      touch(j, atomicOr(&tab[j], E_BIAS));
-    });
-    __syncthreads();
-    each([&](int i, int32_t, uint32_t j) {
-      if (j < (uint32_t)vn && bt[j] != (uint32_t)i) atomicOr(&tab[j], E_BIASES);
-    });
-    __syncthreads();
-    each([&](int i, int32_t tok, uint32_t j) {
-      if (j >= (uint32_t)vn) return;
-      float v = i == i0 + t ? bval0 : a.bval[i];
-      if (tab[j] & E_BIASES) {
-        for (int k = i0; k < i; ++k)
-          if (a.btok[k] == tok) return;
-        for (int k = i + 1; k < i1; ++k)
-          if (a.btok[k] == tok) v += a.bval[k];
+    // the thread that holds the first or, of a chain, its head
+    const int nb = i1 - i0;
+    if (nb <= BIAS_LDS) {
+      // each token's biases chained through LDS; the chain's order is any, so
+      // the head takes the lowest index left until none is (or, of a long
+      // chain, looks through all in order)
+      for (int i = t; i < nb; i += nt) {
+        const uint32_t j = (uint32_t)(i == t ? btok0 : a.btok[i0 + i]) - (uint32_t)v0;
+        bvals[i] = i == t ? bval0 : a.bval[i0 + i];
+        btoks[i] = j < (uint32_t)vn ? (uint16_t)j : NONE;
+        if (j < (uint32_t)vn) {
+          bnext[i] = (uint16_t)atomicExch(&bt[j], (uint32_t)i);
+          touch(j, atomicOr(&tab[j], E_BIAS));
+        }
       }
-      bt[j] = __float_as_uint(v);  // its index is not looked at any more
-    });
+      __syncthreads();
+      uint32_t head = 0;
+      for (int i = t, c = 0; i < nb; i += nt, ++c)
+        if (btoks[i] != NONE && bt[btoks[i]] == (uint32_t)i) head |= 1u << c;
+      __syncthreads();  // the sums take the heads' place
+      for (int i = t, c = 0; i < nb; i += nt, ++c) {
+        if (!((head >> c) & 1)) continue;
+        float v = bvals[i];
+        if (bnext[i] != NONE) {
+          int len = 0;
+          for (int k = i; k != NONE; k = bnext[k]) ++len;
+          v = 0.0f;
+          if (len <= 16) {
+            for (int q = 0, last = -1; q < len; ++q) {
+              int low = NONE;
+              for (int k = i; k != NONE; k = bnext[k])
+                if (k > last) low = min(low, k);
+              v = q == 0 ? bvals[low] : v + bvals[low];
+              last = low;
+            }
+          } else {
+            bool any = false;
+            for (int k = 0; k < nb; ++k)
+              if (btoks[k] == btoks[i]) {
+                v = any ? v + bvals[k] : bvals[k];
+                any = true;
+              }
+          }
+        }
+        bt[btoks[i]] = __float_as_uint(v);
+      }
+    } else {
+      for (int i = i0 + t; i < i1; i += nt) {
+        const uint32_t j = (uint32_t)a.btok[i] - (uint32_t)v0;
+        if (j >= (uint32_t)vn) continue;
+        atomicMin(&bt[j], (uint32_t)i);
+        touch(j, atomicOr(&tab[j], E_BIAS));
+      }
+      __syncthreads();
+      for (int i = i0 + t; i < i1; i += nt) {
+        const uint32_t j = (uint32_t)a.btok[i] - (uint32_t)v0;
+        if (j < (uint32_t)vn && bt[j] != (uint32_t)i) atomicOr(&tab[j], E_BIASES);
+      }
+      __syncthreads();
+      for (int i = i0 + t; i < i1; i += nt) {
+        const int32_t tok = a.btok[i];
+        const uint32_t j = (uint32_t)tok - (uint32_t)v0;
+        if (j >= (uint32_t)vn) continue;
+        float v = a.bval[i];
+        if (tab[j] & E_BIASES) {
+          bool first = true;
+          for (int k = i0; k < i && first; ++k) first = a.btok[k] != tok;
+          if (!first) continue;
+          for (int k = i + 1; k < i1; ++k)
+            if (a.btok[k] == tok) v += a.bval[k];
+        }
+        bt[j] = __float_as_uint(v);  // its index is not looked at any more
+      }
+    }
   }
   if (table) __syncthreads();
 
   const float rep = a.rep ? a.rep[b] : 1.0f, freq = a.freq ? a.freq[b] : 0.0f, pres = a.pres ? a.pres[b] : 0.0f;
   const float rinv = 1.0f / rep;
   const bool biased = a.cub != nullptr;
-  // token v of a row that has seen the first nseen drafts: table entry e, bias w
-  auto fix = [&](float l, uint32_t e, uint32_t w, int v, int nseen) {
-    float c = 0.0f;
-    if (e & E_DRAFT)
-      for (int k = 0; k < nseen; ++k) c += xs[k] == v ? 1.0f : 0.0f;
+  // a token's logit in a row that has seen the drafts in `seen`: table entry e, bias w
+  auto fix = [&](float l, uint32_t e, uint32_t w, uint64_t seen) {
+    const float c = e & E_DRAFT ? (float)__popcll(same[(e >> E_SHIFT) & 63] & seen) : 0.0f;
     return adjusted(l, e, __uint_as_float(w), c, rep, rinv, freq, pres);
+  };
+  auto seen_by = [&](int r) {
+    const int k = a.seen + r;
+    return k >= 64 ? ~0ull : (1ull << k) - 1;
   };
 
   if (INPLACE) {
@@ -349,7 +411,7 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
         char* p = out + (size_t)r * pitch;
         const float x = DT == T_F32 ? reinterpret_cast<const float*>(p)[v]
                                     : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[v] << 16);
-        store1<DT>(p, v, fix(x, tab[j], biased ? bt[j] : 0u, v, min(nd, a.seen + r)));
+        store1<DT>(p, v, fix(x, tab[j], biased ? bt[j] : 0u, seen_by(r)));
       }
     }
     return;
@@ -393,12 +455,12 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
             f[k] = x * (x > 0.0f ? rinv : rep) - sub[k];
           }
         } else {
-          const int nseen = min(nd, a.seen + r + u);
+          const uint64_t seen = seen_by(r + u);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint32_t e = tab[8 * t + k];
             f[k] = l[u].get(k);
-            if (e) f[k] = fix(f[k], e, biased ? bt[8 * t + k] : 0u, vt + k, nseen);
+            if (e) f[k] = fix(f[k], e, biased ? bt[8 * t + k] : 0u, seen);
           }
         }
 #pragma unroll
@@ -433,12 +495,12 @@ hipError_t launch_adjust(AdjArgs a, int32_t rows_per_seq, hipStream_t s) {
   while (a.cap <= 16384 && nt == 256 && (int64_t)a.B * slices(nt) < 512) nt = 128;
   a.nslices = slices(nt);
   const int64_t wgs = (int64_t)a.B * a.nslices;
-  const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(512 / wgs, (rows_per_seq + 3) / 4));
+  const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(2048 / wgs, (rows_per_seq + 3) / 4));
   a.rgroup = (rows_per_seq + groups - 1) / groups;
   const dim3 grid((unsigned)wgs, (unsigned)((rows_per_seq + a.rgroup - 1) / a.rgroup));
   const size_t S = (size_t)nt * ADJ_EPT;
   const bool table = a.rep || a.freq || a.pres || a.cub;
-  const size_t lds = table ? S * 4 * (a.cub ? 2 : 1) + (inplace ? S * 2 : 0) : 0;
+  const size_t lds = table ? S * 4 * (a.cub ? 2 : 1) + (a.cub ? BIAS_LDS * 8 : 0) + (inplace ? S * 2 : 0) : 0;
   if (inplace)
     hipLaunchKernelGGL((adjust_kernel<DT, true>), grid, dim3(nt), lds, s, a);
   else

@@ -282,6 +282,15 @@ def test_many_biases_of_one_token_add_up_in_their_order():
             if t == j:
                 s = v if s is None else np.float32(s + v)
         want[j] = 0.0 if s is None else s
+    # and more of them than the kernel holds on chip
+    more = np.concatenate([tok, np.full(1500, 499, dtype=np.int32), tok])
+    mval = np.concatenate([val, np.full(1500, 2.0 ** -3, dtype=np.float32), val])
+    mw = np.zeros(V, dtype=np.float32)
+    for t, v in zip(more, mval):
+        mw[t] = np.float32(mw[t] + v)
+    out = adjust_logits(torch.zeros((1, V), device="cuda"),
+                        bias=(cuda(np.array([0, 2500], dtype=np.int32)), cuda(more), cuda(mval))).cpu().numpy()
+    assert np.array_equal(out[0], mw)
     cu = cuda(np.array([0, 500], dtype=np.int32))
     for _ in range(3):
         out = adjust_logits(torch.zeros((1, V), device="cuda"), bias=(cu, cuda(tok), cuda(val))).cpu().numpy()
