@@ -1,0 +1,261 @@
+"""The operators between a model's last layer and the verification, run
+together as a serving round runs them: the last norm, draft heads and
+projections, the logits' penalties and masks, the sampler and the
+verification; eagerly, on other streams, and captured into graphs that are
+replayed."""
+import numpy as np
+import pytest
+
+import oracle
+from oracle import last_layer as ref
+from tests.harness import log
+
+pytestmark = pytest.mark.gpu
+
+
+def np64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+class Round:
+    """A round's tensors: B sequences, K draft heads, vocabulary V, width d."""
+
+    def __init__(self, B=5, K=3, V=3008, d=256, seed=0):
+        import torch
+
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        rnd = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+        self.B, self.K, self.V, self.d = B, K, V, d
+        self.x = rnd(B, K + 1, d).bfloat16()
+        self.residual = rnd(B, K + 1, d).bfloat16()
+        self.norm_w = (1 + 0.1 * rnd(d)).bfloat16()
+        f = rnd(V, d) * 0.2
+        self.w = f.bfloat16()
+        self.w_scale = f.abs().amax(1) / 448
+        self.w8 = (f / self.w_scale[:, None]).to(torch.float8_e4m3fn)
+        self.head_w = (rnd(K * d, d) * d ** -0.5).bfloat16()
+        self.head_b = (0.1 * rnd(K * d)).bfloat16()
+        self.history = torch.randint(0, V, (B, 200), device="cuda", generator=g, dtype=torch.int32)
+        self.history_len = torch.randint(0, 201, (B,), device="cuda", generator=g, dtype=torch.int32)
+        self.prompt_len = self.history_len // 2
+        self.rep = 1 + 0.5 * torch.rand((B,), device="cuda", generator=g)
+        self.freq = 0.3 * torch.rand((B,), device="cuda", generator=g)
+        self.mask = torch.randint(-2 ** 31, 2 ** 31 - 1, (B * (K + 1), (V + 31) // 32), device="cuda", generator=g,
+                                  dtype=torch.int32)
+        self.draft_u = torch.rand((B, K), device="cuda", generator=g)
+        self.u = torch.rand((B, K + 1), device="cuda", generator=g)
+
+    def penalties(self):
+        return dict(history=self.history, history_len=self.history_len, prompt_len=self.prompt_len,
+                    repetition_penalty=self.rep, frequency_penalty=self.freq)
+
+    def run(self, T=0.8, top_p=0.9, stream=None):
+        """One round; returns every stage's output."""
+        import torch
+
+        import rejection_sampling_verify_09_amd as sv
+
+        B, K, V, d = self.B, self.K, self.V, self.d
+        o = {}
+        # the position before the round: its norm feeds the draft heads, which
+        # predict the K positions after it; each head's rows are penalised for
+        # the drafts before them, so they are drawn one after the other
+        o["h"], _, _ = sv.rms_norm(self.x[:, 0].contiguous(), self.norm_w, residual=self.residual[:, 0].contiguous(),
+                                   stream=stream)
+        o["heads"] = sv.linear(o["h"], self.head_w, bias=self.head_b, residual=o["h"], activation="silu", stream=stream)
+        o["draft_raw"] = sv.lm_logits(o["heads"].view(B, K, d), self.w, stream=stream)
+        x = torch.zeros((B, K), device="cuda", dtype=torch.int32)
+        rows = []
+        for i in range(K):
+            row = sv.adjust_logits(o["draft_raw"][:, i].contiguous(), draft_tokens=x, drafts_seen=i, stream=stream,
+                                   **self.penalties())
+            tok, _ = sv.sample(row, self.draft_u[:, i].contiguous(), T, 0, top_p, stream=stream)
+            x[:, i] = tok
+            rows.append(row)
+        o["draft"] = torch.stack(rows, 1)
+        o["x"] = x
+        # the target's rows, projected in 8 bits, penalised and masked in place
+        o["y8"], o["ys"], o["res"] = sv.rms_norm(self.x, self.norm_w, residual=self.residual,
+                                                 out_dtype=torch.float8_e4m3fn, stream=stream)
+        o["raw"] = sv.linear(o["y8"], self.w8, x_scale=o["ys"], weight_scale=self.w_scale, out_dtype=torch.float32,
+                             stream=stream)
+        o["target"] = sv.adjust_logits(o["raw"], draft_tokens=x, mask=self.mask, stream=stream, **self.penalties())
+        inplace = o["raw"].clone()
+        sv.adjust_logits(inplace, draft_tokens=x, mask=self.mask, out=inplace, stream=stream, **self.penalties())
+        o["inplace"] = inplace
+        o["tokens"], o["n"] = sv.spec_verify(o["target"], o["draft"], x, self.u, T, 0, top_p, stream=stream)
+        return o
+
+
+def adjusted(R, logits, x, first, mask):
+    """float64 rows [B, R, V] and error bounds from the device's own logits."""
+    out = np.empty(logits.shape)
+    tol = np.empty(logits.shape)
+    h, n, p = R.history.cpu().numpy(), R.history_len.cpu().numpy(), R.prompt_len.cpu().numpy()
+    rep, freq = np64(R.rep), np64(R.freq)
+    for b in range(logits.shape[0]):
+        for i in range(logits.shape[1]):
+            allowed = None
+            if mask is not None:
+                w = mask[b * logits.shape[1] + i].astype(np.uint32)
+                allowed = ((w[:, None] >> np.arange(32, dtype=np.uint32)) & 1).reshape(-1)[:logits.shape[2]].astype(bool)
+            out[b, i], m, _ = ref.adjust_row(logits[b, i], h[b, :p[b]], list(h[b, p[b]:n[b]]) + list(x[b, :first + i]),
+                                             rep[b], freq[b], 0.0, (), allowed)
+            tol[b, i] = 2.0 ** -23 * m
+    return out, tol
+
+
+def near(got, want, tol):
+    inf = np.isinf(want)
+    assert np.array_equal(got[inf], want[inf])
+    assert np.all(np.abs(got[~inf] - want[~inf]) <= tol[~inf])
+
+
+def test_a_round_from_the_last_layer_to_the_accepted_tokens():
+    """Every stage against the float64 oracle on that stage's own inputs, and
+    the round's tokens against the oracle's verification."""
+    log("[last layer] one round")
+    R = Round()
+    o = R.run()
+    B, K, V, d = R.B, R.K, R.V, R.d
+    half = 2.0 ** -8
+    want, _ = ref.rms_norm(np64(R.x[:, 0]), np64(R.norm_w), np64(R.residual[:, 0]))
+    assert np.all(np.abs(np64(o["h"]) - want) <= (half + 2.0 ** -17) * np.abs(want))
+    h = np64(o["h"])
+    want = ref.linear(h, np64(R.head_w), np64(R.head_b), h, "silu")
+    # d float32 additions at the activation's slope of at most 1.1, the activation's own 8 ulp, one rounding
+    mag = np.abs(h) @ np.abs(np64(R.head_w)).T + np.abs(np64(R.head_b))
+    tol = 1.1 * (d + 2) * 2.0 ** -24 * mag + 8 * 2.0 ** -23 * np.abs(want) + half * np.abs(want) + 2.0 ** -23 * np.abs(np.tile(h, (1, K)))
+    assert np.all(np.abs(np64(o["heads"]) - want) <= tol)
+    x = o["x"].cpu().numpy()
+    near(np64(o["draft"]), *adjusted(R, np64(o["draft_raw"]), x, 0, None))
+    want, hres = ref.rms_norm(np64(R.x), np64(R.norm_w), np64(R.residual))
+    y = np64(o["y8"]) * np64(o["ys"])[..., None]
+    assert np.all(np.abs(y - want) <= (2.0 ** -4 + 2.0 ** -17) * np.abs(want) + 2.0 ** -9 * np64(o["ys"])[..., None])
+    assert np.all(np.abs(np64(o["res"]) - hres) <= half * np.abs(hres) * (1 + 2.0 ** -20))
+    y8, ys = np64(o["y8"]).reshape(-1, d), np64(o["ys"]).reshape(-1)
+    want = ref.linear(y8, np64(R.w8), x_scale=ys, weight_scale=np64(R.w_scale))
+    bound = (d + 4) * 2.0 ** -24 * (np.abs(y8) @ np.abs(np64(R.w8)).T) * ys[:, None] * np64(R.w_scale)[None, :]
+    assert np.all(np.abs(np64(o["raw"]).reshape(-1, V) - want) <= bound)
+    mask = R.mask.cpu().numpy()
+    near(np64(o["target"]), *adjusted(R, np64(o["raw"]), x, 0, mask))
+    assert np.array_equal(np64(o["target"]), np64(o["inplace"]))
+    u = R.u.cpu().numpy()
+    tg, dr = o["target"].cpu().numpy(), o["draft"].cpu().numpy()
+    tok, n = oracle.verify(tg, dr, x, u, 0.8, 0, 0.9, dtype="f32")[:2]
+    got_t, got_n = o["tokens"].cpu().numpy(), o["n"].cpu().numpy()
+    log(f"   accepted {got_n.tolist()}")
+    for b in range(B):
+        if got_n[b] == n[b] and np.array_equal(got_t[b], tok[b]):
+            continue
+        v, why = oracle.classify(tg[b], dr[b], x[b], u[b], 0.8, 0, 0.9, "f32", got_t[b], got_n[b])
+        assert v in (oracle.MATCH, oracle.FLAGGED), why
+
+
+def _flat(o):
+    import torch
+
+    return {k: v.clone().view(torch.uint8) if v.dtype == torch.float8_e4m3fn else v.clone() for k, v in o.items()}
+
+
+def _same(a, b):
+    import torch
+
+    return all(torch.equal(torch.nan_to_num(a[k].float()), torch.nan_to_num(b[k].float())) for k in a)
+
+
+def test_on_another_stream_and_on_two_at_once():
+    import torch
+
+    log("[last layer] streams")
+    rounds = [Round(seed=1), Round(B=9, K=4, V=5000, d=512, seed=2)]
+    want = [_flat(r.run()) for r in rounds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for rep in range(3):
+        got = []
+        for r, s in zip(rounds, streams):
+            with torch.cuda.stream(s):
+                got.append(r.run())
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert _same(_flat(g), w), rep
+
+
+def test_the_stream_argument():
+    """A call queued on a stream that is not the current one: its output's memory is not handed out again while
+    that stream still works on it."""
+    import torch
+
+    import rejection_sampling_verify_09_amd as sv
+
+    log("[last layer] stream argument")
+    x = torch.randn((2000, 1024), device="cuda").bfloat16()
+    w = torch.randn((1024,), device="cuda").bfloat16()
+    want, _, _ = sv.rms_norm(x, w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for handle in (side, side.cuda_stream):
+        got = sv.rms_norm(x, w, stream=handle)[0]
+        lin = sv.linear(x, x[:64].contiguous(), stream=handle)
+        adj = sv.adjust_logits(x, presence_penalty=torch.zeros(2000, device="cuda"), stream=handle)
+        junk = [torch.full_like(x, 3.0) for _ in range(4)]
+        side.synchronize()
+        assert torch.equal(got, want) and torch.equal(adj, x)
+        assert torch.equal(lin, sv.linear(x, x[:64].contiguous()))
+        del junk
+
+
+def test_captured_rounds_replay():
+    """Two graphs of the operators, replayed in turn with new inputs and eager calls between the replays."""
+    import torch
+
+    import rejection_sampling_verify_09_amd as sv
+
+    log("[last layer] graphs")
+
+    def chain(r):
+        y8, ys, res = sv.rms_norm(r.x, r.norm_w, residual=r.residual, out_dtype=torch.float8_e4m3fn)
+        raw = sv.linear(y8, r.w8, x_scale=ys, weight_scale=r.w_scale, out_dtype=torch.float32)
+        heads = sv.linear(res, r.head_w, bias=r.head_b, residual=res, activation="gelu_tanh")
+        out = sv.adjust_logits(raw, draft_tokens=r.drafts, mask=r.mask, **r.penalties())
+        low = sv.linear(y8, r.w8, x_scale=ys, weight_scale=r.w_scale)
+        sv.adjust_logits(low, draft_tokens=r.drafts, mask=r.mask, out=low, **r.penalties())
+        return dict(y8=y8, ys=ys, res=res, heads=heads, out=out, low=low)
+
+    rounds = [Round(seed=3), Round(B=70, K=5, V=4001, d=192, seed=4), Round(B=1, K=0 + 1, V=9000, d=1024, seed=5)]
+    graphs = []
+    for r in rounds:
+        r.drafts = torch.randint(0, r.V, (r.B, r.K), device="cuda", dtype=torch.int32)
+        chain(r)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = chain(r)
+        graphs.append((g, o))
+    for rep in range(4):
+        for r, (g, o) in zip(rounds, graphs):
+            fresh = Round(r.B, r.K, r.V, r.d, seed=10 + rep)
+            for k in ("x", "residual", "history", "history_len", "prompt_len", "rep", "freq", "mask"):
+                getattr(r, k).copy_(getattr(fresh, k))
+            r.drafts.random_(0, r.V)
+            g.replay()
+        for r, (g, o) in zip(rounds, graphs):
+            want = _flat(chain(r))
+            assert _same(_flat(o), want), rep
+
+
+def test_tensors_off_the_current_device_are_refused(monkeypatch):
+    import torch
+
+    import rejection_sampling_verify_09_amd as sv
+
+    log("[last layer] wrong device")
+    x = torch.zeros((2, 64), device="cuda", dtype=torch.bfloat16)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for f in (lambda: sv.rms_norm(x, x[0]), lambda: sv.linear(x, x), lambda: sv.adjust_logits(x)):
+        with pytest.raises(ValueError, match="current device"):
+            f()
