@@ -516,8 +516,8 @@ int check_and_launch(AdjArgs& a, int64_t rows, int32_t dtype, void* stream) {
       a.mask_rows < 0)
     return SV_ERR_SHAPE;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
-  // the smallest slices have 64 threads for 512 tokens
-  if ((int64_t)a.B * (((int64_t)V + 511) / 512) * 64 > kGridThreads || rows > INT32_MAX) return SV_ERR_SHAPE;
+  // a thread for every 8 tokens, the last of a sequence's workgroups filled up
+  if ((int64_t)a.B * (V / ADJ_EPT + ADJ_MAX_WG) > kGridThreads || rows > INT32_MAX) return SV_ERR_SHAPE;
   const size_t oe = (size_t)type_bytes(dtype);
   if (!is_aligned(a.in, oe) || !is_aligned(a.out, oe) || !is_aligned(a.hist, 4) || !is_aligned(a.hlen, 4) ||
       !is_aligned(a.plen, 4) || !is_aligned(a.drafts, 4) || !is_aligned(a.cu, 4) || !is_aligned(a.rep, 4) ||

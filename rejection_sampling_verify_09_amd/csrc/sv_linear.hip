@@ -296,17 +296,32 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs 
   // byte of chunk c, row r of a staged block: the 16 rows that are read at once
   // lie in 16 different 16-byte columns of the banks
   auto at = [](int r, int c) { return r * 128 + 16 * (c ^ ((r >> 1) & 7)); };
-  // Past the end of k both operands read as zeros.  Every load is issued on
-  // every path, so that the waits count exactly.
-  auto load = [&](uint4& v, __amdgpu_buffer_rsrc_t rs, int rows, int i, int round) {
-    const int e = t + i * NTH, row = e >> 3, c = e & 7, r = row % rows;
-    const int k = (round * WK + row / rows) * 128 + 16 * c;
-    v = __builtin_bit_cast(uint4, load16(rs, r * kbytes + k, 0, k < kbytes));
+  // A thread stages the 16-byte chunk t % 8 of rows t / 8 + 64 i (NTH = 512)
+  // of the round's WK blocks of `rows` rows.  What the i-th adds to the first's
+  // address is the same for all threads.  Past the end of k both operands read
+  // as zeros; every load is issued on every path, so that the waits count
+  // exactly.
+  constexpr int RT = NTH / 8;
+  const int trow = t >> 3, tch = 16 * (t & 7);
+  struct Base {
+    int off, col;
+  };
+  auto base_of = [&](int rows) {
+    const int r = WK == 1 || rows >= RT ? trow : trow % rows, col = (WK == 1 ? 0 : trow / rows) * 128 + tch;
+    return Base{r * kbytes + col, col};
+  };
+  auto load = [&](uint4& v, __amdgpu_buffer_rsrc_t rs, int rows, const Base& b, int i, int round) {
+    const int dr = WK == 1 ? i * RT : rows >= RT ? i * RT % rows : 0;
+    const int db = WK == 1 ? 0 : rows >= RT ? i * RT / rows : i * (RT / rows);
+    const int k0 = round * WK * 128 + db * 128;
+    v = __builtin_bit_cast(uint4, load16(rs, b.off + (dr * kbytes + k0), 0, b.col + k0 < kbytes));
   };
   auto store = [&](const uint4& v, char* stage, int rows, int n, int i) {
-    const int e = t + i * NTH, row = e >> 3, c = e & 7;
-    if (n * NTH == WK * rows * 8 || row < WK * rows) *reinterpret_cast<uint4*>(stage + at(row, c)) = v;
+    if (n * NTH == WK * rows * 8 || trow + i * RT < WK * rows) *reinterpret_cast<uint4*>(stage + at(trow, t & 7) + i * RT * 128) = v;
   };
+  static_assert(RT % 16 == 0 && (WK == 1 || ((TM >= RT ? TM % RT : RT % TM) == 0 && (TN >= RT ? TN % RT : RT % TN) == 0)),
+                "the threads' rows fall alike into every block");
+  const Base bx = base_of(TM), bw = base_of(TN);
   char* const ws = smem + 3 * WK * TM * 128;
   auto read = [&](const char* p, int i) {
     return frag(*reinterpret_cast<const i32x4*>(p + at(16 * i + l16, g)), *reinterpret_cast<const i32x4*>(p + at(16 * i + l16, 4 + g)));
@@ -324,31 +339,29 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs 
   // that ends the one before, and no wave waits at its start.
   uint4 xr[CX], wr[D][CW];
   Frag wf[NB];
-  // stages 0 and 1 of both; the registers then hold round 2 (and for the
-  // weight D - 1 rounds more)
+  // stages 0 and 1 of both; the registers then hold the rounds from 2 on
 #pragma unroll
-  for (int i = 0; i < CX; ++i) load(xr[i], rx, TM, i, 0);
+  for (int i = 0; i < CX; ++i) load(xr[i], rx, TM, bx, i, 0);
 #pragma unroll
   for (int s = 0; s < D; ++s)
 #pragma unroll
-    for (int i = 0; i < CW; ++i) load(wr[s][i], rw, TN, i, s);
+    for (int i = 0; i < CW; ++i) load(wr[s][i], rw, TN, bw, i, s);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
 #pragma unroll
     for (int i = 0; i < CX; ++i) {
       store(xr[i], smem + s * WK * TM * 128, TM, CX, i);
-      load(xr[i], rx, TM, i, s + 1);
+      load(xr[i], rx, TM, bx, i, s + 1);
     }
 #pragma unroll
     for (int i = 0; i < CW; ++i) {
       store(wr[s % D][i], ws + s * WK * TN * 128, TN, CW, i);
-      load(wr[s % D][i], rw, TN, i, s + D);
+      load(wr[s % D][i], rw, TN, bw, i, s + D);
     }
   }
   __syncthreads();
   constexpr int AH = MB > 1 ? 2 : 1;  // fragments of x ahead of the one that is multiplied
-  constexpr int UN = lcm2(2, MB % AH ? AH : 1);
-  static_assert(UN % D == 0, "the rings close together");
+  constexpr int UN = lcm3(2, D, MB % AH ? AH : 1);  // the rings close together
   Frag xf[AH];
 #pragma unroll
   for (int k = 0; k < NB; ++k) wf[k] = getw(0, k);
@@ -370,14 +383,14 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs 
 #pragma unroll
         for (int k = 0; k < CW; ++k)
           if (k * MB / CW == i) {
-            store(wr[u % D][k], ws + u % 2 * WK * TN * 128, TN, CW, k);
-            load(wr[u % D][k], rw, TN, k, r + 2 + D);
+            store(wr[(u + 2) % D][k], ws + u % 2 * WK * TN * 128, TN, CW, k);
+            load(wr[(u + 2) % D][k], rw, TN, bw, k, r + 2 + D);
           }
 #pragma unroll
         for (int k = 0; k < CX; ++k)
           if ((2 * k + 1) * MB / (2 * CX) == i) {
             store(xr[k], smem + st2 * WK * TM * 128, TM, CX, k);
-            load(xr[k], rx, TM, k, r + 3);
+            load(xr[k], rx, TM, bx, k, r + 3);
           }
         if (MB > 4) __builtin_amdgcn_sched_barrier(0);
       }
@@ -490,21 +503,34 @@ int pick_tile(int64_t M, int64_t N, int64_t steps) {
   return best;
 }
 
+// The kernel of a product: an index of kTiles, or one of these for up to 16 rows.
+enum Few : int { ROWS_16 = -1, ROWS_32 = -2, TILE_16 = -3 };  // 16 and 32 columns a workgroup; 16 x 64 tiles
+
+int pick_kernel(int64_t M, int64_t N, int64_t kbytes, bool bf16) {
+  if (M > 16) return pick_tile(M, N, (kbytes + 127) / 128);
+  // Up to 8192 columns are at most 512 workgroups of 16 columns, whose eight
+  // waves share k (1 x 4096 x 4096 bfloat16: 9.3 us, 13 us with 32 columns and
+  // four waves, 10.6 us with the smallest tile).  Longer weights: 32 columns
+  // for e4m3 (1 x 128256 x 4096: 90 us either way, 7 rows to float32: 93
+  // against 98 us), and tiles for more than 8 rows, which share the rows of x
+  // (16 x 128256 x 2048 bfloat16: 95 against 102 us, 8-bit: 51 against 57).
+  if (N <= 8192 || (M <= 8 && bf16)) return ROWS_16;
+  return M <= 8 ? ROWS_32 : TILE_16;
+}
+
+// Threads of the launch, or an upper bound (every workgroup has at most 512).
+int64_t launch_threads(int kernel, int64_t M, int64_t N) {
+  const int64_t tm = kernel >= 0 ? kTiles[kernel].tm : 16;
+  const int64_t tn = kernel >= 0 ? kTiles[kernel].tn : kernel == ROWS_16 ? 16 : kernel == ROWS_32 ? 32 : 64;
+  return (((M + tm - 1) / tm) * ((N + tn - 1) / tn) + LIN_XCD) * 512;
+}
+
 template <int MODE, int OUT>
-hipError_t launch_linear(LinArgs a, hipStream_t s) {
-  if (a.M <= 16) {
-    // Up to 8192 columns are at most 512 workgroups of 16 columns, whose eight
-    // waves share k (1 x 4096 x 4096 bfloat16: 9.3 us, 13 us with 32 columns and
-    // four waves, 10.6 us with the smallest tile).  Longer weights: 32 columns
-    // for e4m3 (1 x 128256 x 4096: 90 us either way, 7 rows to float32: 93
-    // against 98 us), and tiles for more than 8 rows, which share the rows of x
-    // (16 x 128256 x 2048 bfloat16: 95 against 102 us, 8-bit: 51 against 57).
-    if (a.N <= 8192 || (a.M <= 8 && MODE == L_BF16)) return launch_rows<MODE, OUT, 1, 1, 8, 4>(a, s);
-    if (a.M <= 8) return launch_rows<MODE, OUT, 2, 1, 4, 4>(a, s);
-    return launch_tile<MODE, OUT, 1, 1, 1, 4, 2, 2>(a, s);
-  }
-  const int kbytes = a.K * (MODE == L_BF16 ? 2 : 1);
-  switch (pick_tile(a.M, a.N, (kbytes + 127) / 128)) {
+hipError_t launch_linear(const LinArgs& a, int kernel, hipStream_t s) {
+  switch (kernel) {
+    case ROWS_16: return launch_rows<MODE, OUT, 1, 1, 8, 4>(a, s);
+    case ROWS_32: return launch_rows<MODE, OUT, 2, 1, 4, 4>(a, s);
+    case TILE_16: return launch_tile<MODE, OUT, 1, 1, 1, 4, 2, 2>(a, s);
     case 0: return launch_tile<MODE, OUT, 2, 1, 1, 2, 4, 2>(a, s);
     case 1: return launch_tile<MODE, OUT, 2, 2, 1, 2, 4, 2>(a, s);
     case 2: return launch_tile<MODE, OUT, 2, 2, 2, 2, 2, 2>(a, s);
@@ -529,8 +555,9 @@ extern "C" int sv_linear(const void* x, const void* weight, const float* x_scale
   if (out_dtype != SV_F32 && out_dtype != SV_BF16) return SV_ERR_DTYPE;
   if (activation < SV_ACT_NONE || activation > SV_ACT_GELU_TANH) return SV_ERR_PARAM;
   if (residual && (residual_cols < 1 || N % residual_cols != 0)) return SV_ERR_SHAPE;
-  if ((((int64_t)M + 15) / 16) * (((int64_t)N + 15) / 16) * 64 > kGridThreads) return SV_ERR_SHAPE;
   if (M == 0) return SV_OK;
+  const int kernel = pick_kernel(M, N, (int64_t)K * type_bytes(dtype), dtype == SV_BF16);
+  if (launch_threads(kernel, M, N) > kGridThreads) return SV_ERR_SHAPE;
   const bool scaled = dtype == SV_E4M3;
   if (!x || !weight || !out || (scaled && (!x_scale || !weight_scale))) return SV_ERR_NULL;
   const size_t ie = (size_t)type_bytes(dtype), oe = (size_t)type_bytes(out_dtype);
@@ -559,7 +586,7 @@ extern "C" int sv_linear(const void* x, const void* weight, const float* x_scale
   a.act = activation;
   hipStream_t s = (hipStream_t)stream;
   const hipError_t e = dtype == SV_BF16
-                           ? (out_dtype == SV_F32 ? launch_linear<L_BF16, T_F32>(a, s) : launch_linear<L_BF16, T_BF16>(a, s))
-                           : (out_dtype == SV_F32 ? launch_linear<L_F8W, T_F32>(a, s) : launch_linear<L_F8, T_BF16>(a, s));
+                           ? (out_dtype == SV_F32 ? launch_linear<L_BF16, T_F32>(a, kernel, s) : launch_linear<L_BF16, T_BF16>(a, kernel, s))
+                           : (out_dtype == SV_F32 ? launch_linear<L_F8W, T_F32>(a, kernel, s) : launch_linear<L_F8, T_BF16>(a, kernel, s));
   return e == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
