@@ -13,9 +13,8 @@
 // there; for a float32 output the operands are converted to bfloat16 (exactly:
 // 4 significant bits) and multiplied as such, which measures 8e-8.
 //
-// Two kernels: linear_rows_kernel for up to 16 rows, which streams the weight
-// from memory into registers, and linear_tile_kernel, whose tiles launch_linear
-// chooses.  In both the weight is the matrix instruction's first operand, so
+// Two kernels: linear_rows_kernel for up to 16 rows, whose waves share k, and
+// linear_tile_kernel for more, and for many columns; pick_kernel chooses.  In both the weight is the matrix instruction's first operand, so
 // that a lane holds four consecutive columns of the output.
 #include "sv_ops.hpp"
 #include "specverify.h"
@@ -174,37 +173,59 @@ struct Cols {
   }
 };
 
+// Byte of chunk c (16 bytes), row r of a staged block of 128-byte rows: the 16
+// rows that a fragment reads at once lie in 16 different 16-byte columns of
+// the banks.
+__device__ __forceinline__ int at(int r, int c) { return r * 128 + 16 * (c ^ ((r >> 1) & 7)); }
+
+// The fragment of rows 16 i .. 16 i + 15 of a staged block.
+__device__ __forceinline__ Frag read_frag(const char* block, int i) {
+  const int l16 = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  return frag(*reinterpret_cast<const i32x4*>(block + at(16 * i + l16, g)),
+              *reinterpret_cast<const i32x4*>(block + at(16 * i + l16, 4 + g)));
+}
+
+// Orders a wave's own LDS accesses across its lanes.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Few rows: a workgroup owns 16 MT rows and 16 NT columns of the output, its W
 // waves take turns over the 128-byte steps of k, D of them in flight in
-// registers, straight from memory; the waves' sums are added in LDS.  Bound by
-// the weight's bytes: 1 x 4096 x 4096 bfloat16 takes 8.6 us on the device (3.9
-// TB/s, the launch and the first loads' way included), 1 x 128256 x 4096 e4m3
-// 90 us (5.8 TB/s).
+// registers; the waves' sums are added in LDS.  Loads take whole 128-byte
+// lines, eight rows each (a fragment's own layout, 16 rows across neighbouring
+// lanes, keeps the address unit four times as long, 64 against 16 cycles a
+// load), and a wave brings them into fragments through LDS of its own: 16 x
+// 4096 x 4096 bfloat16 9.2 us a call against 10.2 with fragments loaded
+// directly, 16 x 24576 x 4096 41 against 50, 16 x 128256 x 4096 e4m3 98 against
+// 112 (1 row: 92 against 94).  Bound by the weight's bytes, 5.7 to 6.3 TB/s on
+// long ones, the launch on short ones.
 template <int MODE, int OUT, int NT, int MT, int W, int D>
 __global__ void __launch_bounds__(64 * W) linear_rows_kernel(LinArgs a) {
   constexpr int IN = MODE == L_BF16 ? T_BF16 : T_E4M3;
-  extern __shared__ __attribute__((aligned(16))) char smem[];
+  extern __shared__ __attribute__((aligned(16))) char smem[];  // [W][16 (MT + NT)][128], then the sums
   f32x4* part = reinterpret_cast<f32x4*>(smem);  // [W][MT * NT * 64]
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int l16 = lane & 15, g = lane >> 4;
   const int nt0 = blockIdx.x / a.mtiles, mt0 = blockIdx.x - nt0 * a.mtiles;
   const int m0 = mt0 * 16 * MT, n0 = nt0 * 16 * NT;
   const int kbytes = a.K * (IN == T_BF16 ? 2 : 1);
   const int steps = (kbytes + 127) / 128;
-  // buffer loads that end at the last valid row: rows past it read as zeros
+  // buffer loads that end at the last valid row: rows past it read as zeros,
+  // and so does what lies past the end of k, without touching memory (every
+  // load is issued on every path, so that the waits count exactly)
   const auto rx = wave_rsrc(a.x + (size_t)m0 * kbytes, min(16 * MT, a.M - m0) * kbytes);
   const auto rw = wave_rsrc(a.w + (size_t)n0 * kbytes, min(16 * NT, a.N - n0) * kbytes);
-  const int off = l16 * kbytes + 16 * g;
-  Frag xf[D][MT], wf[D][NT];
-  auto load = [&](Frag (&x)[MT], Frag (&wt)[NT], int step) {
+  const int row = lane >> 3, col = 16 * (lane & 7), off = row * kbytes + col;
+  uint4 xr[D][2 * MT], wr[D][2 * NT];
+  auto load = [&](uint4 (&x)[2 * MT], uint4 (&wt)[2 * NT], int step) {
     const int k0 = step * 128;
-    const bool whole = IN == T_BF16 || k0 + 64 < kbytes;  // the last 64 bytes of k may stand alone
+    const bool in = k0 + col < kbytes;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      wt[j] = frag(load16(rw, off + j * 16 * kbytes, k0, true), load16(rw, off + j * 16 * kbytes, k0 + 64, whole));
+    for (int l = 0; l < 2 * NT; ++l) wt[l] = __builtin_bit_cast(uint4, load16(rw, off + (8 * l * kbytes + k0), 0, in));
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
-      x[j] = frag(load16(rx, off + j * 16 * kbytes, k0, true), load16(rx, off + j * 16 * kbytes, k0 + 64, whole));
+    for (int l = 0; l < 2 * MT; ++l) x[l] = __builtin_bit_cast(uint4, load16(rx, off + (8 * l * kbytes + k0), 0, in));
   };
   f32x4 acc[MT][NT];
 #pragma unroll
@@ -212,18 +233,28 @@ __global__ void __launch_bounds__(64 * W) linear_rows_kernel(LinArgs a) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (w + d * W < steps) load(xf[d], wf[d], w + d * W);
-  for (int s = w; s < steps; s += D * W) {
+  for (int d = 0; d < D; ++d) load(xr[d], wr[d], w + d * W);
+  char* const xl = smem + w * (MT + NT) * 2048;
+  char* const wl = xl + MT * 2048;
+  for (int s = w; s < steps;) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      if (s + d * W < steps) {
+      wave_sync();
 #pragma unroll
-        for (int i = 0; i < MT; ++i) mma16<MODE>(acc[i], xf[d][i], wf[d]);
-        if (s + (d + D) * W < steps) load(xf[d], wf[d], s + (d + D) * W);
-      }
+      for (int l = 0; l < 2 * NT; ++l) *reinterpret_cast<uint4*>(wl + at(8 * l + row, lane & 7)) = wr[d][l];
+#pragma unroll
+      for (int l = 0; l < 2 * MT; ++l) *reinterpret_cast<uint4*>(xl + at(8 * l + row, lane & 7)) = xr[d][l];
+      load(xr[d], wr[d], s + D * W);
+      wave_sync();
+      Frag wf[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) wf[j] = read_frag(wl, j);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) mma16<MODE>(acc[i], read_frag(xl, i), wf);
+      s += W;  // past the last step: zeros
     }
   }
+  __syncthreads();  // the sums take the rows' place
   // lane l of block (i, j) holds row 16 i + l % 16, columns 16 j + 4 (l / 16) + 0 .. 3
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -232,12 +263,12 @@ __global__ void __launch_bounds__(64 * W) linear_rows_kernel(LinArgs a) {
   __syncthreads();
   for (int q = t; q < MT * NT * 64; q += 64 * W) {
     // four threads along each 16-column block, its row's blocks next
-    const int c = q & 3, j = (q >> 2) % NT, row = (q >> 2) / NT;
-    const int m = m0 + row, n = n0 + 16 * j + 4 * c;
+    const int c = q & 3, j = (q >> 2) % NT, r = (q >> 2) / NT;
+    const int m = m0 + r, n = n0 + 16 * j + 4 * c;
     if (m >= a.M || n >= a.N) continue;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < W; ++k) v += part[(k * MT * NT + (row >> 4) * NT + j) * 64 + 16 * c + (row & 15)];
+    for (int k = 0; k < W; ++k) v += part[(k * MT * NT + (r >> 4) * NT + j) * 64 + 16 * c + (r & 15)];
     Cols<IN, OUT>(a, n).put(a, m, v, IN == T_E4M3 ? a.sx[m] : 1.0f);
   }
 }
@@ -246,7 +277,7 @@ template <int MODE, int OUT, int NT, int MT, int W, int D>
 hipError_t launch_rows(LinArgs a, hipStream_t s) {
   a.mtiles = (a.M + 16 * MT - 1) / (16 * MT);
   a.ntiles = (a.N + 16 * NT - 1) / (16 * NT);
-  const size_t lds = (size_t)W * MT * NT * 64 * sizeof(f32x4);
+  constexpr size_t lds = std::max(W * (MT + NT) * 2048, W * MT * NT * 1024);
   hipLaunchKernelGGL((linear_rows_kernel<MODE, OUT, NT, MT, W, D>), dim3((unsigned)a.mtiles * (unsigned)a.ntiles),
                      dim3(64 * W), lds, s, a);
   return hipGetLastError();
@@ -271,8 +302,9 @@ constexpr int LIN_XCD = 8;  // XCDs the workgroup ids are dealt over
 // workgroup a compute unit): its rounds take about 1.4 us, 1.0 of them the
 // matrix instructions' at the clock they leave the chip, the rest LDS traffic
 // (112 KB of rows, 64 KB of weights read, 60 KB written a round) that overlaps
-// them in part.  1.95 PFLOP/s e4m3, 1.07 PFLOP/s bfloat16 at 448 x 128256 x 4096
-// (the library's product: 1.60 and 0.87).
+// them in part.  At 448 x 128256 x 4096: e4m3 to bfloat16 244 us (1.93 PFLOP/s),
+// bfloat16 432 (1.09), e4m3 to float32 395 (1.19); the library's products take
+// 295 and 543.
 template <int MODE, int OUT, int MB, int NB, int WM, int WN, int WK, int D>
 __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs a) {
   constexpr int IN = MODE == L_BF16 ? T_BF16 : T_E4M3;
@@ -293,9 +325,6 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs 
   const auto rx = wave_rsrc(a.x + (size_t)m0 * kbytes, min(TM, a.M - m0) * kbytes);
   const auto rw = wave_rsrc(a.w + (size_t)n0 * kbytes, min(TN, a.N - n0) * kbytes);
 
-  // byte of chunk c, row r of a staged block: the 16 rows that are read at once
-  // lie in 16 different 16-byte columns of the banks
-  auto at = [](int r, int c) { return r * 128 + 16 * (c ^ ((r >> 1) & 7)); };
   // A thread stages the 16-byte chunk t % 8 of rows t / 8 + 64 i (NTH = 512)
   // of the round's WK blocks of `rows` rows.  What the i-th adds to the first's
   // address is the same for all threads.  Past the end of k both operands read
@@ -323,11 +352,8 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs 
                 "the threads' rows fall alike into every block");
   const Base bx = base_of(TM), bw = base_of(TN);
   char* const ws = smem + 3 * WK * TM * 128;
-  auto read = [&](const char* p, int i) {
-    return frag(*reinterpret_cast<const i32x4*>(p + at(16 * i + l16, g)), *reinterpret_cast<const i32x4*>(p + at(16 * i + l16, 4 + g)));
-  };
-  auto getx = [&](int stage, int i) { return read(smem + (stage * WK + wk) * TM * 128 + wm * MB * 2048, i); };
-  auto getw = [&](int stage, int j) { return read(ws + (stage * WK + wk) * TN * 128 + wn * NB * 2048, j); };
+  auto getx = [&](int stage, int i) { return read_frag(smem + (stage * WK + wk) * TM * 128 + wm * MB * 2048, i); };
+  auto getw = [&](int stage, int j) { return read_frag(ws + (stage * WK + wk) * TN * 128 + wn * NB * 2048, j); };
   f32x4 acc[MB][NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i)
@@ -506,16 +532,20 @@ int pick_tile(int64_t M, int64_t N, int64_t steps) {
 // The kernel of a product: an index of kTiles, or one of these for up to 16 rows.
 enum Few : int { ROWS_16 = -1, ROWS_32 = -2, TILE_16 = -3 };  // 16 and 32 columns a workgroup; 16 x 64 tiles
 
-int pick_kernel(int64_t M, int64_t N, int64_t kbytes, bool bf16) {
+int pick_kernel(int64_t M, int64_t N, int64_t kbytes) {
   if (M > 16) return pick_tile(M, N, (kbytes + 127) / 128);
-  // Up to 8192 columns are at most 512 workgroups of 16 columns, whose eight
-  // waves share k (1 x 4096 x 4096 bfloat16: 9.3 us, 13 us with 32 columns and
-  // four waves, 10.6 us with the smallest tile).  Longer weights: 32 columns
-  // for e4m3 (1 x 128256 x 4096: 90 us either way, 7 rows to float32: 93
-  // against 98 us), and tiles for more than 8 rows, which share the rows of x
-  // (16 x 128256 x 2048 bfloat16: 95 against 102 us, 8-bit: 51 against 57).
-  if (N <= 8192 || (M <= 8 && bf16)) return ROWS_16;
-  return M <= 8 ? ROWS_32 : TILE_16;
+  // Up to 8192 columns: 16 a workgroup, whose eight waves share k, so that
+  // there are enough of them (16 x 1000 x 16384 bfloat16: 15 us, 23 with 32
+  // columns and four waves; 16 x 8192 x 16384: 57 against 63).  Then 32 columns
+  // where rows are short, since each wave has only a few steps of one (k of
+  // 4096 bytes, 16 x 128256 e4m3: 98 against 113 us; of 2048, 16 x 24576: 10.6
+  // against 12.0), 16 where they are longer (8192 bytes, 1 x 24576: 26 against
+  // 35 us), and tiles where many columns meet more than 8 rows, whose x they
+  // share (16 x 128256 x 4096 bfloat16: 178 against 203 us, 24576 columns: 42
+  // against 41, 8 rows: 174 against 178, 1 row: 169 against 166).
+  if (N <= 8192) return ROWS_16;
+  if (kbytes <= 4096) return ROWS_32;
+  return M <= 8 || N <= 24576 ? ROWS_16 : TILE_16;
 }
 
 // Threads of the launch, or an upper bound (every workgroup has at most 512).
@@ -528,8 +558,8 @@ int64_t launch_threads(int kernel, int64_t M, int64_t N) {
 template <int MODE, int OUT>
 hipError_t launch_linear(const LinArgs& a, int kernel, hipStream_t s) {
   switch (kernel) {
-    case ROWS_16: return launch_rows<MODE, OUT, 1, 1, 8, 4>(a, s);
-    case ROWS_32: return launch_rows<MODE, OUT, 2, 1, 4, 4>(a, s);
+    case ROWS_16: return launch_rows<MODE, OUT, 1, 1, 8, 2>(a, s);
+    case ROWS_32: return launch_rows<MODE, OUT, 2, 1, 4, 2>(a, s);
     case TILE_16: return launch_tile<MODE, OUT, 1, 1, 1, 4, 2, 2>(a, s);
     case 0: return launch_tile<MODE, OUT, 2, 1, 1, 2, 4, 2>(a, s);
     case 1: return launch_tile<MODE, OUT, 2, 2, 1, 2, 4, 2>(a, s);
@@ -556,7 +586,7 @@ extern "C" int sv_linear(const void* x, const void* weight, const float* x_scale
   if (activation < SV_ACT_NONE || activation > SV_ACT_GELU_TANH) return SV_ERR_PARAM;
   if (residual && (residual_cols < 1 || N % residual_cols != 0)) return SV_ERR_SHAPE;
   if (M == 0) return SV_OK;
-  const int kernel = pick_kernel(M, N, (int64_t)K * type_bytes(dtype), dtype == SV_BF16);
+  const int kernel = pick_kernel(M, N, (int64_t)K * type_bytes(dtype));
   if (launch_threads(kernel, M, N) > kGridThreads) return SV_ERR_SHAPE;
   const bool scaled = dtype == SV_E4M3;
   if (!x || !weight || !out || (scaled && (!x_scale || !weight_scale))) return SV_ERR_NULL;
