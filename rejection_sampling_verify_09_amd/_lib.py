@@ -420,13 +420,16 @@ def spec_verify_lmhead(hidden_target: torch.Tensor, weight_target: torch.Tensor,
     return out_tokens, out_n
 
 
-_CODES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float8_e4m3fn: SV_E4M3}
+_FLOATS = {torch.float32: SV_F32, torch.bfloat16: SV_BF16}
+_OPERANDS = {torch.bfloat16: SV_BF16, torch.float8_e4m3fn: SV_E4M3}
+_CODES = {**_FLOATS, **_OPERANDS}
 
 
 def _code(dtype: torch.dtype, name: str, allowed) -> int:
-    if dtype not in allowed:
+    code = allowed.get(dtype)
+    if code is None:
         raise TypeError(f"{name} must be one of {', '.join(str(t) for t in allowed)}, got {dtype}")
-    return _CODES[dtype]
+    return code
 
 
 def _arg(t: torch.Tensor | None, name: str, dtype, shape, dev: int):
@@ -453,11 +456,13 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     return t
 
 
-def _on_current_device(dev: int, name: str) -> None:
+def _stream_on(dev: int, name: str, stream) -> int:
+    """The stream's handle for work on ``dev``, which must be the current device."""
     if dev < 0:
         raise ValueError(f"{name} must be a device tensor")
     if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -472,9 +477,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     Returns (out, out_scale [...] or None, h rounded to x's type or None
     without a residual).  out and out_residual may be x or residual (in
     place)."""
-    code = _code(x.dtype, "x", (torch.float32, torch.bfloat16))
+    code = _code(x.dtype, "x", _FLOATS)
     out_dtype = x.dtype if out_dtype is None else out_dtype
-    ocode = _code(out_dtype, "out_dtype", (torch.float32, torch.bfloat16, torch.float8_e4m3fn))
+    ocode = _code(out_dtype, "out_dtype", _CODES)
     if x.dim() < 1 or weight.dim() != 1 or x.shape[-1] != weight.shape[0] or weight.shape[0] < 1:
         raise ValueError("x must be [..., d] and weight [d]")
     d = weight.shape[0]
@@ -490,7 +495,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     sp = _arg(out_scale, "out_scale", torch.float32, x.shape[:-1], dev)
     hp = _arg(out_residual, "out_residual", x.dtype, x.shape, dev)
     xp = _arg(x, "x", x.dtype, x.shape, dev)
-    _on_current_device(dev, "x")
+    s = _stream_on(dev, "x", stream)
     if out is None:
         out = _new(x.shape, out_dtype, x, stream)
         op = out.data_ptr()
@@ -500,7 +505,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     if residual is not None and out_residual is None:
         out_residual = _new(x.shape, x.dtype, x, stream)
         hp = out_residual.data_ptr()
-    st = lib().sv_rms_norm(xp, rp, wp, float(eps), op, sp, hp, rows, d, code, ocode, _stream(stream))
+    st = lib().sv_rms_norm(xp, rp, wp, float(eps), op, sp, hp, rows, d, code, ocode, s)
     if st != SV_OK:
         raise SpecVerifyError(st, "sv_rms_norm")
     return out, out_scale, out_residual
@@ -518,8 +523,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     adds residual column n mod R (several draft heads stacked along N share
     one residual).  activation: "none", "relu", "silu", "gelu" or "gelu_tanh".
     Returns out [..., N]."""
-    code = _code(x.dtype, "x", (torch.bfloat16, torch.float8_e4m3fn))
-    ocode = _code(out_dtype, "out_dtype", (torch.float32, torch.bfloat16))
+    code = _code(x.dtype, "x", _OPERANDS)
+    ocode = _code(out_dtype, "out_dtype", _FLOATS)
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
     if x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[1] or weight.shape[1] < 1:
@@ -542,12 +547,11 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     rp = _arg(residual, "residual", out_dtype, lead + (R,), dev)
     op = _arg(out, "out", out_dtype, lead + (N,), dev)
     xp = _arg(x, "x", x.dtype, x.shape, dev)
-    _on_current_device(dev, "x")
+    s = _stream_on(dev, "x", stream)
     if out is None:
         out = _new(lead + (N,), out_dtype, x, stream)
         op = out.data_ptr()
-    st = lib().sv_linear(xp, wp, xsp, wsp, bp, rp, op, M, N, K, R, ACTIVATIONS[activation], code, ocode,
-                         _stream(stream))
+    st = lib().sv_linear(xp, wp, xsp, wsp, bp, rp, op, M, N, K, R, ACTIVATIONS[activation], code, ocode, s)
     if st != SV_OK:
         raise SpecVerifyError(st, "sv_linear")
     return out
@@ -576,7 +580,7 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
     [mask_rows, ceil(V / 32)] int32, bit j % 32 of word j / 32 set where token j
     is allowed; mask_index [rows] int32, each row's row of mask (outside of it:
     not masked).  Returns out; out=logits adjusts in place."""
-    code = _code(logits.dtype, "logits", (torch.float32, torch.bfloat16))
+    code = _code(logits.dtype, "logits", _FLOATS)
     i32, f32 = torch.int32, torch.float32
     if logits.dim() not in (2, 3):
         raise ValueError("logits must be [B, R, V] or [rows, V]")
@@ -636,11 +640,10 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
     mi = _arg(mask_index, "mask_index", i32, (rows,), dev)
     op = _arg(out, "out", logits.dtype, logits.shape, dev)
     lp = _arg(logits, "logits", logits.dtype, logits.shape, dev)
-    _on_current_device(dev, "logits")
+    s = _stream_on(dev, "logits", stream)
     if out is None:
         out = _new(logits.shape, logits.dtype, logits, stream)
         op = out.data_ptr()
-    s = _stream(stream)
     if cu_num_draft is not None:
         st = lib().sv_adjust_logits_ragged(lp, op, hp, hl, pl, xp, cp, rp, fp, pp, cb, bt, bv, mp, mi, B, N, int(max_k),
                                            bonus, cap, nb, mrows, V, code, s)
