@@ -497,7 +497,7 @@ int sv_linear(const void* x, const void* weight, const float* x_scale, const flo
  * once.  Logits that none of these touches keep their
  * bits.  Row i of a sequence has s = drafts_seen + i.
  *
- * logits       [B, R, V] dtype (SV_F32 or SV_BF16), device
+ * logits       [B, R, V] dtype (SV_F32 or SV_BF16), device; at most 2^30 rows
  * out_logits   the same shape and type, device; may be logits itself (in
  *              place: only the logits that change are written)
  * history      [B, history_cap] int32, device: the prompt, then the tokens

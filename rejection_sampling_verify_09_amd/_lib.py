@@ -447,6 +447,12 @@ def _arg(t: torch.Tensor | None, name: str, dtype, shape, dev: int):
     return t.data_ptr()
 
 
+def _int32(*sizes: int) -> None:
+    """The C ABI's sizes are 32-bit, and ctypes cuts larger ones off without a word."""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < 0:
+        raise ValueError(f"sizes must be nonnegative and fit 32 bits, got {', '.join(map(str, sizes))}")
+
+
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """An output tensor, its memory kept until the work on ``stream`` is done."""
     # empty_like takes half of torch.empty's time on the host
@@ -484,6 +490,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
         raise ValueError("x must be [..., d] and weight [d]")
     d = weight.shape[0]
     rows = x.numel() // d
+    _int32(rows, d)
     dev = x.get_device()
     wp = _arg(weight, "weight", x.dtype, (d,), dev)
     rp = _arg(residual, "residual", x.dtype, x.shape, dev)
@@ -531,6 +538,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
         raise ValueError("x must be [..., K] and weight [N, K]")
     N, K = weight.shape
     M = x.numel() // K
+    _int32(M, N, K)
     lead = x.shape[:-1]
     dev = x.get_device()
     if (code == SV_E4M3) != (x_scale is not None) or (code == SV_E4M3) != (weight_scale is not None):
@@ -598,8 +606,6 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
         if rows not in (N, N + B):
             raise ValueError("logits must be [N + B, V] (target rows) or [N, V] (draft rows) for N draft_tokens")
         bonus = 1 if rows == N + B else 0
-        xp = _arg(draft_tokens, "draft_tokens", i32, (N,), dev)
-        cp = _arg(cu_num_draft, "cu_num_draft", i32, (B + 1,), dev)
     else:
         B = logits.shape[0]
         R = logits.shape[1] if logits.dim() == 3 else 1
@@ -607,7 +613,6 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
             if draft_tokens.dim() != 2:
                 raise ValueError("draft_tokens must be [B, K]")
             K = draft_tokens.shape[1]
-        xp = _arg(draft_tokens, "draft_tokens", i32, (B, K), dev)
     cap = 0
     if history is not None:
         if history.dim() != 2:
@@ -615,6 +620,22 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
         cap = history.shape[1]
     elif history_len is not None or prompt_len is not None:
         raise ValueError("history_len and prompt_len go with a history")
+    nb = 0 if bias is None else bias[1].numel()
+    mrows = 0
+    if mask is not None:
+        if mask.dim() != 2:
+            raise ValueError("mask must be [mask_rows, ceil(V / 32)]")
+        mrows = mask.shape[0]
+        if mask_index is None and mrows != rows:
+            raise ValueError("mask must have a row for each row of logits, unless mask_index says which")
+    elif mask_index is not None:
+        raise ValueError("mask_index goes with a mask")
+    _int32(rows, V, B, K, N, cap, nb, mrows, drafts_seen, max_k or 0)
+    if cu_num_draft is not None:
+        xp = _arg(draft_tokens, "draft_tokens", i32, (N,), dev)
+        cp = _arg(cu_num_draft, "cu_num_draft", i32, (B + 1,), dev)
+    else:
+        xp = _arg(draft_tokens, "draft_tokens", i32, (B, K), dev)
     hp = _arg(history, "history", i32, (B, cap), dev)
     hl = _arg(history_len, "history_len", i32, (B,), dev)
     pl = _arg(prompt_len, "prompt_len", i32, (B,), dev)
@@ -622,20 +643,11 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
     fp = _arg(frequency_penalty, "frequency_penalty", f32, (B,), dev)
     pp = _arg(presence_penalty, "presence_penalty", f32, (B,), dev)
     cb = bt = bv = None
-    nb = 0
     if bias is not None:
         cu_bias, btok, bval = bias
-        nb = btok.numel()
         cb = _arg(cu_bias, "cu_bias", i32, (B + 1,), dev)
         bt = _arg(btok, "bias tokens", i32, (nb,), dev)
         bv = _arg(bval, "bias values", f32, (nb,), dev)
-    mrows = 0
-    if mask is not None:
-        mrows = mask.shape[0] if mask.dim() == 2 else -1
-        if mask_index is None and mrows != rows:
-            raise ValueError("mask must have a row for each row of logits, unless mask_index says which")
-    elif mask_index is not None:
-        raise ValueError("mask_index goes with a mask")
     mp = _arg(mask, "mask", i32, (mrows, (V + 31) // 32), dev)
     mi = _arg(mask_index, "mask_index", i32, (rows,), dev)
     op = _arg(out, "out", logits.dtype, logits.shape, dev)

@@ -508,6 +508,8 @@ hipError_t launch_adjust(AdjArgs a, int32_t rows_per_seq, hipStream_t s) {
   return hipGetLastError();
 }
 
+constexpr int64_t kMaxRows = int64_t(1) << 30;  // row numbers a few rows past the last are formed in 32 bits
+
 size_t words_of(int32_t V) { return ((size_t)V + 31) / 32; }
 
 int check_and_launch(AdjArgs& a, int64_t rows, int32_t dtype, void* stream) {
@@ -517,7 +519,7 @@ int check_and_launch(AdjArgs& a, int64_t rows, int32_t dtype, void* stream) {
     return SV_ERR_SHAPE;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
   // a thread for every 8 tokens, the last of a sequence's workgroups filled up
-  if ((int64_t)a.B * (V / ADJ_EPT + ADJ_MAX_WG) > kGridThreads || rows > INT32_MAX) return SV_ERR_SHAPE;
+  if ((int64_t)a.B * (V / ADJ_EPT + ADJ_MAX_WG) > kGridThreads || rows > kMaxRows) return SV_ERR_SHAPE;
   const size_t oe = (size_t)type_bytes(dtype);
   if (!is_aligned(a.in, oe) || !is_aligned(a.out, oe) || !is_aligned(a.hist, 4) || !is_aligned(a.hlen, 4) ||
       !is_aligned(a.plen, 4) || !is_aligned(a.drafts, 4) || !is_aligned(a.cu, 4) || !is_aligned(a.rep, 4) ||

@@ -315,3 +315,19 @@ def test_offsets_past_32_bits():
         v = o.view(-1, V)
         assert (v[:, -1] == -1).all() and (v[:, 0] == -float("inf")).all()
         assert int(torch.count_nonzero(v[-1])) == 2 and int(torch.count_nonzero(v[0])) == 2
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("nbias", [60, 3000])
+def test_the_widest_slices(nbias, dtype):
+    """Long histories take the widest slices: with biases, and in place, the
+    tables fill more than 64 KB of LDS."""
+    import torch
+
+    log(f"[adjust] widest slices {nbias} {dtype}")
+    c = make(40 + nbias, B=2, R=3, K=2, V=20003, cap=20000, dtype=dtype, nbias=nbias, mask="index")
+    got = call(c)
+    check(c, got)
+    mine = c["logits"].clone()
+    call(c, out=mine, logits=mine)
+    assert torch.equal(mine.view(_bits(c)), got.view(_bits(c)))

@@ -259,3 +259,52 @@ def test_tensors_off_the_current_device_are_refused(monkeypatch):
     for f in (lambda: sv.rms_norm(x, x[0]), lambda: sv.linear(x, x), lambda: sv.adjust_logits(x)):
         with pytest.raises(ValueError, match="current device"):
             f()
+
+
+FIRST_CALL = """
+import torch
+import rejection_sampling_verify_09_amd as sv
+gen = torch.Generator(device="cuda").manual_seed(1)
+x = torch.randn((300, 128), device="cuda", generator=gen).bfloat16()
+w = torch.randn((70000, 128), device="cuda", generator=gen).bfloat16()
+few = x[:2].contiguous()
+norm_w = torch.ones(128, device="cuda").bfloat16()
+hist = torch.arange(40000, device="cuda", dtype=torch.int32).view(2, 20000) % 70000
+pen = torch.tensor([1.5, 0.5], device="cuda")
+bias = (torch.tensor([0, 1, 2], device="cuda", dtype=torch.int32), torch.tensor([5, 6], device="cuda", dtype=torch.int32), pen)
+
+
+def chain():
+    y = sv.rms_norm(x, norm_w)[0]
+    big = sv.linear(y, w)
+    logits = sv.linear(few, w)
+    sv.adjust_logits(logits, history=hist, repetition_penalty=pen, bias=bias, out=logits)
+    return big, logits
+
+
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = chain()
+for rep in range(3):
+    x.mul_(0.5)
+    few.mul_(0.5)
+    g.replay()
+    want = chain()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16)), rep
+print("first calls captured", flush=True)
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    """Nothing is set up lazily in a way that a capture forbids."""
+    import os
+    import subprocess
+    import sys
+
+    log("[last layer] first call captured")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "first calls captured" in r.stdout, r.stderr[-2000:]

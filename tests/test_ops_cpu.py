@@ -192,3 +192,36 @@ def test_oracle_adjust_pins():
                                      allowed=np.array([True, True, True, True, False]))
     assert row[:4].tolist() == [1.0, -4.0, 0.0, 4.0] and row[4] == -np.inf
     assert touched.tolist() == [True, True, True, True, False]
+
+
+def test_sizes_past_32_bits_are_refused_not_cut_off():
+    """The C ABI counts in 32 bits; ctypes would pass 2^32 + 3 on as 3."""
+    big, b, i32 = (1 << 32) + 3, torch.bfloat16, torch.int32
+    x = torch.zeros((1, 64), dtype=b).expand(big, 64)
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.rms_norm(x, x[0])
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.linear(x, torch.zeros((10, 64), dtype=b))
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.linear(torch.zeros((2, 64), dtype=b), x)
+    wide = torch.zeros((1, 1)).expand(2, big)
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.rms_norm(wide, wide[0])
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.adjust_logits(wide)
+    lg, many = torch.zeros((2, 3, 100)), torch.zeros((1,), dtype=i32).expand(big)
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.adjust_logits(lg[:, 0], draft_tokens=torch.zeros((2, 1), dtype=i32), drafts_seen=1 << 32)
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.adjust_logits(lg, history=many.expand(2, big), presence_penalty=torch.zeros(2))
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.adjust_logits(lg, bias=(torch.zeros(3, dtype=i32), many, many.float()))
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.adjust_logits(lg, mask=many[:, None].expand(big, 4), mask_index=torch.zeros(6, dtype=i32))
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.adjust_logits(lg[:, 0], cu_num_draft=torch.zeros(3, dtype=i32), max_k=1 << 32)
+
+
+def test_rows_that_the_grid_cannot_count_are_refused():
+    assert adj(B=1, R=(1 << 31) - 1, K=0, V=1, midx=P(20), dt=L.SV_BF16) == L.SV_ERR_SHAPE
+    assert adj(B=1, R=(1 << 30) + 1, K=0, V=1, midx=P(20), dt=L.SV_BF16) == L.SV_ERR_SHAPE
