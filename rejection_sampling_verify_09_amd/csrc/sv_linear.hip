@@ -43,6 +43,7 @@ struct LinArgs {
   int32_t M, N, K, R;
   int32_t act;
   int32_t mtiles, ntiles;
+  int32_t turn;  // workgroups begin at different parts of k
 };
 
 __device__ __forceinline__ float activate(float v, int act) {
@@ -192,6 +193,21 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// The workgroups begin their rounds over k at different ones, each group of
+// about 256 columns at its own: where they all begin at 0, they ask for the
+// same bytes of every row at once, and rows a power of two apart keep only some
+// of the memory's channels busy (64 x 24576 x 4096 bfloat16 with 64 x 128 tiles:
+// 47.7 us from 0, 40.6 so; 16 x 32000 x 4096 e4m3: 28.1 and 24.2; rows of 4224
+// bytes: alike).  Where x is larger than an XCD's L2, all begin at 0, so that
+// the column panels read the same part of x (4096 x 16384 x 4096 e4m3: 264 us,
+// 275 otherwise).
+__device__ __forceinline__ int first_round(const LinArgs& a, int n0, int rounds) {
+  return a.turn ? (n0 >> 8) % rounds : 0;
+}
+__device__ __forceinline__ int turned(int round, int first, int rounds) {
+  return round + first - (round + first >= rounds ? rounds : 0);
+}
+
 // Few rows: a workgroup owns 16 MT rows and 16 NT columns of the output, its W
 // waves take turns over the 128-byte steps of k, D of them in flight in
 // registers; the waves' sums are added in LDS.  Loads take whole 128-byte
@@ -211,7 +227,7 @@ __global__ void __launch_bounds__(64 * W) linear_rows_kernel(LinArgs a) {
   const int nt0 = blockIdx.x / a.mtiles, mt0 = blockIdx.x - nt0 * a.mtiles;
   const int m0 = mt0 * 16 * MT, n0 = nt0 * 16 * NT;
   const int kbytes = a.K * (IN == T_BF16 ? 2 : 1);
-  const int steps = (kbytes + 127) / 128;
+  const int steps = (kbytes + 127) / 128, first = first_round(a, n0, steps);
   // buffer loads that end at the last valid row: rows past it read as zeros,
   // and so does what lies past the end of k, without touching memory (every
   // load is issued on every path, so that the waits count exactly)
@@ -220,7 +236,7 @@ __global__ void __launch_bounds__(64 * W) linear_rows_kernel(LinArgs a) {
   const int row = lane >> 3, col = 16 * (lane & 7), off = row * kbytes + col;
   uint4 xr[D][2 * MT], wr[D][2 * NT];
   auto load = [&](uint4 (&x)[2 * MT], uint4 (&wt)[2 * NT], int step) {
-    const int k0 = step * 128;
+    const int k0 = step < steps ? turned(step, first, steps) * 128 : kbytes;
     const bool in = k0 + col < kbytes;
 #pragma unroll
     for (int l = 0; l < 2 * NT; ++l) wt[l] = __builtin_bit_cast(uint4, load16(rw, off + (8 * l * kbytes + k0), 0, in));
@@ -321,6 +337,7 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs 
   const int nt0 = q / a.mtiles, m0 = (q - nt0 * a.mtiles) * TM, n0 = nt0 * TN;
   const int kbytes = a.K * (IN == T_BF16 ? 2 : 1);
   const int steps = (kbytes + 127) / 128, rounds = (steps + WK - 1) / WK;
+  const int first = first_round(a, n0, rounds);
   // buffer loads that end at the last valid row: rows past it read as zeros
   const auto rx = wave_rsrc(a.x + (size_t)m0 * kbytes, min(TM, a.M - m0) * kbytes);
   const auto rw = wave_rsrc(a.w + (size_t)n0 * kbytes, min(TN, a.N - n0) * kbytes);
@@ -342,7 +359,7 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs 
   auto load = [&](uint4& v, __amdgpu_buffer_rsrc_t rs, int rows, const Base& b, int i, int round) {
     const int dr = WK == 1 ? i * RT : rows >= RT ? i * RT % rows : 0;
     const int db = WK == 1 ? 0 : rows >= RT ? i * RT / rows : i * (RT / rows);
-    const int k0 = round * WK * 128 + db * 128;
+    const int k0 = (round < rounds ? turned(round, first, rounds) * WK * 128 : kbytes) + db * 128;
     v = __builtin_bit_cast(uint4, load16(rs, b.off + (dr * kbytes + k0), 0, b.col + k0 < kbytes));
   };
   auto store = [&](const uint4& v, char* stage, int rows, int n, int i) {
@@ -507,21 +524,27 @@ constexpr TileCost kTiles[] = {
     {192, 256, 1, 1, 1150.0f, 1360.0f}, {224, 256, 1, 1, 1300.0f, 1570.0f},
 };
 
-// The tile with the least estimated time: its rounds, times the tiles that
-// follow one another on a compute unit.  Measured against each of them on 29
-// shapes and three type combinations, the choice is the fastest or within 6%
-// of it; 64 x 64 everywhere, for one, takes twice as long at 448 x 128256 x
-// 4096 (856 against 442 us), and 224 x 256 five times as long at 128 x 4096 x
-// 4096 (84 against 17 us).
+// The tile with the least estimated time: that of the compute unit with the
+// most tiles, per_cu of them at a time, their rounds and 2.5 us around each
+// such turn.  Tiles of 32 rows are for products whose tiles all run at once:
+// in turns they reach less of the memory's bandwidth (32 x 24576 x 4096: 45 us,
+// 38 with 64 x 128).  Measured against each of them on 34 shapes and three type
+// combinations, the choice is 0.6% slower than the fastest in the mean, 15% at
+// most; 64 x 64 everywhere, for one, takes twice as long at 448 x 128256 x 2048
+// (483 against 255 us), and 224 x 256 five times as long at 128 x 4096 x 4096
+// (83 against 17 us).
 int pick_tile(int64_t M, int64_t N, int64_t steps) {
-  int best = 0;
+  int best = -1;
   double least = 0.0;
   for (int i = 0; i < (int)(sizeof kTiles / sizeof *kTiles); ++i) {
     const TileCost& c = kTiles[i];
-    const double tiles = (double)(((M + c.tm - 1) / c.tm) * ((N + c.tn - 1) / c.tn));
-    const double turns = std::max(1.0, std::ceil(tiles / (256.0 / c.per_cu)) / c.per_cu);
-    const double ns = (double)((steps + c.wk - 1) / c.wk) * std::max((double)c.lat, turns * c.thr);
-    if (i == 0 || ns < least) {
+    const int64_t tiles = ((M + c.tm - 1) / c.tm) * ((N + c.tn - 1) / c.tn);
+    if (c.tm == 32 && tiles > 256 * c.per_cu) continue;
+    const double rounds = (double)((steps + c.wk - 1) / c.wk);
+    const int64_t most = (tiles + 255) / 256, turns = most / c.per_cu, left = most % c.per_cu;
+    double ns = turns * (rounds * std::max(c.lat, c.per_cu * c.thr) + 2500.0);
+    if (left) ns += rounds * std::max(c.lat, left * c.thr) + 2500.0;
+    if (best < 0 || ns < least) {
       least = ns;
       best = i;
     }
@@ -614,6 +637,7 @@ extern "C" int sv_linear(const void* x, const void* weight, const float* x_scale
   a.K = K;
   a.R = residual ? residual_cols : 1;
   a.act = activation;
+  a.turn = (int64_t)M * K * (int64_t)ie <= (int64_t)4 << 20;
   hipStream_t s = (hipStream_t)stream;
   const hipError_t e = dtype == SV_BF16
                            ? (out_dtype == SV_F32 ? launch_linear<L_BF16, T_F32>(a, kernel, s) : launch_linear<L_BF16, T_BF16>(a, kernel, s))
