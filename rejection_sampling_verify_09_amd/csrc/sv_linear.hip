@@ -29,6 +29,7 @@ namespace {
 
 typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 bf16x8;
 typedef __attribute__((__vector_size__(8 * sizeof(int)))) int i32x8;
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
 
 enum Act : int { A_NONE = 0, A_RELU = 1, A_SILU = 2, A_GELU = 3, A_GELU_TANH = 4 };
 
@@ -46,14 +47,28 @@ struct LinArgs {
   int32_t turn;  // workgroups begin at different parts of k
 };
 
-__device__ __forceinline__ float activate(float v, int act) {
+// Of four values at a time, so that their chains of instructions overlap.
+__device__ __forceinline__ void activate(f32x4& v, int act) {
   switch (act) {
-    case A_RELU: return v > 0.0f ? v : (v != v ? v : 0.0f);
-    case A_SILU: return v / (1.0f + expf(-v));
+    case A_RELU:
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = v[r] > 0.0f ? v[r] : (v[r] != v[r] ? v[r] : 0.0f);
+      break;
+    case A_SILU:
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = v[r] / (1.0f + expf(-v[r]));
+      break;
     // forms without the cancellation of 1 + erf and 1 + tanh at negative v
-    case A_GELU: return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    case A_GELU_TANH: return v / (1.0f + expf(-1.59576912160573071f * (v + 0.044715f * v * v * v)));
-    default: return v;
+    case A_GELU:
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = 0.5f * v[r] * erfcf(-0.70710678118654752f * v[r]);
+      break;
+    case A_GELU_TANH:
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        v[r] = v[r] / (1.0f + expf(-1.59576912160573071f * (v[r] + 0.044715f * v[r] * v[r] * v[r])));
+      break;
+    default: break;
   }
 }
 
@@ -77,7 +92,6 @@ __device__ __forceinline__ bf16x8 widen8(uint2 v) {
 // instructions (bfloat16 output); e4m3 operands widened to bfloat16 (float32
 // output).
 enum Mode : int { L_BF16 = 0, L_F8 = 1, L_F8W = 2 };
-typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
 
 typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
 
@@ -132,25 +146,41 @@ struct Cols {
       bias[r] = a.bias && r < nv ? load_o<OUT>(a.bias, n + r) : 0.0f;
     }
   }
-  __device__ __forceinline__ void put(const LinArgs& a, int m, const f32x4& s, float sx) const {
-    float v[4];
+  // the residual's values of row m (0 without one)
+  __device__ __forceinline__ f32x4 residual(const LinArgs& a, int m) const {
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (!a.res) return v;
+    const size_t row = (size_t)m * a.R;
+    if (nv == 4 && rc + 4 <= a.R) {
+      if (OUT == T_F32) {
+        __builtin_memcpy(&v, static_cast<const float*>(a.res) + row + rc, 16);
+      } else {
+        uint2 q;
+        __builtin_memcpy(&q, static_cast<const uint16_t*>(a.res) + row + rc, 8);
+        v = f32x4{bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
+      }
+    } else {
+      int c = rc;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r < nv) v[r] = load_o<OUT>(a.res, row + c);
+        c = c + 1 == a.R ? 0 : c + 1;
+      }
+    }
+    return v;
+  }
+  // out[m, n .. n + 3] from the sums s, the row's scale and the residual's
+  // values.  PLAIN: neither activation nor residual.
+  template <bool PLAIN>
+  __device__ __forceinline__ void put(const LinArgs& a, int m, const f32x4& s, float sx, const f32x4& res) const {
+    f32x4 v;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       v[r] = IN == T_E4M3 ? s[r] * sx * sw[r] : s[r];
       if (a.bias) v[r] += bias[r];
     }
-    if (a.act != A_NONE) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = activate(v[r], a.act);
-    }
-    if (a.res) {
-      int c = rc;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (r < nv) v[r] += load_o<OUT>(a.res, (size_t)m * a.R + c);
-        c = c + 1 == a.R ? 0 : c + 1;
-      }
-    }
+    if (!PLAIN && a.act != A_NONE) activate(v, a.act);
+    if (!PLAIN && a.res) v += res;
     const size_t at = (size_t)m * a.N + n;
     if (nv == 4) {
       // rows may start at any element: the hardware splits a store where it crosses
@@ -285,7 +315,8 @@ __global__ void __launch_bounds__(64 * W) linear_rows_kernel(LinArgs a) {
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < W; ++k) v += part[(k * MT * NT + (r >> 4) * NT + j) * 64 + 16 * c + (r & 15)];
-    Cols<IN, OUT>(a, n).put(a, m, v, IN == T_E4M3 ? a.sx[m] : 1.0f);
+    const Cols<IN, OUT> cols(a, n);
+    cols.template put<false>(a, m, v, IN == T_E4M3 ? a.sx[m] : 1.0f, cols.residual(a, m));
   }
 }
 
@@ -458,30 +489,57 @@ done:
   if (IN == T_E4M3)
     for (int i = t; i < min(TM, a.M - m0); i += NTH) sxs[i] = a.sx[m0 + i];
   float* mine = tile + (wm * 16 * EB + l16) * PITCH + wn * 16 * NB + 4 * g;
-#pragma unroll
+  static_assert(WM <= 2, "the rows of a pass lie in at most two parts");
+#pragma unroll 1  // the code of a pass stays short: unrolled, its instructions miss their cache
   for (int ib = 0; ib < MB; ib += EB) {
     const int rows = 16 * min(EB, MB - ib);  // of each of the WM parts
 #pragma unroll
     for (int k = 0; k < WK; ++k) {
       if (WK == 1 || wk == k) {
 #pragma unroll
-        for (int i = 0; i < EB; ++i)
+        for (int b = 0; b < MB; b += EB) {
+          if (ib != b) continue;
 #pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            if (ib + i >= MB) continue;
-            f32x4* p = reinterpret_cast<f32x4*>(mine + 16 * i * PITCH + 16 * j);
-            *p = k == 0 ? acc[ib + i][j] : *p + acc[ib + i][j];
-          }
+          for (int i = b; i < b + EB && i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+              f32x4* p = reinterpret_cast<f32x4*>(mine + 16 * (i - b) * PITCH + 16 * j);
+              *p = k == 0 ? acc[i][j] : *p + acc[i][j];
+            }
+        }
       }
       __syncthreads();
     }
     if (ncol < a.N) {
+      const int all = WM * rows, tc = t % (TN / 4) * 4;
+      auto row_of = [&](int e) { return e < rows ? 16 * ib + e : 16 * (MB + ib) + e - rows; };  // of the tile
+      auto sums = [&](int e) {
+        return *reinterpret_cast<const f32x4*>(tile + (e < rows ? e : 16 * EB + e - rows) * PITCH + tc);
+      };
+      if (!a.res && a.act == A_NONE) {
 #pragma unroll 4
-      for (int e = t / (TN / 4); e < WM * rows; e += RS) {
-        const int p = WM == 1 ? 0 : e / rows, r = e - p * rows, m = p * 16 * MB + 16 * ib + r;  // row of the tile
-        if (m0 + m < a.M)
-          cols.put(a, m0 + m, *reinterpret_cast<const f32x4*>(tile + (p * 16 * EB + r) * PITCH + t % (TN / 4) * 4),
-                   IN == T_E4M3 ? sxs[m] : 1.0f);
+        for (int e = t / (TN / 4); e < all; e += RS) {
+          const int m = row_of(e);
+          if (m0 + m < a.M) cols.template put<true>(a, m0 + m, sums(e), IN == T_E4M3 ? sxs[m] : 1.0f, f32x4{});
+        }
+      } else {
+        // four rows at a time: their residuals are loaded before any is stored
+        constexpr int RB = 4;
+#pragma unroll 1
+        for (int e0 = t / (TN / 4); e0 < all; e0 += RB * RS) {
+          f32x4 res[RB];
+#pragma unroll
+          for (int k = 0; k < RB; ++k) {
+            const int e = e0 + k * RS, m = m0 + row_of(e);
+            if (e < all && m < a.M) res[k] = cols.residual(a, m);
+          }
+#pragma unroll
+          for (int k = 0; k < RB; ++k) {
+            const int e = e0 + k * RS, m = row_of(e);
+            if (e < all && m0 + m < a.M)
+              cols.template put<false>(a, m0 + m, sums(e), IN == T_E4M3 ? sxs[m] : 1.0f, res[k]);
+          }
+        }
       }
     }
     __syncthreads();
