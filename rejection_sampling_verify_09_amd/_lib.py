@@ -436,15 +436,15 @@ def _arg(t: torch.Tensor | None, name: str, dtype, shape, dev: int):
     """Pointer of an optional contiguous tensor of this type and shape on device ``dev`` (-1: not a device)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.get_device() == dev >= 0 and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} must be a device tensor" + (f" on cuda:{dev}" if dev >= 0 else ""))
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _int32(*sizes: int) -> None:
@@ -453,10 +453,8 @@ def _int32(*sizes: int) -> None:
         raise ValueError(f"sizes must be nonnegative and fit 32 bits, got {', '.join(map(str, sizes))}")
 
 
-def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
-    """An output tensor, its memory kept until the work on ``stream`` is done."""
-    # empty_like takes half of torch.empty's time on the host
-    t = torch.empty_like(like, dtype=dtype) if shape is like.shape or shape == like.shape else like.new_empty(shape, dtype=dtype)
+def _keep(t: torch.Tensor, stream) -> torch.Tensor:
+    """A new output, its memory kept until the work on ``stream`` is done."""
     if stream is not None:
         t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream)))
     return t
@@ -504,13 +502,13 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     xp = _arg(x, "x", x.dtype, x.shape, dev)
     s = _stream_on(dev, "x", stream)
     if out is None:
-        out = _new(x.shape, out_dtype, x, stream)
+        out = _keep(torch.empty_like(x, dtype=out_dtype), stream)  # half of torch.empty's time on the host
         op = out.data_ptr()
     if ocode == SV_E4M3 and out_scale is None:
-        out_scale = _new(x.shape[:-1], torch.float32, x, stream)
+        out_scale = _keep(x.new_empty(x.shape[:-1], dtype=torch.float32), stream)
         sp = out_scale.data_ptr()
     if residual is not None and out_residual is None:
-        out_residual = _new(x.shape, x.dtype, x, stream)
+        out_residual = _keep(torch.empty_like(x), stream)
         hp = out_residual.data_ptr()
     st = lib().sv_rms_norm(xp, rp, wp, float(eps), op, sp, hp, rows, d, code, ocode, s)
     if st != SV_OK:
@@ -557,7 +555,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     xp = _arg(x, "x", x.dtype, x.shape, dev)
     s = _stream_on(dev, "x", stream)
     if out is None:
-        out = _new(lead + (N,), out_dtype, x, stream)
+        out = _keep(x.new_empty(lead + (N,), dtype=out_dtype), stream)
         op = out.data_ptr()
     st = lib().sv_linear(xp, wp, xsp, wsp, bp, rp, op, M, N, K, R, ACTIVATIONS[activation], code, ocode, s)
     if st != SV_OK:
@@ -654,7 +652,7 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
     lp = _arg(logits, "logits", logits.dtype, logits.shape, dev)
     s = _stream_on(dev, "logits", stream)
     if out is None:
-        out = _new(logits.shape, logits.dtype, logits, stream)
+        out = _keep(torch.empty_like(logits), stream)
         op = out.data_ptr()
     if cu_num_draft is not None:
         st = lib().sv_adjust_logits_ragged(lp, op, hp, hl, pl, xp, cp, rp, fp, pp, cb, bt, bv, mp, mi, B, N, int(max_k),
