@@ -169,16 +169,21 @@ struct Cols {
     }
     return v;
   }
-  // out[m, n .. n + 3] from the sums s, the row's scale and the residual's
-  // values.  PLAIN: neither activation nor residual.
-  template <bool PLAIN>
-  __device__ __forceinline__ void put(const LinArgs& a, int m, const f32x4& s, float sx, const f32x4& res) const {
+  // the sums s with the scales and the bias
+  __device__ __forceinline__ f32x4 value(const LinArgs& a, const f32x4& s, float sx) const {
     f32x4 v;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       v[r] = IN == T_E4M3 ? s[r] * sx * sw[r] : s[r];
       if (a.bias) v[r] += bias[r];
     }
+    return v;
+  }
+  // out[m, n .. n + 3] from the sums s, the row's scale and the residual's
+  // values.  PLAIN: neither activation nor residual.
+  template <bool PLAIN>
+  __device__ __forceinline__ void put(const LinArgs& a, int m, const f32x4& s, float sx, const f32x4& res) const {
+    f32x4 v = value(a, s, sx);
     if (!PLAIN && a.act != A_NONE) activate(v, a.act);
     if (!PLAIN && a.res) v += res;
     const size_t at = (size_t)m * a.N + n;
@@ -476,6 +481,48 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs 
     }
   }
 done:
+  // Bfloat16 without activation and residual: the whole tile at once, rounded
+  // before it goes through LDS to be stored in whole rows.
+  if (OUT == T_BF16 && WK == 1 && !a.res && a.act == A_NONE) {
+    constexpr int P2 = 2 * TN + 16;  // bytes of a row, and a pad that keeps the lanes' rows in different banks
+    float sx[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const int m = m0 + wm * 16 * MB + 16 * i + l16;
+      sx[i] = IN == T_E4M3 ? a.sx[min(m, a.M - 1)] : 1.0f;
+    }
+    __syncthreads();  // the fragments read ahead
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int c = wn * 16 * NB + 16 * j + 4 * g;
+      const Cols<IN, OUT> cols(a, min(n0 + c, a.N - 1));
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const f32x4 v = cols.value(a, acc[i][j], sx[i]);
+        *reinterpret_cast<uint2*>(smem + (wm * 16 * MB + 16 * i + l16) * P2 + 2 * c) =
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      }
+    }
+    __syncthreads();
+    constexpr int TR = TN / 8;  // threads a row, eight columns each
+    const int c = t % TR * 8, nv = a.N - n0 - c;
+    char* const out = static_cast<char*>(a.out) + 2 * ((size_t)m0 * a.N + n0 + c);
+    const int mv = min(TM, a.M - m0);
+#pragma unroll 4
+    for (int m = t / TR; m < mv; m += NTH / TR) {
+      const uint4 v = *reinterpret_cast<const uint4*>(smem + m * P2 + 2 * c);
+      char* const o = out + 2 * (size_t)m * a.N;
+      if (nv >= 8) {
+        __builtin_memcpy(o, &v, 16);
+      } else {
+        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < nv) reinterpret_cast<uint16_t*>(o)[k] = (uint16_t)(q[k / 2] >> (k & 1 ? 16 : 0));
+      }
+    }
+    return;
+  }
   // Lane l of block (i, j) holds row 16 i + l % 16, columns 16 j + 4 (l / 16)
   // + 0 .. 3.  Through LDS, EB blocks of rows at a time: there the groups' sums
   // are added, in order, and the rows are stored whole, a thread having four
@@ -551,6 +598,7 @@ hipError_t launch_tile(LinArgs a, hipStream_t s) {
   constexpr int TM = 16 * MB * WM, TN = 16 * NB * WN;
   constexpr int lds = std::max(3 * WK * TM * 128 + 2 * WK * TN * 128, (16 * WM * tile_eb(MB, WM) * (TN + 4) + TM) * 4);
   static_assert(lds <= 160 * 1024, "LDS of a compute unit");
+  static_assert(WK > 1 || TM * (2 * TN + 16) <= lds, "a bfloat16 tile goes through LDS at once");
   a.mtiles = (a.M + TM - 1) / TM;
   a.ntiles = (a.N + TN - 1) / TN;
   // the limit is raised once per device (twice from racing first calls is harmless)
