@@ -47,28 +47,55 @@ struct LinArgs {
   int32_t turn;  // workgroups begin at different parts of k
 };
 
-// Of four values at a time, so that their chains of instructions overlap.
-__device__ __forceinline__ void activate(f32x4& v, int act) {
-  switch (act) {
-    case A_RELU:
+// v / (1 + exp(-z)): exp as 2^t (1 + d ln 2) with d what rounding t = -z log2(e)
+// left out, so that the whole is good to 4 units in the last place.  Where 2^t
+// is infinite or zero d plays no part (and may be NaN).
+__device__ __forceinline__ float gated(float v, float z) {
+  const float t = -1.44269504f * z;
+  const float d = __builtin_fmaf(z, -1.92596299e-8f, __builtin_fmaf(z, -1.44269504f, -t));
+  const float e = __builtin_amdgcn_exp2f(t) * (fabsf(z) < 128.0f ? __builtin_fmaf(d, 0.693147181f, 1.0f) : 1.0f);
+  return v * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
+// v erfc(-v / sqrt 2) / 2 without the cancellation of 1 + erf at negative v:
+// erfc(z) = exp(-z^2) t P(t), t = 1 / (1 + 0.3 z), with the polynomial P of
+// least relative error (2.0e-8) for z in [0, 10]; past it the result is 0 or v.
+__device__ __forceinline__ float gelu(float v) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(v), 0.3f * 0.707106781f, 1.0f));
+  float p = -0.129522771f;
+  p = __builtin_fmaf(p, t, 0.485562563f);
+  p = __builtin_fmaf(p, t, -0.512276769f);
+  p = __builtin_fmaf(p, t, 0.547718585f);
+  p = __builtin_fmaf(p, t, -0.0946497396f);
+  p = __builtin_fmaf(p, t, 0.214925647f);
+  p = __builtin_fmaf(p, t, 0.148339272f);
+  p = __builtin_fmaf(p, t, 0.170715213f);
+  p = __builtin_fmaf(p, t, 0.169188008f);
+  const float q = p * t * __builtin_amdgcn_exp2f(v * v * -0.721347520f);
+  return 0.5f * v * (v < 0.0f ? q : 2.0f - q);
+}
+
+// Of n values at a time, so that their chains of instructions overlap.
+template <int n>
+__device__ __forceinline__ void activate(f32x4 (&v)[n], int act) {
+  if (act == A_RELU) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = v[r] > 0.0f ? v[r] : (v[r] != v[r] ? v[r] : 0.0f);
-      break;
-    case A_SILU:
+    for (int r = 0; r < 4 * n; ++r) {
+      const float x = v[r / 4][r % 4];
+      v[r / 4][r % 4] = x > 0.0f ? x : (x != x ? x : 0.0f);
+    }
+  } else if (act == A_SILU) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = v[r] / (1.0f + expf(-v[r]));
-      break;
-    // forms without the cancellation of 1 + erf and 1 + tanh at negative v
-    case A_GELU:
+    for (int r = 0; r < 4 * n; ++r) v[r / 4][r % 4] = gated(v[r / 4][r % 4], v[r / 4][r % 4]);
+  } else if (act == A_GELU) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = 0.5f * v[r] * erfcf(-0.70710678118654752f * v[r]);
-      break;
-    case A_GELU_TANH:
+    for (int r = 0; r < 4 * n; ++r) v[r / 4][r % 4] = gelu(v[r / 4][r % 4]);
+  } else if (act == A_GELU_TANH) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        v[r] = v[r] / (1.0f + expf(-1.59576912160573071f * (v[r] + 0.044715f * v[r] * v[r] * v[r])));
-      break;
-    default: break;
+    for (int r = 0; r < 4 * n; ++r) {
+      const float x = v[r / 4][r % 4];
+      v[r / 4][r % 4] = gated(x, 1.59576912f * __builtin_fmaf(0.044715f * x * x, x, x));
+    }
   }
 }
 
@@ -179,13 +206,8 @@ struct Cols {
     }
     return v;
   }
-  // out[m, n .. n + 3] from the sums s, the row's scale and the residual's
-  // values.  PLAIN: neither activation nor residual.
-  template <bool PLAIN>
-  __device__ __forceinline__ void put(const LinArgs& a, int m, const f32x4& s, float sx, const f32x4& res) const {
-    f32x4 v = value(a, s, sx);
-    if (!PLAIN && a.act != A_NONE) activate(v, a.act);
-    if (!PLAIN && a.res) v += res;
+  // out[m, n .. n + 3]
+  __device__ __forceinline__ void store(const LinArgs& a, int m, const f32x4& v) const {
     const size_t at = (size_t)m * a.N + n;
     if (nv == 4) {
       // rows may start at any element: the hardware splits a store where it crosses
@@ -321,7 +343,10 @@ __global__ void __launch_bounds__(64 * W) linear_rows_kernel(LinArgs a) {
 #pragma unroll
     for (int k = 0; k < W; ++k) v += part[(k * MT * NT + (r >> 4) * NT + j) * 64 + 16 * c + (r & 15)];
     const Cols<IN, OUT> cols(a, n);
-    cols.template put<false>(a, m, v, IN == T_E4M3 ? a.sx[m] : 1.0f, cols.residual(a, m));
+    f32x4 y[1] = {cols.value(a, v, IN == T_E4M3 ? a.sx[m] : 1.0f)};
+    activate(y, a.act);
+    if (a.res) y[0] += cols.residual(a, m);
+    cols.store(a, m, y[0]);
   }
 }
 
@@ -563,30 +588,36 @@ done:
       auto sums = [&](int e) {
         return *reinterpret_cast<const f32x4*>(tile + (e < rows ? e : 16 * EB + e - rows) * PITCH + tc);
       };
-      if (!a.res && a.act == A_NONE) {
-#pragma unroll 4
-        for (int e = t / (TN / 4); e < all; e += RS) {
-          const int m = row_of(e);
-          if (m0 + m < a.M) cols.template put<true>(a, m0 + m, sums(e), IN == T_E4M3 ? sxs[m] : 1.0f, f32x4{});
-        }
-      } else {
-        // four rows at a time: their residuals are loaded before any is stored
-        constexpr int RB = 4;
+      // four rows at a time, all loads before the stores; rows past the last
+      // one are read as that one
+      constexpr int RB = 4;
 #pragma unroll 1
-        for (int e0 = t / (TN / 4); e0 < all; e0 += RB * RS) {
-          f32x4 res[RB];
+      for (int e0 = t / (TN / 4); e0 < all; e0 += RB * RS) {
+        f32x4 v[RB], res[RB];
+        float sx[RB];
+        int m[RB];
 #pragma unroll
-          for (int k = 0; k < RB; ++k) {
-            const int e = e0 + k * RS, m = m0 + row_of(e);
-            if (e < all && m < a.M) res[k] = cols.residual(a, m);
-          }
-#pragma unroll
-          for (int k = 0; k < RB; ++k) {
-            const int e = e0 + k * RS, m = row_of(e);
-            if (e < all && m0 + m < a.M)
-              cols.template put<false>(a, m0 + m, sums(e), IN == T_E4M3 ? sxs[m] : 1.0f, res[k]);
-          }
+        for (int k = 0; k < RB; ++k) {
+          const int e = min(e0 + k * RS, all - 1);
+          m[k] = row_of(e);
+          v[k] = sums(e);
+          sx[k] = IN == T_E4M3 ? sxs[m[k]] : 1.0f;
+          m[k] += m0;
         }
+        if (a.res) {
+#pragma unroll
+          for (int k = 0; k < RB; ++k) res[k] = cols.residual(a, min(m[k], a.M - 1));
+        }
+#pragma unroll
+        for (int k = 0; k < RB; ++k) v[k] = cols.value(a, v[k], sx[k]);
+        activate(v, a.act);
+        if (a.res) {
+#pragma unroll
+          for (int k = 0; k < RB; ++k) v[k] += res[k];
+        }
+#pragma unroll
+        for (int k = 0; k < RB; ++k)
+          if (e0 + k * RS < all && m[k] < a.M) cols.store(a, m[k], v[k]);
       }
     }
     __syncthreads();
