@@ -49,6 +49,7 @@ struct AdjArgs {
   const int32_t* midx;    // [rows], or null (row r has mask r)
   int32_t B, R, K, seen, V, cap, nbias, mask_rows, words;
   int32_t N, max_k, bonus;  // ragged: drafts in all, the most of one sequence, rows past them (0 or 1)
+  int32_t bcap;             // a slice's biases held in LDS (at most 16 a thread)
   int32_t nslices, rgroup;  // slices of the vocabulary; rows of a sequence per workgroup
 };
 
@@ -57,7 +58,6 @@ constexpr uint32_t E_PROMPT = 1u << 31, E_DRAFT = 1u << 30, E_BIAS = 1u << 29, E
 constexpr int E_SHIFT = 22;  // six bits: of a drafted token, the first draft that is it
 constexpr uint32_t E_COUNT = (1u << E_SHIFT) - 1;
 static_assert(SV_MAX_HISTORY <= E_COUNT && MAX_K <= 64, "counts and drafts fit an entry");
-constexpr int BIAS_LDS = 1024;  // a sequence's biases held in LDS (at most 16 a thread)
 constexpr uint16_t NONE = 0xFFFFu;
 constexpr int ADJ_MAX_WG = 1024, ADJ_EPT = 8;  // a thread has 8 tokens of the slice
 
@@ -152,14 +152,15 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint32_t smem[];
   const int t = threadIdx.x, nt = blockDim.x, S = nt * ADJ_EPT;
   uint32_t* tab = smem;                                           // [S]
-  uint32_t* bt = smem + S;                                        // [S] with biases: index of the token's first, then the sum
-  float* bvals = reinterpret_cast<float*>(smem + 2 * S);          // [BIAS_LDS] with biases: their values,
-  uint16_t* btoks = reinterpret_cast<uint16_t*>(bvals + BIAS_LDS);  // [BIAS_LDS] their tokens in the slice
-  uint16_t* bnext = btoks + BIAS_LDS;                             // [BIAS_LDS] and another of the same token
-  uint16_t* list = reinterpret_cast<uint16_t*>(smem + (a.cub ? 2 * S + 2 * BIAS_LDS : S));  // [S] in place: tokens of nonzero entries
+  uint32_t* bt = smem + S;                                        // [S] with biases: head of the token's chain, then the sum
+  float* bvals = reinterpret_cast<float*>(smem + 2 * S);          // [bcap] with biases: values of the slice's,
+  int32_t* bidx = reinterpret_cast<int32_t*>(bvals + a.bcap);     // [bcap] their indices,
+  uint16_t* btoks = reinterpret_cast<uint16_t*>(bidx + a.bcap);   // [bcap] their tokens
+  uint16_t* bnext = btoks + a.bcap;                               // [bcap] and another of the same token
+  uint16_t* list = a.cub ? bnext + a.bcap : reinterpret_cast<uint16_t*>(smem + S);  // [S] in place: tokens of nonzero entries
   __shared__ int32_t xs[MAX_K];                                   // the sequence's drafts,
   __shared__ uint64_t same[MAX_K];                                // and which of them are the same token
-  __shared__ int32_t nlist;
+  __shared__ int32_t nlist, nbiased;
   const int b = blockIdx.x / a.nslices, sl = blockIdx.x - b * a.nslices;
   const int v0 = sl * S, vn = min(S, a.V - v0);
   constexpr int EB = DT == T_F32 ? 4 : 2;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
       reinterpret_cast<uint4*>(tab)[i] = make_uint4(0u, 0u, 0u, 0u);
       if (a.cub) reinterpret_cast<uint4*>(bt)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
     }
-    if (t == 0) nlist = 0;
+    if (t == 0) nlist = nbiased = 0;
     __syncthreads();
   }
   // every entry becomes nonzero once, by whichever operation comes first: that thread lists the token
@@ -287,52 +288,59 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   if (a.cub) {
     // several biases of one token are added in the order they are listed, by
     // the thread that holds the first or, of a chain, its head
-    const int nb = i1 - i0;
-    if (nb <= BIAS_LDS) {
-      // each token's biases chained through LDS; the chain's order is any, so
-      // the head takes the lowest index left until none is (or, of a long
-      // chain, looks through all in order)
-      for (int i = t; i < nb; i += nt) {
-        const uint32_t j = (uint32_t)(i == t ? btok0 : a.btok[i0 + i]) - (uint32_t)v0;
-        bvals[i] = i == t ? bval0 : a.bval[i0 + i];
-        btoks[i] = j < (uint32_t)vn ? (uint16_t)j : NONE;
-        if (j < (uint32_t)vn) {
-          bnext[i] = (uint16_t)atomicExch(&bt[j], (uint32_t)i);
-          touch(j, atomicOr(&tab[j], E_BIAS));
-        }
+    for (int i = i0 + t; i < i1; i += nt) {
+      const uint32_t j = (uint32_t)(i == i0 + t ? btok0 : a.btok[i]) - (uint32_t)v0;
+      if (j >= (uint32_t)vn) continue;
+      const int p = atomicAdd(&nbiased, 1);
+      if (p < a.bcap) {
+        bidx[p] = i;
+        btoks[p] = (uint16_t)j;
+        bvals[p] = i == i0 + t ? bval0 : a.bval[i];
+        bnext[p] = (uint16_t)atomicExch(&bt[j], (uint32_t)p);
       }
-      __syncthreads();
+    }
+    __syncthreads();
+    const int nb = nbiased;
+    if (nb <= a.bcap) {
+      // the slice's biases in LDS, each token's chained, both in any order:
+      // a chain's head takes the lowest index left until none is (or, of a
+      // long chain, looks through the list in order)
       uint32_t head = 0;
-      for (int i = t, c = 0; i < nb; i += nt, ++c)
-        if (btoks[i] != NONE && bt[btoks[i]] == (uint32_t)i) head |= 1u << c;
+      for (int p = t, c = 0; p < nb; p += nt, ++c)
+        if (bt[btoks[p]] == (uint32_t)p) head |= 1u << c;
       __syncthreads();  // the sums take the heads' place
-      for (int i = t, c = 0; i < nb; i += nt, ++c) {
+      for (int p = t, c = 0; p < nb; p += nt, ++c) {
         if (!((head >> c) & 1)) continue;
-        float v = bvals[i];
-        if (bnext[i] != NONE) {
+        const int j = btoks[p];
+        float v = bvals[p];
+        if (bnext[p] != NONE) {
           int len = 0;
-          for (int k = i; k != NONE; k = bnext[k]) ++len;
-          v = 0.0f;
+          for (int k = p; k != NONE; k = bnext[k]) ++len;
+          bool any = false;
           if (len <= 16) {
             for (int q = 0, last = -1; q < len; ++q) {
-              int low = NONE;
-              for (int k = i; k != NONE; k = bnext[k])
-                if (k > last) low = min(low, k);
-              v = q == 0 ? bvals[low] : v + bvals[low];
+              int low = INT32_MAX, at = p;
+              for (int k = p; k != NONE; k = bnext[k])
+                if (bidx[k] > last && bidx[k] < low) low = bidx[k], at = k;
+              v = any ? v + bvals[at] : bvals[at];
+              any = true;
               last = low;
             }
           } else {
-            bool any = false;
-            for (int k = 0; k < nb; ++k)
-              if (btoks[k] == btoks[i]) {
-                v = any ? v + bvals[k] : bvals[k];
+            for (int k = i0; k < i1; ++k)
+              if (a.btok[k] == v0 + j) {
+                v = any ? v + a.bval[k] : a.bval[k];
                 any = true;
               }
           }
         }
-        bt[btoks[i]] = __float_as_uint(v);
+        bt[j] = __float_as_uint(v);
+        touch(j, atomicOr(&tab[j], E_BIAS));
       }
     } else {
+      // too many: bt first takes the index of each token's first
+      for (int i = t; i < S; i += nt) bt[i] = ~0u;
+      __syncthreads();
       for (int i = i0 + t; i < i1; i += nt) {
         const uint32_t j = (uint32_t)a.btok[i] - (uint32_t)v0;
         if (j >= (uint32_t)vn) continue;
@@ -498,9 +506,13 @@ hipError_t launch_adjust(AdjArgs a, int32_t rows_per_seq, hipStream_t s) {
   const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(2048 / wgs, (rows_per_seq + 3) / 4));
   a.rgroup = (rows_per_seq + groups - 1) / groups;
   const dim3 grid((unsigned)wgs, (unsigned)((rows_per_seq + a.rgroup - 1) / a.rgroup));
+  // A slice among many has few of its sequence's biases, and room for few of
+  // them leaves the compute unit room for more workgroups (128 x 11 bfloat16
+  // rows of 24979 with 300 biases each: 45 us with room for 1024, 37 with 384).
+  a.bcap = a.nslices >= 8 ? 384 : 1024;
   const size_t S = (size_t)nt * ADJ_EPT;
   const bool table = a.rep || a.freq || a.pres || a.cub;
-  const size_t lds = table ? S * 4 * (a.cub ? 2 : 1) + (a.cub ? BIAS_LDS * 8 : 0) + (inplace ? S * 2 : 0) : 0;
+  const size_t lds = table ? S * 4 * (a.cub ? 2 : 1) + (a.cub ? (size_t)a.bcap * 12 : 0) + (inplace ? S * 2 : 0) : 0;
   if (inplace)
     hipLaunchKernelGGL((adjust_kernel<DT, true>), grid, dim3(nt), lds, s, a);
   else

@@ -331,3 +331,32 @@ def test_the_widest_slices(nbias, dtype):
     mine = c["logits"].clone()
     call(c, out=mine, logits=mine)
     assert torch.equal(mine.view(_bits(c)), got.view(_bits(c)))
+
+
+@pytest.mark.parametrize("n,tokens", [(200, 3), (200, 40), (250, 1), (256, 256), (257, 30), (17, 1), (18, 1)])
+def test_chains_of_biases_add_up_in_their_order(n, tokens):
+    """Few and many biases of one token, in one slice and on both sides of
+    what it holds on chip; the float32 sums are those of the listed order."""
+    import torch
+
+    from rejection_sampling_verify_09_amd import adjust_logits
+
+    log(f"[adjust] {n} biases of {tokens} tokens")
+    g = np.random.default_rng(n * 1000 + tokens)
+    V = 900
+    tok = (g.permutation(n) % tokens * 3 + 1).astype(np.int32)
+    val = (g.standard_normal(n) * 10.0 ** g.integers(-4, 5, n)).astype(np.float32)
+    want = np.zeros(V, dtype=np.float32)
+    seen = set()
+    for t, v in zip(tok, val):
+        want[t] = np.float32(want[t] + v) if t in seen else v
+        seen.add(int(t))
+    # a second sequence without any, and a third with the same in another place of the list
+    cu = cuda(np.array([0, n, n, 2 * n], dtype=np.int32))
+    b = (cu, cuda(np.concatenate([tok, tok])), cuda(np.concatenate([val, val])))
+    lg = torch.zeros((3, V), device="cuda")
+    for _ in range(2):
+        out = adjust_logits(lg, bias=b).cpu().numpy()
+        assert np.array_equal(out[0], want) and np.array_equal(out[2], want) and not out[1].any()
+    adjust_logits(lg, bias=b, out=lg)
+    assert np.array_equal(lg.cpu().numpy(), out)
