@@ -84,6 +84,25 @@ struct Eight {
   __device__ __forceinline__ float get(int k) const {
     return DT == T_F32 ? __uint_as_float(w[k]) : (k & 1) ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);
   }
+  // Element k, in a register that only run time knows: by masks (a choice
+  // between the words would put them into memory).
+  __device__ __forceinline__ float pick(int k) const {
+    const int word = DT == T_F32 ? k : k >> 1;
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v |= w[i] & (word == i ? ~0u : 0u);
+    return DT == T_F32 ? __uint_as_float(v) : (k & 1) ? bf16_hi(v) : bf16_lo(v);
+  }
+  __device__ __forceinline__ void put(int k, float f) {
+    const int word = DT == T_F32 ? k : k >> 1;
+    const uint32_t b = DT == T_F32 ? __float_as_uint(f) : (uint32_t)to_bf16(f) << (k & 1 ? 16 : 0);
+    const uint32_t part = DT == T_F32 ? ~0u : k & 1 ? 0xFFFF0000u : 0xFFFFu;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t on = word == i ? part : 0u;
+      w[i] = (w[i] & ~on) | (b & on);
+    }
+  }
   // n < 8: the first n of them, the others 0.  Rows may start at any element
   // (the hardware splits a 16-byte access where it crosses a boundary).
   __device__ __forceinline__ void load(const char* p, int n) {
@@ -197,6 +216,13 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   const int r0 = blockIdx.y * a.rgroup, r1 = min(nr, r0 + a.rgroup);
   const size_t pitch = (size_t)a.V * EB;
 
+  // what the table takes, loaded ahead of the rows
+  const float rep = a.rep ? a.rep[b] : 1.0f, freq = a.freq ? a.freq[b] : 0.0f, pres = a.pres ? a.pres[b] : 0.0f;
+  const float rinv = 1.0f / rep;
+  const int nh = !counts || !a.hist ? 0 : a.hlen ? min(max(a.hlen[b], 0), a.cap) : a.cap;
+  const int np = nh && a.plen ? min(max(a.plen[b], 0), nh) : 0;
+  const int32_t draft = counts && t < nd ? a.drafts[d0 + t] : -1;
+
   // Out of place: this thread's 8 tokens of every row, UN rows' loads in
   // flight; the first ones are under way while the table is built
   constexpr int UN = 4;
@@ -249,8 +275,6 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   if (counts) {
     if (a.hist) {
       const int32_t* h = a.hist + (size_t)b * a.cap;
-      const int nh = a.hlen ? min(max(a.hlen[b], 0), a.cap) : a.cap;
-      const int np = a.plen ? min(max(a.plen[b], 0), nh) : 0;
       auto count = [&](int i, int32_t tok) {
         const uint32_t j = (uint32_t)tok - (uint32_t)v0;
         if (j < (uint32_t)vn) touch(j, i < np ? atomicOr(&tab[j], E_PROMPT) : atomicAdd(&tab[j], 1u));
@@ -275,7 +299,7 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
           for (int k = 0; k < 4; ++k) count(i + 4 * u * nt + k, q[u][k]);
       }
     }
-    if (t < nd) xs[t] = a.drafts[d0 + t];
+    if (t < nd) xs[t] = draft;
     __syncthreads();
     if (t < nd) {
       uint64_t m = 0;
@@ -371,8 +395,6 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   }
   if (table) __syncthreads();
 
-  const float rep = a.rep ? a.rep[b] : 1.0f, freq = a.freq ? a.freq[b] : 0.0f, pres = a.pres ? a.pres[b] : 0.0f;
-  const float rinv = 1.0f / rep;
   const bool biased = a.cub != nullptr;
   // a token's logit in a row that has seen the drafts in `seen`: table entry e, bias w
   auto fix = [&](float l, uint32_t e, uint32_t w, uint64_t seen) {
@@ -428,22 +450,23 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   if (n <= 0) return;
   // Per token once for all rows: what its count takes off (sub), and the bits
   // of the words it changes (sel).  Every wave of a sequence with a history
-  // has such tokens, so the common ones are handled without a branch; a
-  // thread with a drafted or biased token goes through its table entries.
+  // has such tokens, so the common ones are handled without a branch, and
+  // then the drafted and biased ones (odd) one by one.
   float sub[8];
-  uint32_t sel[Eight<DT>::W];
-  bool any = false, odd = false;
+  uint32_t sel[Eight<DT>::W], odd = 0;
+  bool any = false;
 #pragma unroll
   for (int k = 0; k < Eight<DT>::W; ++k) sel[k] = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const uint32_t e = table ? tab[8 * t + k] : 0u;
+    const bool own = e & (E_DRAFT | E_BIAS), plain = e && !own;
     sub[k] = penalty((float)(e & E_COUNT), freq, pres);
-    any |= e != 0;
-    odd |= (e & (E_DRAFT | E_BIAS)) != 0;
+    any |= plain;
+    if (own) odd |= 1u << k;
     if (DT == T_F32)
-      sel[k] = e ? ~0u : 0u;
-    else if (e)
+      sel[k] = plain ? ~0u : 0u;
+    else if (plain)
       sel[k / 2] |= (k & 1) ? 0xFFFF0000u : 0xFFFFu;
   }
   char* out = static_cast<char*>(a.out) + (size_t)row0 * pitch + (size_t)vt * EB;
@@ -456,20 +479,10 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
       if (r + u >= r1) continue;
       if (any) {
         float f[8];
-        if (!odd) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float x = l[u].get(k);
-            f[k] = x * (x > 0.0f ? rinv : rep) - sub[k];
-          }
-        } else {
-          const uint64_t seen = seen_by(r + u);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t e = tab[8 * t + k];
-            f[k] = l[u].get(k);
-            if (e) f[k] = fix(f[k], e, biased ? bt[8 * t + k] : 0u, seen);
-          }
+        for (int k = 0; k < 8; ++k) {
+          const float x = l[u].get(k);
+          f[k] = x * (x > 0.0f ? rinv : rep) - sub[k];
         }
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
@@ -480,6 +493,10 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
             l[u].w[k / 2] = (pack_bf16(f[k], f[k + 1]) & sel[k / 2]) | (l[u].w[k / 2] & ~sel[k / 2]);
           }
         }
+      }
+      for (uint32_t q = odd; q; q &= q - 1) {
+        const int k = __builtin_ctz(q);
+        l[u].put(k, fix(l[u].pick(k), tab[8 * t + k], biased ? bt[8 * t + k] : 0u, seen_by(r + u)));
       }
       if (m[u] != 0xFFu) l[u].forbid(m[u]);
       l[u].store(out + (size_t)(r + u) * pitch, n);
