@@ -17,13 +17,13 @@
 // Bound by memory.  Out of place every logit is read and written once, 16
 // bytes a lane, four rows' loads in flight, the first of them under way while
 // the table is built: 256 x 9 float32 rows of 152064 with histories of 8192
-// and masks take 550 us (5.2 TB/s; a large copy reaches 5.1), 64 x 7 bfloat16
-// rows of 128256 56 us (4.1 TB/s).  There the arithmetic shows: a branch per
+// and masks take 497 us (5.7 TB/s; a large copy reaches 5.1), 64 x 7 bfloat16
+// rows of 128256 55 us (4.2 TB/s).  There the arithmetic shows: a branch per
 // touched token, with a division in it, took 73 us, the branch-free form on 8
-// tokens a lane 56.  In place only what changes is touched: the list of the
-// slice's tokens, and the runs of 8 that a mask cuts (the same 64 x 7 rows:
-// 30 us, whose scattered logits lie in half of all lines; masks alone on 32 x 7
-// rows: 16 us).
+// tokens a lane 59, the drafted and biased ones alone one by one 55.  In place
+// only what changes is touched: the list of the slice's tokens, and the runs of
+// 8 that a mask cuts (the same 64 x 7 rows: 30 us, whose scattered logits lie in
+// half of all lines; masks alone on 32 x 7 rows: 14 us).
 #include "sv_ops.hpp"
 #include "specverify.h"
 

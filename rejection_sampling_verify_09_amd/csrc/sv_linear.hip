@@ -254,7 +254,7 @@ __device__ __forceinline__ void wave_sync() {
 // about 256 columns at its own: where they all begin at 0, they ask for the
 // same bytes of every row at once, and rows a power of two apart keep only some
 // of the memory's channels busy (64 x 24576 x 4096 bfloat16 with 64 x 128 tiles:
-// 47.7 us from 0, 40.6 so; 16 x 32000 x 4096 e4m3: 28.1 and 24.2; rows of 4224
+// 48.0 us from 0, 40.4 so; 16 x 32000 x 4096 e4m3: 27.2 and 24.2; rows of 4224
 // bytes: alike).  Where x is larger than an XCD's L2, all begin at 0, so that
 // the column panels read the same part of x (4096 x 16384 x 4096 e4m3: 264 us,
 // 275 otherwise).
@@ -270,11 +270,11 @@ __device__ __forceinline__ int turned(int round, int first, int rounds) {
 // registers; the waves' sums are added in LDS.  Loads take whole 128-byte
 // lines, eight rows each (a fragment's own layout, 16 rows across neighbouring
 // lanes, keeps the address unit four times as long, 64 against 16 cycles a
-// load), and a wave brings them into fragments through LDS of its own: 16 x
-// 4096 x 4096 bfloat16 9.2 us a call against 10.2 with fragments loaded
-// directly, 16 x 24576 x 4096 41 against 50, 16 x 128256 x 4096 e4m3 98 against
-// 112 (1 row: 92 against 94).  Bound by the weight's bytes, 5.7 to 6.3 TB/s on
-// long ones, the launch on short ones.
+// load), and a wave brings them into fragments through LDS of its own (16 x
+// 24576 x 4096 bfloat16 41 us, 50 with fragments loaded directly).  Bound by
+// the weight's bytes on long weights: 1 x 128256 x 4096 takes 164 us in
+// bfloat16 (6.4 TB/s) and 85 in e4m3 (6.2), 7 rows to float32 89; by the launch
+// on short ones (1 x 4096 x 4096: 9.0 us).
 template <int MODE, int OUT, int NT, int MT, int W, int D>
 __global__ void __launch_bounds__(64 * W) linear_rows_kernel(LinArgs a) {
   constexpr int IN = MODE == L_BF16 ? T_BF16 : T_E4M3;
@@ -379,9 +379,12 @@ constexpr int LIN_XCD = 8;  // XCDs the workgroup ids are dealt over
 // workgroup a compute unit): its rounds take about 1.4 us, 1.0 of them the
 // matrix instructions' at the clock they leave the chip, the rest LDS traffic
 // (112 KB of rows, 64 KB of weights read, 60 KB written a round) that overlaps
-// them in part.  At 448 x 128256 x 4096: e4m3 to bfloat16 244 us (1.93 PFLOP/s),
-// bfloat16 432 (1.09), e4m3 to float32 395 (1.19); the library's products take
-// 295 and 543.
+// them in part; by the counters the matrix units are busy 53% of the whole time
+// and LDS 39%.  At 448 x 128256 x 4096: e4m3 to bfloat16 231 us (2.04 PFLOP/s),
+// bfloat16 427 (1.10), e4m3 to float32 381 (1.24); the library's products of
+// 8-bit and bfloat16 operands take 295 and 543.  The small tiles are bound by
+// the latency of a round (loads, LDS, barrier: 0.7 us), of which 333 x 5001 x
+// 2112 has 17 (17.4 us; the library 22.8).
 template <int MODE, int OUT, int MB, int NB, int WM, int WN, int WK, int D>
 __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs a) {
   constexpr int IN = MODE == L_BF16 ? T_BF16 : T_E4M3;
@@ -668,8 +671,8 @@ constexpr TileCost kTiles[] = {
 // 38 with 64 x 128).  Measured against each of them on 34 shapes and three type
 // combinations, the choice is 0.6% slower than the fastest in the mean, 15% at
 // most; 64 x 64 everywhere, for one, takes twice as long at 448 x 128256 x 2048
-// (483 against 255 us), and 224 x 256 five times as long at 128 x 4096 x 4096
-// (83 against 17 us).
+// (471 against 225 us), and 224 x 256 five times as long at 128 x 4096 x 4096
+// (78 against 16 us).
 int pick_tile(int64_t M, int64_t N, int64_t steps) {
   int best = -1;
   double least = 0.0;
@@ -690,28 +693,29 @@ int pick_tile(int64_t M, int64_t N, int64_t steps) {
 }
 
 // The kernel of a product: an index of kTiles, or one of these for up to 16 rows.
-enum Few : int { ROWS_16 = -1, ROWS_32 = -2, TILE_16 = -3 };  // 16 and 32 columns a workgroup; 16 x 64 tiles
+enum Few : int { ROWS_16 = -1, ROWS_32 = -2 };  // 16 and 32 columns a workgroup
 
 int pick_kernel(int64_t M, int64_t N, int64_t kbytes) {
-  if (M > 16) return pick_tile(M, N, (kbytes + 127) / 128);
+  const int64_t steps = (kbytes + 127) / 128;
+  if (M > 16) return pick_tile(M, N, steps);
   // Up to 8192 columns: 16 a workgroup, whose eight waves share k, so that
-  // there are enough of them (16 x 1000 x 16384 bfloat16: 15 us, 23 with 32
-  // columns and four waves; 16 x 8192 x 16384: 57 against 63).  Then 32 columns
-  // where rows are short, since each wave has only a few steps of one (k of
-  // 4096 bytes, 16 x 128256 e4m3: 98 against 113 us; of 2048, 16 x 24576: 10.6
-  // against 12.0), 16 where they are longer (8192 bytes, 1 x 24576: 26 against
-  // 35 us), and tiles where many columns meet more than 8 rows, whose x they
-  // share (16 x 128256 x 4096 bfloat16: 178 against 203 us, 24576 columns: 42
-  // against 41, 8 rows: 174 against 178, 1 row: 169 against 166).
+  // there are enough of them (16 x 1000 x 16384 bfloat16: 15.5 us, 24 with 32
+  // columns and four waves; 16 x 4096 x 4096: 9.1 against 11.4).  Then 32
+  // columns where rows are short, since each wave has only a few steps of one (k
+  // of 4096 bytes, 16 x 128256 e4m3: 94 against 111 us; of 2048, 16 x 24576: 10.7
+  // against 12.3), and 16 where they are longer (8192 bytes, 1 x 128256: 164
+  // against 183 us).  Many columns with more than 8 long rows share the rows of
+  // x in the tiles of larger products (16 x 128256 x 4096 bfloat16: 182 against
+  // 202 us; 8 rows 181 against 177, 1 row 177 against 164).
   if (N <= 8192) return ROWS_16;
   if (kbytes <= 4096) return ROWS_32;
-  return M <= 8 || N <= 24576 ? ROWS_16 : TILE_16;
+  return M <= 8 || N <= 24576 ? ROWS_16 : pick_tile(M, N, steps);
 }
 
 // Threads of the launch, or an upper bound (every workgroup has at most 512).
 int64_t launch_threads(int kernel, int64_t M, int64_t N) {
   const int64_t tm = kernel >= 0 ? kTiles[kernel].tm : 16;
-  const int64_t tn = kernel >= 0 ? kTiles[kernel].tn : kernel == ROWS_16 ? 16 : kernel == ROWS_32 ? 32 : 64;
+  const int64_t tn = kernel >= 0 ? kTiles[kernel].tn : kernel == ROWS_16 ? 16 : 32;
   return (((M + tm - 1) / tm) * ((N + tn - 1) / tn) + LIN_XCD) * 512;
 }
 
@@ -720,7 +724,6 @@ hipError_t launch_linear(const LinArgs& a, int kernel, hipStream_t s) {
   switch (kernel) {
     case ROWS_16: return launch_rows<MODE, OUT, 1, 1, 8, 2>(a, s);
     case ROWS_32: return launch_rows<MODE, OUT, 2, 1, 4, 2>(a, s);
-    case TILE_16: return launch_tile<MODE, OUT, 1, 1, 1, 4, 2, 2>(a, s);
     case 0: return launch_tile<MODE, OUT, 2, 1, 1, 2, 4, 2>(a, s);
     case 1: return launch_tile<MODE, OUT, 2, 2, 1, 2, 4, 2>(a, s);
     case 2: return launch_tile<MODE, OUT, 2, 2, 2, 2, 2, 2>(a, s);

@@ -6,7 +6,7 @@
 // Bound by memory: each element is read once (with its residual) and written
 // once (with the new residual).  A row stays in registers between the sum of
 // squares and the output, so nothing is read twice, whatever its width: 16384
-// x 8192 bfloat16 rows with a residual take 179 us (6.0 TB/s; a large copy
+// x 8192 bfloat16 rows with a residual take 177 us (6.1 TB/s; a large copy
 // reaches 5.1), 8193 columns, whose rows start at any 2 bytes, 248 us (an
 // element a load took 679).  Up to about 2000 rows of 4096 the launch is what
 // counts.
