@@ -47,14 +47,18 @@ struct LinArgs {
   int32_t turn;  // workgroups begin at different parts of k
 };
 
-// v / (1 + exp(-z)): exp as 2^t (1 + d ln 2) with d what rounding t = -z log2(e)
-// left out, so that the whole is good to 4 units in the last place.  Where 2^t
-// is infinite or zero d plays no part (and may be NaN).
+// v / (1 + exp(-z)), from a = exp(-|z|): v / (1 + a), or v a / (1 + a) for
+// negative z.  a is 2^t (1 + d ln 2), d being what rounding t = -|z| log2(e)
+// left out, so that the whole is good to 5 units in the last place; below 2^-64
+// it is held 2^64 times larger, since v a may be a normal number where a is not.
+// Where a is 0, d plays no part (and may be NaN).
 __device__ __forceinline__ float gated(float v, float z) {
-  const float t = -1.44269504f * z;
-  const float d = __builtin_fmaf(z, -1.92596299e-8f, __builtin_fmaf(z, -1.44269504f, -t));
-  const float e = __builtin_amdgcn_exp2f(t) * (fabsf(z) < 128.0f ? __builtin_fmaf(d, 0.693147181f, 1.0f) : 1.0f);
-  return v * __builtin_amdgcn_rcpf(1.0f + e);
+  const float x = fabsf(z), t = -1.44269504f * x;
+  const float d = __builtin_fmaf(x, -1.92596299e-8f, __builtin_fmaf(x, -1.44269504f, -t));
+  const bool small = t < -64.0f;
+  const float a = __builtin_amdgcn_exp2f(small ? t + 64.0f : t) * (x < 128.0f ? __builtin_fmaf(d, 0.693147181f, 1.0f) : 1.0f);
+  const float r = __builtin_amdgcn_rcpf(small ? 1.0f : 1.0f + a);
+  return z >= 0.0f ? v * r : v * a * r * (small ? 0x1p-64f : 1.0f);
 }
 
 // v erfc(-v / sqrt 2) / 2 without the cancellation of 1 + erf at negative v:

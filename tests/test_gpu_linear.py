@@ -231,3 +231,64 @@ def test_offsets_past_32_bits():
         first = linear(x[:2].clone(), w[:77].clone(), out_dtype=torch.float32)
         assert torch.equal(out[:2, :77], first)
         del out, w
+
+
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("M,N,K", [(440, 30001, 64), (1001, 8190, 128), (192, 32003, 64), (130, 20007, 576)])
+def test_wide_tiles_between_margins(M, N, K, dtype, odt):
+    """Products of many tiles, rows of an odd length from any element on: the
+    sums are exact, and nothing around the output is written."""
+    import torch
+
+    from rejection_sampling_verify_09_amd import linear
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + N + K)
+    log(f"[linear wide] M={M} N={N} K={K} {dtype} -> {odt}")
+    x, w = grid(g, (M, K), dtype), grid(g, (N, K), dtype)
+    sx = sw = None
+    if dtype == "e4m3":
+        sx = torch.exp2(torch.randint(-3, 4, (M,), device="cuda", generator=g).float())
+        sw = torch.exp2(torch.randint(-3, 4, (N,), device="cuda", generator=g).float())
+    want = x.float().cpu() @ w.float().cpu().T  # exact
+    if sx is not None:
+        want = want * sx.cpu()[:, None] * sw.cpu()
+    for off in (1, 5):
+        buf = torch.full((M * N + 16,), 7.0, device="cuda", dtype=_t(odt))
+        out = buf[off:off + M * N].view(M, N)
+        linear(x, w, x_scale=sx, weight_scale=sw, out_dtype=_t(odt), out=out)
+        assert torch.equal(out.cpu(), want.to(_t(odt)))
+        assert (buf[:off] == 7).all() and (buf[off + M * N:] == 7).all()
+
+
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [1, 40])
+def test_activations_of_extreme_values(M, act, odt):
+    """Signed zeros, the smallest and largest values, infinities and NaN,
+    brought in by the bias of a product of zeros."""
+    import torch
+
+    from rejection_sampling_verify_09_amd import linear
+
+    log(f"[linear extremes] M={M} {act} -> {odt}")
+    v = [0.0, -0.0, 1e-45, -1e-45, 1.2e-38, -1.2e-38, 1e-20, -1e-20, 1e4, -1e4, 1e10, -1e10, 1e20, -1e20, 3e38, -3e38,
+         float("inf"), -float("inf"), float("nan")]
+    v += [s * k for k in (0.5, 1.0, 5.0, 9.0, 13.0, 14.5, 20.0, 86.0, 87.5, 88.5, 100.0, 103.5, 127.0, 128.0, 129.0)
+          for s in (1.0, -1.0)]
+    bias = torch.tensor(v, device="cuda").to(_t(odt))
+    x = torch.zeros((M, 64), device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros((len(v), 64), device="cuda", dtype=torch.bfloat16)
+    got = np64(linear(x, w, bias=bias, activation=act, out_dtype=_t(odt)))
+    b = np64(bias)
+    with np.errstate(all="ignore"):
+        want = np.tile(ref.activate(b, act), (M, 1))
+        z = np.minimum(np.abs(2 * np.sqrt(2 / np.pi) * (b + 0.044715 * b ** 3)) if act == "gelu_tanh" else np.abs(b), 200.0)
+        rel = (2 * (z * z / 2) + 1) * 2 * ULP + 20 * ULP if act == "gelu" else (8 + 4 * z) * ULP
+        tol = rel * np.abs(want) + 2.0 ** -120 + (2.0 ** -8 if odt == "bf16" else 0.0) * np.abs(want)
+    nan, inf = np.isnan(want), np.isinf(want)
+    assert np.array_equal(np.isnan(got), nan)
+    assert np.array_equal(got[inf], want[inf])
+    ok = ~nan & ~inf
+    assert np.all(np.abs(got[ok] - want[ok]) <= tol[ok])
