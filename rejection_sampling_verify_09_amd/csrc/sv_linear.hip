@@ -61,6 +61,14 @@ __device__ __forceinline__ float gated(float v, float z) {
   return z >= 0.0f ? v * r : v * a * r * (small ? 0x1p-64f : 1.0f);
 }
 
+// The same for a bfloat16 output: what rounding t leaves out is at most |z| 2^-24
+// of the result, and goes without (half the instructions).  All of it 2^8 times
+// smaller, so that the reciprocal is a normal number where the result is.
+__device__ __forceinline__ float gated_bf16(float v, float z) {
+  const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z, -1.44269504f, -8.0f));
+  return v * 0x1p-8f * __builtin_amdgcn_rcpf(0x1p-8f + e);
+}
+
 // v erfc(-v / sqrt 2) / 2 without the cancellation of 1 + erf at negative v:
 // erfc(z) = exp(-z^2) t P(t), t = 1 / (1 + 0.3 z), with the polynomial P of
 // least relative error (2.0e-8) for z in [0, 10]; past it the result is 0 or v.
@@ -80,8 +88,9 @@ __device__ __forceinline__ float gelu(float v) {
 }
 
 // Of n values at a time, so that their chains of instructions overlap.
-template <int n>
+template <int OUT, int n>
 __device__ __forceinline__ void activate(f32x4 (&v)[n], int act) {
+  auto gate = [](float v, float z) { return OUT == T_BF16 ? gated_bf16(v, z) : gated(v, z); };
   if (act == A_RELU) {
 #pragma unroll
     for (int r = 0; r < 4 * n; ++r) {
@@ -90,7 +99,7 @@ __device__ __forceinline__ void activate(f32x4 (&v)[n], int act) {
     }
   } else if (act == A_SILU) {
 #pragma unroll
-    for (int r = 0; r < 4 * n; ++r) v[r / 4][r % 4] = gated(v[r / 4][r % 4], v[r / 4][r % 4]);
+    for (int r = 0; r < 4 * n; ++r) v[r / 4][r % 4] = gate(v[r / 4][r % 4], v[r / 4][r % 4]);
   } else if (act == A_GELU) {
 #pragma unroll
     for (int r = 0; r < 4 * n; ++r) v[r / 4][r % 4] = gelu(v[r / 4][r % 4]);
@@ -98,7 +107,7 @@ __device__ __forceinline__ void activate(f32x4 (&v)[n], int act) {
 #pragma unroll
     for (int r = 0; r < 4 * n; ++r) {
       const float x = v[r / 4][r % 4];
-      v[r / 4][r % 4] = gated(x, 1.59576912f * __builtin_fmaf(0.044715f * x * x, x, x));
+      v[r / 4][r % 4] = gate(x, 1.59576912f * __builtin_fmaf(0.044715f * x * x, x, x));
     }
   }
 }
@@ -348,7 +357,7 @@ __global__ void __launch_bounds__(64 * W) linear_rows_kernel(LinArgs a) {
     for (int k = 0; k < W; ++k) v += part[(k * MT * NT + (r >> 4) * NT + j) * 64 + 16 * c + (r & 15)];
     const Cols<IN, OUT> cols(a, n);
     f32x4 y[1] = {cols.value(a, v, IN == T_E4M3 ? a.sx[m] : 1.0f)};
-    activate(y, a.act);
+    activate<OUT>(y, a.act);
     if (a.res) y[0] += cols.residual(a, m);
     cols.store(a, m, y[0]);
   }
@@ -513,36 +522,94 @@ __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs 
     }
   }
 done:
-  // Bfloat16 without activation and residual: the whole tile at once, rounded
-  // before it goes through LDS to be stored in whole rows.
-  if (OUT == T_BF16 && WK == 1 && !a.res && a.act == A_NONE) {
+  // Bfloat16: the whole tile at once, rounded before it goes through LDS to be
+  // stored in whole rows.  A residual comes the same way, into its elements'
+  // places.
+  if constexpr (OUT == T_BF16 && WK == 1) {
     constexpr int P2 = 2 * TN + 16;  // bytes of a row, and a pad that keeps the lanes' rows in different banks
+    constexpr int TR = TN / 8, NR = TM * TR / NTH;  // threads a row, eight columns each; rows a thread
+    static_assert(TM * TR % NTH == 0, "whole rows");
+    const int tr = t / TR, tc = t % TR * 8, nv = a.N - n0 - tc, mv = min(TM, a.M - m0);
+    uint4 res[NR];
+    if (a.res) {
+      const int rc = (n0 + tc) % a.R;
+#pragma unroll
+      for (int k = 0; k < NR; ++k) {
+        const int m = min(m0 + tr + k * (NTH / TR), a.M - 1);
+        const uint16_t* const r = static_cast<const uint16_t*>(a.res) + (size_t)m * a.R;
+        if (nv >= 8 && rc + 8 <= a.R) {
+          __builtin_memcpy(&res[k], r + rc, 16);
+        } else {
+          uint32_t q[4] = {0, 0, 0, 0};
+          int c = rc;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (e < nv) q[e / 2] |= (uint32_t)r[c] << (e & 1 ? 16 : 0);
+            c = c + 1 == a.R ? 0 : c + 1;
+          }
+          res[k] = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+      }
+    }
     float sx[MB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      const int m = m0 + wm * 16 * MB + 16 * i + l16;
-      sx[i] = IN == T_E4M3 ? a.sx[min(m, a.M - 1)] : 1.0f;
-    }
-    __syncthreads();  // the fragments read ahead
+    for (int i = 0; i < MB; ++i) sx[i] = IN == T_E4M3 ? a.sx[min(m0 + wm * 16 * MB + 16 * i + l16, a.M - 1)] : 1.0f;
+    f32x4 sw[NB], bias[NB];  // of the lane's columns
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const int c = wn * 16 * NB + 16 * j + 4 * g;
-      const Cols<IN, OUT> cols(a, min(n0 + c, a.N - 1));
+      const Cols<IN, OUT> cols(a, min(n0 + wn * 16 * NB + 16 * j + 4 * g, a.N - 1));
+      sw[j] = f32x4{cols.sw[0], cols.sw[1], cols.sw[2], cols.sw[3]};
+      bias[j] = f32x4{cols.bias[0], cols.bias[1], cols.bias[2], cols.bias[3]};
+    }
+    __syncthreads();  // the fragments read ahead
+    char* const mine = smem + (wm * 16 * MB + l16) * P2 + 2 * (wn * 16 * NB + 4 * g);
+    auto scaled = [&](const f32x4& s, int i, const f32x4& w, const f32x4& b) {
+      const f32x4 v = IN == T_E4M3 ? s * sx[i] * w : s;
+      return a.bias ? v + b : v;
+    };
+    auto put = [&](int i, int j, const f32x4& v) {  // 16 i rows and 16 j columns on
+      *reinterpret_cast<uint2*>(mine + 16 * i * P2 + 32 * j) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    };
+    if (!a.res && a.act == A_NONE) {
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        const f32x4 v = cols.value(a, acc[i][j], sx[i]);
-        *reinterpret_cast<uint2*>(smem + (wm * 16 * MB + 16 * i + l16) * P2 + 2 * c) =
-            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < MB; ++i) put(i, j, scaled(acc[i][j], i, sw[j], bias[j]));
+    } else {
+      if (a.res) {
+#pragma unroll
+        for (int k = 0; k < NR; ++k) *reinterpret_cast<uint4*>(smem + (tr + k * (NTH / TR)) * P2 + 2 * tc) = res[k];
+        __syncthreads();
+      }
+#pragma unroll 1  // one copy of the activations' code
+      for (int j = 0; j < NB; ++j) {
+        f32x4 v[MB], w, q;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          if (b != 0 && j != b) continue;
+          w = sw[b];
+          q = bias[b];
+#pragma unroll
+          for (int i = 0; i < MB; ++i) v[i] = acc[i][b];
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i) v[i] = scaled(v[i], i, w, q);
+        activate<OUT>(v, a.act);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          if (a.res) {
+            const uint2 r = *reinterpret_cast<const uint2*>(mine + 16 * i * P2 + 32 * j);
+            v[i] += f32x4{bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y)};
+          }
+          put(i, j, v[i]);
+        }
       }
     }
     __syncthreads();
-    constexpr int TR = TN / 8;  // threads a row, eight columns each
-    const int c = t % TR * 8, nv = a.N - n0 - c;
-    char* const out = static_cast<char*>(a.out) + 2 * ((size_t)m0 * a.N + n0 + c);
-    const int mv = min(TM, a.M - m0);
+    char* const out = static_cast<char*>(a.out) + 2 * ((size_t)m0 * a.N + n0 + tc);
 #pragma unroll 4
-    for (int m = t / TR; m < mv; m += NTH / TR) {
-      const uint4 v = *reinterpret_cast<const uint4*>(smem + m * P2 + 2 * c);
+    for (int m = tr; m < mv; m += NTH / TR) {
+      const uint4 v = *reinterpret_cast<const uint4*>(smem + m * P2 + 2 * tc);
       char* const o = out + 2 * (size_t)m * a.N;
       if (nv >= 8) {
         __builtin_memcpy(o, &v, 16);
@@ -617,7 +684,7 @@ done:
         }
 #pragma unroll
         for (int k = 0; k < RB; ++k) v[k] = cols.value(a, v[k], sx[k]);
-        activate(v, a.act);
+        activate<OUT>(v, a.act);
         if (a.res) {
 #pragma unroll
           for (int k = 0; k < RB; ++k) v[k] += res[k];
