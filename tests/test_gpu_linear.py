@@ -292,3 +292,34 @@ def test_activations_of_extreme_values(M, act, odt):
     assert np.array_equal(got[inf], want[inf])
     ok = ~nan & ~inf
     assert np.all(np.abs(got[ok] - want[ok]) <= tol[ok])
+
+
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("M,N,R", [(440, 30030, 30030), (440, 30030, 10010), (130, 30030, 7), (1001, 6006, 1), (190, 30030, 143)])
+def test_wide_tiles_with_residuals(M, N, R, dtype, odt):
+    """Residuals that repeat inside a tile's columns, of an odd width, and the
+    output's own memory; sums, bias and residual are exact before the one
+    rounding."""
+    import torch
+
+    from rejection_sampling_verify_09_amd import linear
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + N + R)
+    log(f"[linear wide residual] M={M} N={N} R={R} {dtype} -> {odt}")
+    x, w = grid(g, (M, 128), dtype), grid(g, (N, 128), dtype)
+    sx = sw = None
+    if dtype == "e4m3":
+        sx = torch.exp2(torch.randint(-3, 4, (M,), device="cuda", generator=g).float())
+        sw = torch.exp2(torch.randint(-3, 4, (N,), device="cuda", generator=g).float())
+    bias, res = grid(g, (N,), odt), grid(g, (M, R), odt)
+    want = x.float().cpu() @ w.float().cpu().T
+    if sx is not None:
+        want = want * sx.cpu()[:, None] * sw.cpu()
+    want = (want + bias.float().cpu() + res.float().cpu().repeat(1, N // R)).to(_t(odt))
+    out = linear(x, w, bias=bias, residual=res, x_scale=sx, weight_scale=sw, out_dtype=_t(odt))
+    assert torch.equal(out.cpu(), want)
+    if R == N:
+        linear(x, w, bias=bias, residual=res, x_scale=sx, weight_scale=sw, out_dtype=_t(odt), out=res)
+        assert torch.equal(res, out)
