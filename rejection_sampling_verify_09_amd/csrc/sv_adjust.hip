@@ -523,10 +523,11 @@ hipError_t launch_adjust(AdjArgs a, int32_t rows_per_seq, hipStream_t s) {
   const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(2048 / wgs, (rows_per_seq + 3) / 4));
   a.rgroup = (rows_per_seq + groups - 1) / groups;
   const dim3 grid((unsigned)wgs, (unsigned)((rows_per_seq + a.rgroup - 1) / a.rgroup));
-  // A slice among many has few of its sequence's biases, and room for few of
-  // them leaves the compute unit room for more workgroups (128 x 11 bfloat16
-  // rows of 24979 with 300 biases each: 45 us with room for 1024, 37 with 384).
-  a.bcap = a.nslices >= 8 ? 384 : 1024;
+  // Room for twice the biases that a slice has on average: less of it leaves
+  // the compute unit room for more workgroups (128 x 11 bfloat16 rows of 24979
+  // with 300 biases each: 45 us with room for 1024, 37 with 384).
+  const int64_t biases = 2 * (int64_t)a.nbias / wgs;
+  a.bcap = (int)std::min<int64_t>(1024, std::max<int64_t>(384, biases));
   const size_t S = (size_t)nt * ADJ_EPT;
   const bool table = a.rep || a.freq || a.pres || a.cub;
   const size_t lds = table ? S * 4 * (a.cub ? 2 : 1) + (a.cub ? (size_t)a.bcap * 12 : 0) + (inplace ? S * 2 : 0) : 0;
