@@ -156,13 +156,12 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
       for (int i = 1; i < nw; ++i) m = fmaxf(m, part[1][i]);
     }
     const float sc = r != r ? r : fmaxf(m / 448.0f, FLT_MIN);
-    const float inv = 1.0f / sc;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int j = (t + i * nt) * 8;
       if (j < a.d) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[i][k] *= inv;
+        for (int k = 0; k < 8; ++k) h[i][k] /= sc;  // a product with 1 / sc rounds once more, and moves values across ties
         store8<OUT, AL>(static_cast<char*>(a.out) + base + j, h[i], a.d - j);
       }
     }
