@@ -3,15 +3,18 @@
 // on the matrix cores, for bfloat16 operands or e4m3 operands with a float32
 // scale per row.  Products of two bfloat16 values are exact in float32 and are
 // summed in float32 (v_mfma_f32_16x16x32_bf16); the epilogue is float32 too,
-// rounded once.
+// rounded once.  e4m3 operands are read as such, converted to bfloat16 in
+// registers (exactly: 4 significant bits) and multiplied so.
 //
 // The 8-bit matrix instructions (v_mfma_f32_16x16x128_f8f6f4, twice the
-// bfloat16 rate) keep their accumulators in float32 but form the sums of a
-// few products with fewer bits: measured on normal values, 1.5e-5 of the
-// result (2-norm), whatever the length of the sum and with every 8-bit form.
-// That lies 100 times below the rounding of a bfloat16 output and is used
-// there; for a float32 output the operands are converted to bfloat16 (exactly:
-// 4 significant bits) and multiplied as such, which measures 8e-8.
+// bfloat16 rate) do not sum in float32: measured, of each run of eight
+// products along k they cut every one off, towards zero, below 2^-13 of the
+// largest one's power of two, and only then add to a float32 accumulator.  Next
+// to 448 x 448 a product of 7 is lost altogether, also where the large ones
+// cancel (2-norm of the error on normal values 1.5e-5 of the result, with
+// outlier columns 6e-5; so converted, 8e-8).  They are not used, and the
+// largest products take half again as long for it (448 x 128256 x 4096 to
+// bfloat16: 385 us, 235 with them).
 //
 // Two kernels: linear_rows_kernel for up to 16 rows, whose waves share k, and
 // linear_tile_kernel for more, and for many columns; pick_kernel chooses.  In both the weight is the matrix instruction's first operand, so
@@ -128,10 +131,8 @@ __device__ __forceinline__ bf16x8 widen8(uint2 v) {
   return __builtin_bit_cast(bf16x8, p);
 }
 
-// How the sums are formed: bfloat16 operands; e4m3 operands on the 8-bit
-// instructions (bfloat16 output); e4m3 operands widened to bfloat16 (float32
-// output).
-enum Mode : int { L_BF16 = 0, L_F8 = 1, L_F8W = 2 };
+// The operands: bfloat16, or e4m3 widened to bfloat16.
+enum Mode : int { L_BF16 = 0, L_F8 = 1 };
 
 typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
 
@@ -147,10 +148,7 @@ __device__ __forceinline__ i32x4 half(const Frag& f) {
 // Products of a (rows of the result) and NB fragments b (columns), added to c.
 template <int MODE, int NB>
 __device__ __forceinline__ void mma16(f32x4 (&c)[NB], const Frag& x, const Frag (&w)[NB]) {
-  if (MODE == L_F8) {
-#pragma unroll
-    for (int j = 0; j < NB; ++j) c[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[j], x, c[j], 0, 0, 0, 0, 0, 0);
-  } else if (MODE == L_BF16) {
+  if (MODE == L_BF16) {
 #pragma unroll
     for (int j = 0; j < NB; ++j)
       c[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, half<0>(w[j])), __builtin_bit_cast(bf16x8, half<0>(x)), c[j], 0, 0, 0);
@@ -385,17 +383,15 @@ constexpr int LIN_XCD = 8;  // XCDs the workgroup ids are dealt over
 // load: a fragment's own layout, 16 rows across neighbouring lanes, keeps the
 // address unit four times as long (64 against 16 cycles a load), which held
 // an earlier form with the weight straight in registers at 243 us where this
-// one takes 233 (448 x 128256 x 4096, e4m3 to bfloat16), and at 23.5 us where
-// this one takes 18 (333 x 5001 x 2112).
+// one took 233 (448 x 128256 x 4096, both on the 8-bit instructions), and at
+// 23.5 us where this one takes 18 (333 x 5001 x 2112).
 //
 // What bounds the largest tile (224 x 256, k blocks of 128 bytes, 8 waves, one
-// workgroup a compute unit): its rounds take about 1.4 us, 1.0 of them the
-// matrix instructions' at the clock they leave the chip, the rest LDS traffic
-// (112 KB of rows, 64 KB of weights read, 60 KB written a round) that overlaps
-// them in part; by the counters the matrix units are busy 53% of the whole time
-// and LDS 39%.  At 448 x 128256 x 4096: e4m3 to bfloat16 231 us (2.04 PFLOP/s),
-// bfloat16 427 (1.10), e4m3 to float32 381 (1.24); the library's products of
-// 8-bit and bfloat16 operands take 295 and 543.  The small tiles are bound by
+// workgroup a compute unit): the matrix instructions, and in part beside them
+// LDS traffic (112 KB of rows, 64 KB of weights read, 60 KB written a round).
+// At 448 x 128256 x 4096: e4m3 to bfloat16 383 us (1.23 PFLOP/s), to float32
+// 381 (1.24), bfloat16 427 (1.10); the library's product of bfloat16 operands
+// takes 543, that of 8-bit ones, on the 8-bit instructions, 295.  The small tiles are bound by
 // the latency of a round (loads, LDS, barrier: 0.7 us), of which 333 x 5001 x
 // 2112 has 17 (17.4 us; the library 22.8).
 template <int MODE, int OUT, int MB, int NB, int WM, int WN, int WK, int D>
@@ -852,6 +848,6 @@ extern "C" int sv_linear(const void* x, const void* weight, const float* x_scale
   hipStream_t s = (hipStream_t)stream;
   const hipError_t e = dtype == SV_BF16
                            ? (out_dtype == SV_F32 ? launch_linear<L_BF16, T_F32>(a, kernel, s) : launch_linear<L_BF16, T_BF16>(a, kernel, s))
-                           : (out_dtype == SV_F32 ? launch_linear<L_F8W, T_F32>(a, kernel, s) : launch_linear<L_F8, T_BF16>(a, kernel, s));
+                           : (out_dtype == SV_F32 ? launch_linear<L_F8, T_F32>(a, kernel, s) : launch_linear<L_F8, T_BF16>(a, kernel, s));
   return e == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
