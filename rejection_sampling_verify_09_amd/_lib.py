@@ -129,6 +129,23 @@ def _stream(stream) -> int:
     return getattr(stream, "cuda_stream", stream)
 
 
+def _new(stream, dev: int, make, *args, **kw) -> torch.Tensor:
+    """A new output, ``make(*args, **kw)``, that a kernel on ``stream`` (None: the current one) of device ``dev`` writes.
+
+    Its memory comes from that stream's own, since what the current stream has
+    freed it may still be reading; and it is kept for as long as work queued
+    on the current stream by the time it is freed may read it."""
+    if stream is None or _stream(stream) == torch._C._cuda_getCurrentRawStream(dev):
+        return make(*args, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        h = _stream(stream)
+        stream = torch.cuda.ExternalStream(h, device=dev) if h else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
 def spec_verify(target_logits: torch.Tensor, draft_logits: torch.Tensor | None, draft_tokens: torch.Tensor,
                 uniforms: torch.Tensor, temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0,
                 out_tokens: torch.Tensor | None = None, out_num_accepted: torch.Tensor | None = None,
@@ -453,13 +470,6 @@ def _int32(*sizes: int) -> None:
         raise ValueError(f"sizes must be nonnegative and fit 32 bits, got {', '.join(map(str, sizes))}")
 
 
-def _keep(t: torch.Tensor, stream) -> torch.Tensor:
-    """A new output, its memory kept until the work on ``stream`` is done."""
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream)))
-    return t
-
-
 def _stream_on(dev: int, name: str, stream) -> int:
     """The stream's handle for work on ``dev``, which must be the current device."""
     if dev < 0:
@@ -502,13 +512,13 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     xp = _arg(x, "x", x.dtype, x.shape, dev)
     s = _stream_on(dev, "x", stream)
     if out is None:
-        out = _keep(torch.empty_like(x, dtype=out_dtype), stream)  # half of torch.empty's time on the host
+        out = _new(stream, dev, torch.empty_like, x, dtype=out_dtype)  # half of torch.empty's time on the host
         op = out.data_ptr()
     if ocode == SV_E4M3 and out_scale is None:
-        out_scale = _keep(x.new_empty(x.shape[:-1], dtype=torch.float32), stream)
+        out_scale = _new(stream, dev, x.new_empty, x.shape[:-1], dtype=torch.float32)
         sp = out_scale.data_ptr()
     if residual is not None and out_residual is None:
-        out_residual = _keep(torch.empty_like(x), stream)
+        out_residual = _new(stream, dev, torch.empty_like, x)
         hp = out_residual.data_ptr()
     st = lib().sv_rms_norm(xp, rp, wp, float(eps), op, sp, hp, rows, d, code, ocode, s)
     if st != SV_OK:
@@ -555,7 +565,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     xp = _arg(x, "x", x.dtype, x.shape, dev)
     s = _stream_on(dev, "x", stream)
     if out is None:
-        out = _keep(x.new_empty(lead + (N,), dtype=out_dtype), stream)
+        out = _new(stream, dev, x.new_empty, lead + (N,), dtype=out_dtype)
         op = out.data_ptr()
     st = lib().sv_linear(xp, wp, xsp, wsp, bp, rp, op, M, N, K, R, ACTIVATIONS[activation], code, ocode, s)
     if st != SV_OK:
@@ -652,7 +662,7 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
     lp = _arg(logits, "logits", logits.dtype, logits.shape, dev)
     s = _stream_on(dev, "logits", stream)
     if out is None:
-        out = _keep(torch.empty_like(logits), stream)
+        out = _new(stream, dev, torch.empty_like, logits)
         op = out.data_ptr()
     if cu_num_draft is not None:
         st = lib().sv_adjust_logits_ragged(lp, op, hp, hl, pl, xp, cp, rp, fp, pp, cb, bt, bv, mp, mi, B, N, int(max_k),

@@ -1,0 +1,107 @@
+"""Calls with ``stream=``: their new outputs are written on that stream, whose
+work the current stream's is not ordered with, so they must not lie in memory
+that the current stream has freed and still reads, nor be handed out again
+while the current stream reads them."""
+import pytest
+
+from tests.harness import log
+
+pytestmark = pytest.mark.gpu
+
+
+def calls():
+    """name -> (call of the stream argument, bytes of its first output)."""
+    import torch
+
+    import rejection_sampling_verify_09_amd as sv
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    x = torch.randn((2048, 1024), device="cuda", generator=g).bfloat16()
+    w = torch.randn((1024,), device="cuda", generator=g).bfloat16()
+    wide = torch.randn((2048, 1024), device="cuda", generator=g).bfloat16()
+    pres = torch.full((2048,), 0.5, device="cuda")
+    return {
+        "rms_norm": (lambda s: sv.rms_norm(x, w, stream=s)[0], 2048 * 1024 * 2),
+        "linear": (lambda s: sv.linear(x, wide, stream=s), 2048 * 2048 * 2),
+        "adjust_logits": (lambda s: sv.adjust_logits(x, presence_penalty=pres, stream=s), 2048 * 1024 * 2),
+    }
+
+
+def busy(a, n=12):
+    """Some milliseconds of work on the current stream."""
+    for _ in range(n):
+        a = a @ a
+    return a
+
+
+@pytest.mark.parametrize("kind", ["stream", "handle", "default stream's handle"])
+@pytest.mark.parametrize("name", ["rms_norm", "linear", "adjust_logits"])
+def test_outputs_leave_memory_alone_that_the_current_stream_still_reads(name, kind):
+    import torch
+
+    log(f"[streams] {name}, {kind}")
+    call, nbytes = calls()[name]
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    # the stream the program works on, and the one the call is queued on
+    here = other if kind == "default stream's handle" else torch.cuda.current_stream()
+    there = {"stream": side, "handle": side.cuda_stream, "default stream's handle": 0}[kind]
+    want = call(None).clone()
+    mat = torch.eye(4096, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(here):
+        for _ in range(2):
+            held = torch.arange(nbytes // 4, device="cuda", dtype=torch.int32)
+            saved = held.clone()
+            here.synchronize()
+            at = held.data_ptr()
+            busy(mat)
+            copy = held.clone()  # queued behind the work
+            del held  # free again in this stream's memory, and not read yet
+            out = call(there)
+            assert out.data_ptr() != at
+            torch.cuda.synchronize()
+            assert torch.equal(copy, saved)
+            assert torch.equal(out, want)
+            del out
+
+
+@pytest.mark.parametrize("name", ["rms_norm", "linear", "adjust_logits"])
+def test_outputs_stay_until_the_current_stream_has_read_them(name):
+    import torch
+
+    log(f"[streams] {name}, read on the current stream")
+    call, nbytes = calls()[name]
+    side = torch.cuda.Stream()
+    want = call(None).clone()
+    mat = torch.eye(4096, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    for handle in (side, side.cuda_stream):
+        out = call(handle)
+        torch.cuda.current_stream().wait_stream(side)
+        busy(mat)
+        copy = out.clone()  # queued behind the work
+        del out
+        with torch.cuda.stream(side):  # would take the freed memory and write it at once
+            junk = [torch.full((nbytes // 4,), 7, device="cuda", dtype=torch.int32) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want)
+        del junk
+
+
+def test_a_round_given_a_stream():
+    """Every call of a round queued on a stream that is not the current one, the program's own tensor work as well."""
+    import torch
+
+    from tests.test_gpu_last_layer import Round, _flat, _same
+
+    log("[streams] a round on a given stream")
+    r = Round(seed=6)
+    want = _flat(r.run())
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        with torch.cuda.stream(side):
+            got = r.run(stream=handle)
+        torch.cuda.synchronize()
+        assert _same(_flat(got), want)
