@@ -146,6 +146,13 @@ def _new(stream, dev: int, make, *args, **kw) -> torch.Tensor:
     return t
 
 
+def _empty(stream, shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """torch.empty of an output that a kernel on ``stream`` writes."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _new(stream, device.index, torch.empty, shape, dtype=dtype, device=device)
+
+
 def spec_verify(target_logits: torch.Tensor, draft_logits: torch.Tensor | None, draft_tokens: torch.Tensor,
                 uniforms: torch.Tensor, temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0,
                 out_tokens: torch.Tensor | None = None, out_num_accepted: torch.Tensor | None = None,
@@ -179,16 +186,16 @@ def spec_verify(target_logits: torch.Tensor, draft_logits: torch.Tensor | None, 
     xp = _dev(draft_tokens, "draft_tokens", torch.int32) if K > 0 else None
     up = _dev(uniforms, "uniforms", torch.float32)
     if out_tokens is None:
-        out_tokens = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
+        out_tokens = _empty(stream, (B, K + 1), dtype=torch.int32, device=dev)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+        out_num_accepted = _empty(stream, (B,), dtype=torch.int32, device=dev)
     op = _dev(out_tokens, "out_tokens", torch.int32)
     onp = _dev(out_num_accepted, "out_num_accepted", torch.int32)
     s = _stream(stream)
     if draft_temperature is not None:
-        out_p = torch.empty((B, K), dtype=torch.float64, device=dev) if debug else None
-        out_q = torch.empty((B, K), dtype=torch.float64, device=dev) if debug else None
-        out_z = torch.empty((B,), dtype=torch.float64, device=dev) if debug else None
+        out_p = _empty(stream, (B, K), dtype=torch.float64, device=dev) if debug else None
+        out_q = _empty(stream, (B, K), dtype=torch.float64, device=dev) if debug else None
+        out_z = _empty(stream, (B,), dtype=torch.float64, device=dev) if debug else None
         st = lib().sv_spec_verify_dt(tp, dp, xp, up, float(temperature), float(draft_temperature), int(top_k),
                                      float(top_p), op, onp,
                                      out_p.data_ptr() if debug and K > 0 else None,
@@ -200,9 +207,9 @@ def spec_verify(target_logits: torch.Tensor, draft_logits: torch.Tensor | None, 
             return out_tokens, out_num_accepted, dict(p=out_p, q=out_q, z=out_z)
         return out_tokens, out_num_accepted
     if debug:
-        out_p = torch.empty((B, K), dtype=torch.float64, device=dev)
-        out_q = torch.empty((B, K), dtype=torch.float64, device=dev)
-        out_z = torch.empty((B,), dtype=torch.float64, device=dev)
+        out_p = _empty(stream, (B, K), dtype=torch.float64, device=dev)
+        out_q = _empty(stream, (B, K), dtype=torch.float64, device=dev)
+        out_z = _empty(stream, (B,), dtype=torch.float64, device=dev)
         st = lib().sv_spec_verify_debug(tp, dp, xp, up, float(temperature), int(top_k), float(top_p), op, onp,
                                         out_p.data_ptr() if K > 0 else None, out_q.data_ptr() if K > 0 else None,
                                         out_z.data_ptr(), B, K, V, code, s)
@@ -243,9 +250,9 @@ def spec_verify_noalloc(target_logits: torch.Tensor, draft_logits: torch.Tensor 
     xp = _dev(draft_tokens, "draft_tokens", torch.int32) if K > 0 else None
     up = _dev(uniforms, "uniforms", torch.float32)
     if out_tokens is None:
-        out_tokens = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
+        out_tokens = _empty(stream, (B, K + 1), dtype=torch.int32, device=dev)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+        out_num_accepted = _empty(stream, (B,), dtype=torch.int32, device=dev)
     st = lib().sv_spec_verify_noalloc(tp, dp, xp, up, float(temperature), int(top_k), float(top_p),
                                       _dev(out_tokens, "out_tokens", torch.int32),
                                       _dev(out_num_accepted, "out_num_accepted", torch.int32), B, K, V, code,
@@ -293,14 +300,14 @@ def spec_verify_ragged(target_logits: torch.Tensor, draft_logits: torch.Tensor |
     up = _dev(uniforms, "uniforms", torch.float32)
     cp = _dev(cu_num_draft, "cu_num_draft", torch.int32)
     if out_tokens is None:
-        out_tokens = torch.empty((B, int(max_k) + 1), dtype=torch.int32, device=dev)
+        out_tokens = _empty(stream, (B, int(max_k) + 1), dtype=torch.int32, device=dev)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+        out_num_accepted = _empty(stream, (B,), dtype=torch.int32, device=dev)
     if tuple(out_tokens.shape) != (B, int(max_k) + 1):
         raise ValueError("out_tokens must be [B, max_k + 1]")
-    out_p = torch.empty((N,), dtype=torch.float64, device=dev) if debug else None
-    out_q = torch.empty((N,), dtype=torch.float64, device=dev) if debug else None
-    out_z = torch.empty((B,), dtype=torch.float64, device=dev) if debug else None
+    out_p = _empty(stream, (N,), dtype=torch.float64, device=dev) if debug else None
+    out_q = _empty(stream, (N,), dtype=torch.float64, device=dev) if debug else None
+    out_z = _empty(stream, (B,), dtype=torch.float64, device=dev) if debug else None
     Td = float(temperature) if draft_temperature is None else float(draft_temperature)
     st = lib().sv_spec_verify_ragged(tp, dp, xp, up, cp, float(temperature), Td, int(top_k), float(top_p),
                                      _dev(out_tokens, "out_tokens", torch.int32),
@@ -344,12 +351,12 @@ def spec_verify_probs(target_logits: torch.Tensor, draft_probs: torch.Tensor | N
     xp = _dev(draft_tokens, "draft_tokens", torch.int32) if K > 0 else None
     up = _dev(uniforms, "uniforms", torch.float32)
     if out_tokens is None:
-        out_tokens = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
+        out_tokens = _empty(stream, (B, K + 1), dtype=torch.int32, device=dev)
     if out_num_accepted is None:
-        out_num_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
-    out_p = torch.empty((B, K), dtype=torch.float64, device=dev) if debug else None
-    out_q = torch.empty((B, K), dtype=torch.float64, device=dev) if debug else None
-    out_z = torch.empty((B,), dtype=torch.float64, device=dev) if debug else None
+        out_num_accepted = _empty(stream, (B,), dtype=torch.int32, device=dev)
+    out_p = _empty(stream, (B, K), dtype=torch.float64, device=dev) if debug else None
+    out_q = _empty(stream, (B, K), dtype=torch.float64, device=dev) if debug else None
+    out_z = _empty(stream, (B,), dtype=torch.float64, device=dev) if debug else None
     st = lib().sv_spec_verify_probs(_dev(target_logits, "target_logits"), qp, xp, up, float(temperature), int(top_k),
                                     float(top_p), _dev(out_tokens, "out_tokens", torch.int32),
                                     _dev(out_num_accepted, "out_num_accepted", torch.int32),
@@ -374,7 +381,7 @@ def lm_logits(hidden: torch.Tensor, weight: torch.Tensor, out: torch.Tensor | No
     M = hidden.numel() // d if d > 0 else 0
     shape = tuple(hidden.shape[:-1]) + (V,)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=hidden.device)
+        out = _empty(stream, shape, dtype=torch.float32, device=hidden.device)
     elif tuple(out.shape) != shape:
         raise ValueError(f"out must be {shape}")
     st = lib().sv_lm_logits(_dev(hidden, "hidden"), _dev(weight, "weight"), _dev(out, "out", torch.float32), M, V, d,
@@ -420,11 +427,11 @@ def spec_verify_lmhead(hidden_target: torch.Tensor, weight_target: torch.Tensor,
         raise ValueError("draft_tokens must be [B, K] and uniforms [B, K+1]")
     xp = _dev(draft_tokens, "draft_tokens", torch.int32) if K > 0 else None
     up = _dev(uniforms, "uniforms", torch.float32)
-    out_tokens = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
-    out_n = torch.empty((B,), dtype=torch.int32, device=dev)
-    out_p = torch.empty((B, K), dtype=torch.float64, device=dev) if debug else None
-    out_q = torch.empty((B, K), dtype=torch.float64, device=dev) if debug else None
-    out_z = torch.empty((B,), dtype=torch.float64, device=dev) if debug else None
+    out_tokens = _empty(stream, (B, K + 1), dtype=torch.int32, device=dev)
+    out_n = _empty(stream, (B,), dtype=torch.int32, device=dev)
+    out_p = _empty(stream, (B, K), dtype=torch.float64, device=dev) if debug else None
+    out_q = _empty(stream, (B, K), dtype=torch.float64, device=dev) if debug else None
+    out_z = _empty(stream, (B,), dtype=torch.float64, device=dev) if debug else None
     st = lib().sv_spec_verify_lmhead(_dev(hidden_target, "hidden_target"), _dev(weight_target, "weight_target"), hd, wd,
                                      xp, up, float(temperature), int(top_k), float(top_p), out_tokens.data_ptr(),
                                      out_n.data_ptr(), out_p.data_ptr() if debug and K > 0 else None,
@@ -729,7 +736,7 @@ def filtered_probs(logits: torch.Tensor, temperature: float, top_k: int = 0, top
     rows, V = logits.shape
     code = _dtype_code(logits)
     if out is None:
-        out = torch.empty((rows, V), dtype=torch.float32, device=logits.device)
+        out = _empty(stream, (rows, V), dtype=torch.float32, device=logits.device)
     st = lib().sv_filtered_probs(_dev(logits, "logits"), rows, V, code, float(temperature), int(top_k),
                                  float(top_p), _dev(out, "out", torch.float32), _stream(stream))
     if st != SV_OK:
@@ -751,9 +758,9 @@ def sample(logits: torch.Tensor, uniforms: torch.Tensor, temperature: float = 1.
         raise ValueError("uniforms must be [rows]")
     dev = logits.device
     if out_tokens is None:
-        out_tokens = torch.empty((rows,), dtype=torch.int32, device=dev)
+        out_tokens = _empty(stream, (rows,), dtype=torch.int32, device=dev)
     if with_prob and out_prob is None:
-        out_prob = torch.empty((rows,), dtype=torch.float64, device=dev)
+        out_prob = _empty(stream, (rows,), dtype=torch.float64, device=dev)
     pp = _dev(out_prob, "out_prob", torch.float64) if with_prob else None
     st = lib().sv_sample(_dev(logits, "logits"), _dev(uniforms, "uniforms", torch.float32), float(temperature),
                          int(top_k), float(top_p), _dev(out_tokens, "out_tokens", torch.int32), pp, rows, V, code,
@@ -775,7 +782,7 @@ def read_floor(data: torch.Tensor, key: int = 0, out: torch.Tensor | None = None
     nbytes = data.numel() * data.element_size()
     nblk = max(1, -(-nbytes // READ_BLOCK))
     if out is None:
-        out = torch.zeros((nblk,), dtype=torch.int32, device=data.device)
+        out = _new(stream, data.get_device(), torch.zeros, (nblk,), dtype=torch.int32, device=data.device)
     if out.dtype != torch.int32 or not out.is_cuda or out.numel() < nblk:
         raise ValueError("out must be an int32 device tensor of one word per 16 KiB block")
     st = lib().sv_read_floor(ctypes.c_void_p(data.data_ptr()), nbytes, int(key) & 0xFFFFFFFF,

@@ -25,7 +25,43 @@ def calls():
         "rms_norm": (lambda s: sv.rms_norm(x, w, stream=s)[0], 2048 * 1024 * 2),
         "linear": (lambda s: sv.linear(x, wide, stream=s), 2048 * 2048 * 2),
         "adjust_logits": (lambda s: sv.adjust_logits(x, presence_penalty=pres, stream=s), 2048 * 1024 * 2),
+        **verification(g),
     }
+
+
+def verification(g):
+    import torch
+
+    import rejection_sampling_verify_09_amd as sv
+
+    B, K, V, d = 640, 3, 1000, 128
+    rnd = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+    tl, dl = rnd(B, K + 1, V), rnd(B, K, V)
+    x = torch.randint(0, V, (B, K), device="cuda", generator=g, dtype=torch.int32)
+    u = torch.rand((B, K + 1), device="cuda", generator=g)
+    q = torch.softmax(dl, 2)
+    cu = torch.arange(0, (B + 1) * K, K, device="cuda", dtype=torch.int32)
+    h, hd, w = rnd(B, K + 1, d).bfloat16(), rnd(B, K, d).bfloat16(), rnd(V, d).bfloat16()
+    rows, words = tl.view(-1, V), torch.arange(1 << 20, device="cuda", dtype=torch.int32)
+    tokens = B * (K + 1) * 4
+    return {
+        "spec_verify": (lambda s: sv.spec_verify(tl, dl, x, u, stream=s)[0], tokens),
+        "spec_verify debug": (lambda s: sv.spec_verify(tl, dl, x, u, stream=s, debug=True)[2]["p"], B * K * 8),
+        "spec_verify_noalloc": (lambda s: sv.spec_verify_noalloc(tl[:64], dl[:64], x[:64], u[:64], stream=s)[0], 1024),
+        "spec_verify_ragged": (lambda s: sv.spec_verify_ragged(rows, dl.view(-1, V), x.view(-1), u.view(-1), cu, K,
+                                                               stream=s)[0], tokens),
+        "spec_verify_probs": (lambda s: sv.spec_verify_probs(tl, q, x, u, stream=s)[0], tokens),
+        "spec_verify_lmhead": (lambda s: sv.spec_verify_lmhead(h, w, hd, w, x, u, stream=s)[0], tokens),
+        "lm_logits": (lambda s: sv.lm_logits(h, w, stream=s), B * (K + 1) * V * 4),
+        "filtered_probs": (lambda s: sv.filtered_probs(rows, 0.8, stream=s), B * (K + 1) * V * 4),
+        "sample": (lambda s: sv.sample(rows, u.view(-1), stream=s)[0], tokens),
+        "read_floor": (lambda s: sv.read_floor(words, stream=s), 1024),
+    }
+
+
+NAMES = ["rms_norm", "linear", "adjust_logits", "spec_verify", "spec_verify debug", "spec_verify_noalloc",
+         "spec_verify_ragged", "spec_verify_probs", "spec_verify_lmhead", "lm_logits", "filtered_probs", "sample",
+         "read_floor"]
 
 
 def busy(a, n=12):
@@ -36,7 +72,7 @@ def busy(a, n=12):
 
 
 @pytest.mark.parametrize("kind", ["stream", "handle", "default stream's handle"])
-@pytest.mark.parametrize("name", ["rms_norm", "linear", "adjust_logits"])
+@pytest.mark.parametrize("name", NAMES)
 def test_outputs_leave_memory_alone_that_the_current_stream_still_reads(name, kind):
     import torch
 
@@ -66,7 +102,7 @@ def test_outputs_leave_memory_alone_that_the_current_stream_still_reads(name, ki
             del out
 
 
-@pytest.mark.parametrize("name", ["rms_norm", "linear", "adjust_logits"])
+@pytest.mark.parametrize("name", NAMES)
 def test_outputs_stay_until_the_current_stream_has_read_them(name):
     import torch
 
