@@ -438,9 +438,9 @@ int sv_spec_verify_lmhead(const void* hidden_target, const void* weight_target,
  * rows take the vectorised path.  A row whose sum of squares is not finite in
  * float32 (one that holds a NaN or an infinity, for one) comes out all NaN, its
  * scale too.  1 <= d <= SV_MAX_NORM_D, and rows * min(1024, d / 8 in whole
- * waves) threads within one launch (else SV_ERR_SHAPE).  rows == 0 does
- * nothing.  Nothing is allocated and no scratch is used, so calls on any
- * streams may overlap and be captured.
+ * waves) threads within one launch, the rows in whole fours where d <= 512
+ * (else SV_ERR_SHAPE).  rows == 0 does nothing.  Nothing is allocated and no
+ * scratch is used, so calls on any streams may overlap and be captured.
  */
 int sv_rms_norm(const void* x, const void* residual, const void* weight, float eps, void* out, float* out_scale,
                 void* out_residual, int32_t rows, int32_t d, int32_t dtype, int32_t out_dtype, void* stream);

@@ -169,18 +169,28 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
   }
 }
 
+// As many threads a row as it has runs of 8, up to 1024: on 16384 x 8192
+// bfloat16 rows with a residual 1, 2, 4 and 8 runs a thread take 179, 183, 195
+// and 212 us (the wider a workgroup, the sooner a row's loads are all in
+// flight); rows up to 4096 do not tell them apart.  The rows of one wave go
+// four to a workgroup.
+struct NormLaunch {
+  int nt, ny, vpt;  // threads a row, rows a workgroup, runs a thread
+  int64_t wgs;
+  NormLaunch(int64_t rows, int d) {
+    const int nv = (d + 7) / 8;
+    nt = std::min(1024, (nv + 63) / 64 * 64);
+    ny = nt == 64 ? 4 : 1;
+    vpt = (nv + nt - 1) / nt;
+    wgs = (rows + ny - 1) / ny;
+  }
+};
+
 template <int IN, int OUT, bool AL>
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
-  // As many threads a row as it has runs of 8, up to 1024: on 16384 x 8192
-  // bfloat16 rows with a residual 1, 2, 4 and 8 runs a thread take 179, 183,
-  // 195 and 212 us (the wider a workgroup, the sooner a row's loads are all in
-  // flight); rows up to 4096 do not tell them apart.  The rows of one wave go
-  // four to a workgroup.
-  const int nv = (a.d + 7) / 8;
-  const int nt = std::min(1024, (nv + 63) / 64 * 64);
-  const int ny = nt == 64 ? 4 : 1;
-  const int vpt = (nv + nt - 1) / nt;
-  const dim3 grid((unsigned)((a.rows + ny - 1) / ny)), wg((unsigned)nt, (unsigned)ny);
+  const NormLaunch l(a.rows, a.d);
+  const int vpt = l.vpt;
+  const dim3 grid((unsigned)l.wgs), wg((unsigned)l.nt, (unsigned)l.ny);
   if (vpt == 1)
     hipLaunchKernelGGL((rms_norm_kernel<IN, OUT, 1, AL>), grid, wg, 0, s, a);
   else if (vpt == 2)
@@ -217,7 +227,8 @@ extern "C" int sv_rms_norm(const void* x, const void* residual, const void* weig
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
   if (out_dtype != SV_F32 && out_dtype != SV_BF16 && out_dtype != SV_E4M3) return SV_ERR_DTYPE;
   if (!(eps > 0.0f) || !std::isfinite(eps)) return SV_ERR_PARAM;
-  if ((int64_t)rows * std::min(1024, (d + 511) / 512 * 64) > kGridThreads) return SV_ERR_SHAPE;
+  const NormLaunch l(rows, d);
+  if (l.wgs * l.nt * l.ny > kGridThreads) return SV_ERR_SHAPE;
   if (rows == 0) return SV_OK;
   if (!x || !weight || !out || (out_dtype == SV_E4M3 && !out_scale) || (out_residual && !residual)) return SV_ERR_NULL;
   const size_t ie = (size_t)type_bytes(dtype), n = (size_t)rows * (size_t)d;
