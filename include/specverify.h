@@ -491,11 +491,11 @@ int sv_linear(const void* x, const void* weight, const float* x_scale, const flo
  *   l = l > 0 ? l / repetition : l * repetition   if c_j > 0 or j is in the
  *                                                 prompt
  *   l = l - (frequency * c_j + presence)          if c_j > 0
- *   l = l + every bias listed for j, in its order
+ *   l = l + (the biases listed for j, added to each other in their order)
  *   l = -inf                                      if the row's mask forbids j
  * in float32 (l / repetition as a product with the rounded reciprocal), rounded
- * once.  Logits that none of these touches keep their
- * bits.  Row i of a sequence has s = drafts_seen + i.
+ * once.  Logits that none of these touches keep their bits.  Row i of a
+ * sequence has s = drafts_seen + i.
  *
  * logits       [B, R, V] dtype (SV_F32 or SV_BF16), device; at most 2^30 rows
  * out_logits   the same shape and type, device; may be logits itself (in
@@ -525,8 +525,9 @@ int sv_linear(const void* x, const void* weight, const float* x_scale, const flo
  * without a distribution.  Target rows of a round: R = K + 1, drafts_seen 0;
  * its draft rows: R = K, drafts_seen 0; one row while drafting token i: R = 1,
  * drafts_seen = i.  K <= SV_MAX_K, drafts_seen + R - 1 <= K unless K == 0 (then
- * drafts_seen is 0), history_cap <= SV_MAX_HISTORY (else SV_ERR_SHAPE).  Overlap of out_logits with anything but
- * logits itself is SV_ERR_PARAM.  Nothing is allocated and no scratch is used.
+ * drafts_seen is 0), history_cap <= SV_MAX_HISTORY (else SV_ERR_SHAPE).  Overlap
+ * of out_logits with anything but logits itself is SV_ERR_PARAM.  Nothing is
+ * allocated and no scratch is used.
  */
 int sv_adjust_logits(const void* logits, void* out_logits, const int32_t* history, const int32_t* history_len,
                      const int32_t* prompt_len, const int32_t* draft_tokens, const float* repetition,

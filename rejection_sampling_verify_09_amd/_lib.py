@@ -599,7 +599,8 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
     (0 by default): the prompt, then the tokens accepted so far.
     repetition_penalty (prompt, history and drafts), frequency_penalty and
     presence_penalty (history behind the prompt, and drafts): [B] float32.
-    bias: (cu_bias [B + 1] int32, tokens int32, values float32).  mask
+    bias: (cu_bias [B + 1] int32, tokens int32, values float32), several of
+    one token added to each other first, in their order.  mask
     [mask_rows, ceil(V / 32)] int32, bit j % 32 of word j / 32 set where token j
     is allowed; mask_index [rows] int32, each row's row of mask (outside of it:
     not masked).  Returns out; out=logits adjusts in place."""

@@ -5,7 +5,7 @@
 //   l = logit_j
 //   l = l / rep (l > 0) or l * rep        if c_j > 0 or j is in the prompt
 //   l = l - (freq c_j + pres)             if c_j > 0
-//   l = l + the sum of j's biases
+//   l = l + the sum of j's biases, which are added to each other in their order
 //   l = -inf                              if the row's mask forbids j
 // in float32, rounded once to the logits' type.
 //
