@@ -249,12 +249,14 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
     masks(m, r0);
     fetch(r0);
   }
-  // the biases' tokens and values: a thread's first in registers
-  int i0 = 0, i1 = 0, btok0 = 0;
+  // the biases' tokens and values: a thread's first in registers (positions
+  // unsigned: a few past the last one are formed, which 32 bits hold then)
+  uint32_t i0 = 0, i1 = 0;
+  int btok0 = 0;
   float bval0 = 0.0f;
   if (a.cub) {
-    i0 = min(max(a.cub[b], 0), a.nbias);
-    i1 = min(a.cub[b + 1], a.nbias);
+    i0 = (uint32_t)min(max(a.cub[b], 0), a.nbias);
+    i1 = (uint32_t)min(max(a.cub[b + 1], 0), a.nbias);
     if (i0 + t < i1) {
       btok0 = a.btok[i0 + t];
       bval0 = a.bval[i0 + t];
@@ -312,12 +314,12 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   if (a.cub) {
     // several biases of one token are added in the order they are listed, by
     // the thread that holds the first or, of a chain, its head
-    for (int i = i0 + t; i < i1; i += nt) {
+    for (uint32_t i = i0 + t; i < i1; i += nt) {
       const uint32_t j = (uint32_t)(i == i0 + t ? btok0 : a.btok[i]) - (uint32_t)v0;
       if (j >= (uint32_t)vn) continue;
       const int p = atomicAdd(&nbiased, 1);
       if (p < a.bcap) {
-        bidx[p] = i;
+        bidx[p] = (int32_t)i;
         btoks[p] = (uint16_t)j;
         bvals[p] = i == i0 + t ? bval0 : a.bval[i];
         bnext[p] = (uint16_t)atomicExch(&bt[j], (uint32_t)p);
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
               last = low;
             }
           } else {
-            for (int k = i0; k < i1; ++k)
+            for (uint32_t k = i0; k < i1; ++k)
               if (a.btok[k] == v0 + j) {
                 v = any ? v + a.bval[k] : a.bval[k];
                 any = true;
@@ -365,28 +367,28 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
       // too many: bt first takes the index of each token's first
       for (int i = t; i < S; i += nt) bt[i] = ~0u;
       __syncthreads();
-      for (int i = i0 + t; i < i1; i += nt) {
+      for (uint32_t i = i0 + t; i < i1; i += nt) {
         const uint32_t j = (uint32_t)a.btok[i] - (uint32_t)v0;
         if (j >= (uint32_t)vn) continue;
-        atomicMin(&bt[j], (uint32_t)i);
+        atomicMin(&bt[j], i);
         touch(j, atomicOr(&tab[j], E_BIAS));
       }
       __syncthreads();
-      for (int i = i0 + t; i < i1; i += nt) {
+      for (uint32_t i = i0 + t; i < i1; i += nt) {
         const uint32_t j = (uint32_t)a.btok[i] - (uint32_t)v0;
-        if (j < (uint32_t)vn && bt[j] != (uint32_t)i) atomicOr(&tab[j], E_BIASES);
+        if (j < (uint32_t)vn && bt[j] != i) atomicOr(&tab[j], E_BIASES);
       }
       __syncthreads();
-      for (int i = i0 + t; i < i1; i += nt) {
+      for (uint32_t i = i0 + t; i < i1; i += nt) {
         const int32_t tok = a.btok[i];
         const uint32_t j = (uint32_t)tok - (uint32_t)v0;
         if (j >= (uint32_t)vn) continue;
         float v = a.bval[i];
         if (tab[j] & E_BIASES) {
           bool first = true;
-          for (int k = i0; k < i && first; ++k) first = a.btok[k] != tok;
+          for (uint32_t k = i0; k < i && first; ++k) first = a.btok[k] != tok;
           if (!first) continue;
-          for (int k = i + 1; k < i1; ++k)
+          for (uint32_t k = i + 1; k < i1; ++k)
             if (a.btok[k] == tok) v += a.bval[k];
         }
         bt[j] = __float_as_uint(v);  // its index is not looked at any more

@@ -41,3 +41,26 @@ def test_biases_are_added_to_each_other_before_the_logit(n):
         want = np.full((2, V), 1e8, dtype=np.float32)
         want[0, 123] = np.float32(1e8) + total
         assert want[0, 123] >= np.float32(1e8) + 8 and np.array_equal(got, want)
+
+
+def test_biases_at_the_end_of_the_longest_list():
+    """Offsets next to 2^31, where positions a few past the last bias do not fit a signed number; all but the last
+    60 entries of the list are in no sequence."""
+    import torch
+
+    from rejection_sampling_verify_09_amd import adjust_logits
+
+    n, V, m = (1 << 31) - 1, 3000, 60
+    log(f"[adjust] the last {m} of {n} biases")
+    tok = torch.empty((n,), device="cuda", dtype=torch.int32)
+    val = torch.empty((n,), device="cuda", dtype=torch.float32)
+    g = np.random.default_rng(3)
+    t, v = g.integers(-1, 40, m).astype(np.int32) * 71, g.standard_normal(m).astype(np.float32)
+    tok[-m:], val[-m:] = cuda(t), cuda(v)
+    cu = torch.tensor([n - m, n - m + 20, n], device="cuda", dtype=torch.int32)
+    lg = torch.zeros((2, V), device="cuda")
+    for out in (None, lg):
+        got = adjust_logits(lg, bias=(cu, tok, val), out=out).cpu().numpy()
+        for b, s in enumerate((slice(0, 20), slice(20, m))):
+            ok = t[s] >= 0
+            assert np.array_equal(got[b], summed(t[s][ok], v[s][ok], V)[0]), b
