@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   uint16_t* list = a.cub ? bnext + a.bcap : reinterpret_cast<uint16_t*>(smem + S);  // [S] in place: tokens of nonzero entries
   __shared__ int32_t xs[MAX_K];                                   // the sequence's drafts,
   __shared__ uint64_t same[MAX_K];                                // and which of them are the same token
-  __shared__ int32_t nlist, nbiased;
+  __shared__ int32_t nlist, nbiased, nordered;
+  __shared__ int32_t wcount[ADJ_MAX_WG / 64];
   const int b = blockIdx.x / a.nslices, sl = blockIdx.x - b * a.nslices;
   const int v0 = sl * S, vn = min(S, a.V - v0);
   constexpr int EB = DT == T_F32 ? 4 : 2;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
       reinterpret_cast<uint4*>(tab)[i] = make_uint4(0u, 0u, 0u, 0u);
       if (a.cub) reinterpret_cast<uint4*>(bt)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
     }
-    if (t == 0) nlist = nbiased = 0;
+    if (t == 0) nlist = nbiased = nordered = 0;
     __syncthreads();
   }
   // every entry becomes nonzero once, by whichever operation comes first: that thread lists the token
@@ -313,7 +314,8 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   }
   if (a.cub) {
     // several biases of one token are added in the order they are listed, by
-    // the thread that holds the first or, of a chain, its head
+    // the thread that holds the first or, of a chain, its head; those of
+    // E_BIASES tokens by a walk through the list
     for (uint32_t i = i0 + t; i < i1; i += nt) {
       const uint32_t j = (uint32_t)(i == i0 + t ? btok0 : a.btok[i]) - (uint32_t)v0;
       if (j >= (uint32_t)vn) continue;
@@ -329,8 +331,8 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
     const int nb = nbiased;
     if (nb <= a.bcap) {
       // the slice's biases in LDS, each token's chained, both in any order:
-      // a chain's head takes the lowest index left until none is (or, of a
-      // long chain, looks through the list in order)
+      // a chain's head takes the lowest index left until none is, or leaves a
+      // long chain to the walk
       uint32_t head = 0;
       for (int p = t, c = 0; p < nb; p += nt, ++c)
         if (bt[btoks[p]] == (uint32_t)p) head |= 1u << c;
@@ -339,11 +341,13 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
         if (!((head >> c) & 1)) continue;
         const int j = btoks[p];
         float v = bvals[p];
+        uint32_t bits = E_BIAS;
         if (bnext[p] != NONE) {
+          constexpr int LONG = 17;
           int len = 0;
-          for (int k = p; k != NONE; k = bnext[k]) ++len;
+          for (int k = p; k != NONE && len < LONG; k = bnext[k]) ++len;
           bool any = false;
-          if (len <= 16) {
+          if (len < LONG) {
             for (int q = 0, last = -1; q < len; ++q) {
               int low = INT32_MAX, at = p;
               for (int k = p; k != NONE; k = bnext[k])
@@ -353,15 +357,12 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
               last = low;
             }
           } else {
-            for (uint32_t k = i0; k < i1; ++k)
-              if (a.btok[k] == v0 + j) {
-                v = any ? v + a.bval[k] : a.bval[k];
-                any = true;
-              }
+            bits |= E_BIASES;
+            nordered = 1;
           }
         }
         bt[j] = __float_as_uint(v);
-        touch(j, atomicOr(&tab[j], E_BIAS));
+        touch(j, atomicOr(&tab[j], bits));
       }
     } else {
       // too many: bt first takes the index of each token's first
@@ -376,26 +377,60 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
       __syncthreads();
       for (uint32_t i = i0 + t; i < i1; i += nt) {
         const uint32_t j = (uint32_t)a.btok[i] - (uint32_t)v0;
-        if (j < (uint32_t)vn && bt[j] != i) atomicOr(&tab[j], E_BIASES);
+        if (j < (uint32_t)vn && bt[j] != i) {
+          atomicOr(&tab[j], E_BIASES);
+          nordered = 1;
+        }
       }
       __syncthreads();
       for (uint32_t i = i0 + t; i < i1; i += nt) {
-        const int32_t tok = a.btok[i];
-        const uint32_t j = (uint32_t)tok - (uint32_t)v0;
-        if (j >= (uint32_t)vn) continue;
-        float v = a.bval[i];
-        if (tab[j] & E_BIASES) {
-          bool first = true;
-          for (uint32_t k = i0; k < i && first; ++k) first = a.btok[k] != tok;
-          if (!first) continue;
-          for (uint32_t k = i + 1; k < i1; ++k)
-            if (a.btok[k] == tok) v += a.bval[k];
-        }
-        bt[j] = __float_as_uint(v);  // its index is not looked at any more
+        const uint32_t j = (uint32_t)a.btok[i] - (uint32_t)v0;
+        if (j < (uint32_t)vn && !(tab[j] & E_BIASES)) bt[j] = __float_as_uint(a.bval[i]);
       }
     }
+    __syncthreads();
+    if (nordered) {
+      // The walk: of each piece of the list the E_BIASES tokens' entries are
+      // brought together, in order, and every thread adds those of its 8
+      // tokens.  Time grows with the list's length alone, however often a
+      // token is in it.
+      const int piece = min(nt, a.bcap);
+      uint32_t begun = 0;  // which of the thread's tokens have a sum
+      for (uint32_t base = i0; base < i1; base += piece) {
+        const uint32_t i = base + t;
+        uint32_t j = 0;
+        bool mine = false;
+        if (t < piece && i < i1) {
+          j = (uint32_t)a.btok[i] - (uint32_t)v0;
+          mine = j < (uint32_t)vn && (tab[j] & E_BIASES);
+        }
+        const uint64_t m = __ballot(mine);
+        if ((t & 63) == 0) wcount[t >> 6] = __popcll(m);
+        __syncthreads();
+        int at = __popcll(m & ((1ull << (t & 63)) - 1)), total = 0;
+        for (int w = 0; w < nt >> 6; ++w) {
+          const int c = wcount[w];
+          at += w < t >> 6 ? c : 0;
+          total += c;
+        }
+        if (mine) {
+          btoks[at] = (uint16_t)j;
+          bvals[at] = a.bval[i];
+        }
+        __syncthreads();
+        for (int p = 0; p < total; ++p) {
+          const int q = btoks[p];
+          if (q / ADJ_EPT != t) continue;
+          const uint32_t bit = 1u << q % ADJ_EPT;
+          bt[q] = __float_as_uint(begun & bit ? __uint_as_float(bt[q]) + bvals[p] : bvals[p]);
+          begun |= bit;
+        }
+        __syncthreads();  // the next piece takes its place
+      }
+    }
+  } else if (table) {
+    __syncthreads();
   }
-  if (table) __syncthreads();
 
   const bool biased = a.cub != nullptr;
   // a token's logit in a row that has seen the drafts in `seen`: table entry e, bias w

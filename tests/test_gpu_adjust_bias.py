@@ -64,3 +64,69 @@ def test_biases_at_the_end_of_the_longest_list():
         for b, s in enumerate((slice(0, 20), slice(20, m))):
             ok = t[s] >= 0
             assert np.array_equal(got[b], summed(t[s][ok], v[s][ok], V)[0]), b
+
+
+def many(kind, n, V, g):
+    """Token lists of n biases of one sequence."""
+    if kind == "two tokens, one behind the other":
+        return np.repeat(np.array([5, 900], dtype=np.int32), n // 2)
+    if kind == "every token twice, far apart":
+        one = g.permutation(V)[:n // 2].astype(np.int32)
+        return np.concatenate([one, one[::-1]])
+    if kind == "one long chain among others":
+        tok = g.integers(0, V, n).astype(np.int32)
+        tok[g.permutation(n)[:40]] = 77
+        return tok
+    return g.integers(0, 300, n).astype(np.int32)
+
+
+@pytest.mark.parametrize("kind,n,V", [
+    ("two tokens, one behind the other", 200_000, 1000), ("every token twice, far apart", 150_000, 100_000),
+    ("one long chain among others", 60_000, 128_256), ("a few tokens over and over", 200_000, 2049),
+    ("a few tokens over and over", 1_025, 2049), ("a few tokens over and over", 5_000, 1)])
+def test_long_lists_of_repeated_biases(kind, n, V):
+    """The walk through the list, whose time is the list's length times a constant: a search for each bias of a
+    repeated token would take n^2 / 4 steps here."""
+    import torch
+
+    from rejection_sampling_verify_09_amd import adjust_logits
+
+    log(f"[adjust] {n} biases, V={V}: {kind}")
+    g = np.random.default_rng(n + V)
+    tok = many(kind, n, V, g)
+    val = (g.standard_normal(len(tok)) * 10.0 ** g.integers(-3, 4, len(tok))).astype(np.float32)
+    few = g.integers(0, V, 9).astype(np.int32)  # and an ordinary sequence next to it
+    fval = g.standard_normal(9).astype(np.float32)
+    cu = cuda(np.array([0, len(tok), len(tok) + 9], dtype=np.int32))
+    bias = (cu, cuda(np.concatenate([tok, few])), cuda(np.concatenate([val, fval])))
+    keep = tok < V
+    want = np.stack([summed(tok[keep], val[keep], V)[0], summed(few, fval, V)[0]])
+    lg = torch.zeros((2, 3, V), device="cuda")
+    for out in (None, None, lg):
+        got = adjust_logits(lg, bias=bias, out=out).cpu().numpy()
+        for r in range(3):
+            assert np.array_equal(got[:, r], want)
+
+
+def test_long_histories_beside_long_lists_of_biases():
+    """The widest slices, whose workgroups have more threads than the walk's pieces have room."""
+    import torch
+
+    from rejection_sampling_verify_09_amd import adjust_logits
+
+    V, n = 20_003, 30_000
+    log(f"[adjust] {n} biases beside a history of 20,000")
+    g = np.random.default_rng(11)
+    tok = np.where(g.random(n) < 0.5, g.integers(0, 50, n), g.integers(0, V, n)).astype(np.int32)
+    val = g.standard_normal(n).astype(np.float32)
+    hist = torch.zeros((40, 20_000), device="cuda", dtype=torch.int32)
+    cu = np.zeros(41, dtype=np.int32)
+    cu[1:] = n  # the first sequence has them all, so that the slices' room is the least
+    want = np.zeros((40, V), dtype=np.float32)
+    want[0] = summed(tok, val, V)[0]
+    pres = torch.full((40,), 2.0, device="cuda")
+    lg = torch.zeros((40, V), device="cuda")
+    want[:, 0] = np.float32(-2.0) + want[:, 0]
+    for out in (None, lg):
+        got = adjust_logits(lg, history=hist, presence_penalty=pres, bias=(cuda(cu), cuda(tok), cuda(val)), out=out)
+        assert np.array_equal(got.cpu().numpy(), want)
