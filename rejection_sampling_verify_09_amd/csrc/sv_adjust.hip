@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   const bool counts = a.rep || a.freq || a.pres;
   const bool table = counts || a.cub;
   const int r0 = blockIdx.y * a.rgroup, r1 = min(nr, r0 + a.rgroup);
+  if (r0 >= r1) return;  // a ragged batch's shorter sequences have fewer groups of rows
   const size_t pitch = (size_t)a.V * EB;
 
   // what the table takes, loaded ahead of the rows
