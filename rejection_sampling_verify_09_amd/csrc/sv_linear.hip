@@ -19,6 +19,7 @@
 // Two kernels: linear_rows_kernel for up to 16 rows, whose waves share k, and
 // linear_tile_kernel for more, and for many columns; pick_kernel chooses.  In both the weight is the matrix instruction's first operand, so
 // that a lane holds four consecutive columns of the output.
+#include "sv_linear_pick.hpp"
 #include "sv_ops.hpp"
 #include "specverify.h"
 
@@ -715,68 +716,6 @@ hipError_t launch_tile(LinArgs a, hipStream_t s) {
   const unsigned grid = ((unsigned)a.mtiles * (unsigned)a.ntiles + LIN_XCD - 1) / LIN_XCD * LIN_XCD;
   hipLaunchKernelGGL((linear_tile_kernel<MODE, OUT, MB, NB, WM, WN, WK, D>), dim3(grid), dim3(64 * WM * WN * WK), lds, s, a);
   return hipGetLastError();
-}
-
-// The tiles to choose from: rows, columns, steps of k a round, workgroups a
-// compute unit holds, and the time of a round in nanoseconds, alone on its
-// compute unit (lat) and among others (thr), fitted to bfloat16 products of 32
-// to 1024 rows.  8-bit operands keep the order.
-struct TileCost {
-  int tm, tn, wk, per_cu;
-  float lat, thr;
-};
-constexpr TileCost kTiles[] = {
-    {32, 32, 4, 2, 530.0f, 450.0f},  {32, 64, 4, 1, 770.0f, 770.0f},    {64, 64, 2, 2, 550.0f, 490.0f},
-    {64, 128, 2, 1, 720.0f, 900.0f}, {128, 128, 1, 2, 600.0f, 590.0f},  {128, 256, 1, 1, 850.0f, 1050.0f},
-    {192, 256, 1, 1, 1150.0f, 1360.0f}, {224, 256, 1, 1, 1300.0f, 1570.0f},
-};
-
-// The tile with the least estimated time: that of the compute unit with the
-// most tiles, per_cu of them at a time, their rounds and 2.5 us around each
-// such turn.  Tiles of 32 rows are for products whose tiles all run at once:
-// in turns they reach less of the memory's bandwidth (32 x 24576 x 4096: 45 us,
-// 38 with 64 x 128).  Measured against each of them on 34 shapes and three type
-// combinations, the choice is 0.6% slower than the fastest in the mean, 15% at
-// most; 64 x 64 everywhere, for one, takes twice as long at 448 x 128256 x 2048
-// (471 against 225 us), and 224 x 256 five times as long at 128 x 4096 x 4096
-// (78 against 16 us).
-int pick_tile(int64_t M, int64_t N, int64_t steps) {
-  int best = -1;
-  double least = 0.0;
-  for (int i = 0; i < (int)(sizeof kTiles / sizeof *kTiles); ++i) {
-    const TileCost& c = kTiles[i];
-    const int64_t tiles = ((M + c.tm - 1) / c.tm) * ((N + c.tn - 1) / c.tn);
-    if (c.tm == 32 && tiles > 256 * c.per_cu) continue;
-    const double rounds = (double)((steps + c.wk - 1) / c.wk);
-    const int64_t most = (tiles + 255) / 256, turns = most / c.per_cu, left = most % c.per_cu;
-    double ns = turns * (rounds * std::max(c.lat, c.per_cu * c.thr) + 2500.0);
-    if (left) ns += rounds * std::max(c.lat, left * c.thr) + 2500.0;
-    if (best < 0 || ns < least) {
-      least = ns;
-      best = i;
-    }
-  }
-  return best;
-}
-
-// The kernel of a product: an index of kTiles, or one of these for up to 16 rows.
-enum Few : int { ROWS_16 = -1, ROWS_32 = -2 };  // 16 and 32 columns a workgroup
-
-int pick_kernel(int64_t M, int64_t N, int64_t kbytes) {
-  const int64_t steps = (kbytes + 127) / 128;
-  if (M > 16) return pick_tile(M, N, steps);
-  // Up to 8192 columns: 16 a workgroup, whose eight waves share k, so that
-  // there are enough of them (16 x 1000 x 16384 bfloat16: 15.5 us, 24 with 32
-  // columns and four waves; 16 x 4096 x 4096: 9.1 against 11.4).  Then 32
-  // columns where rows are short, since each wave has only a few steps of one (k
-  // of 4096 bytes, 16 x 128256 e4m3: 94 against 111 us; of 2048, 16 x 24576: 10.7
-  // against 12.3), and 16 where they are longer (8192 bytes, 1 x 128256: 164
-  // against 183 us).  Many columns with more than 8 long rows share the rows of
-  // x in the tiles of larger products (16 x 128256 x 4096 bfloat16: 182 against
-  // 202 us; 8 rows 181 against 177, 1 row 177 against 164).
-  if (N <= 8192) return ROWS_16;
-  if (kbytes <= 4096) return ROWS_32;
-  return M <= 8 || N <= 24576 ? ROWS_16 : pick_tile(M, N, steps);
 }
 
 // Threads of the launch, or an upper bound (every workgroup has at most 512).
