@@ -483,6 +483,8 @@ def _stream_on(dev: int, name: str, stream) -> int:
         raise ValueError(f"{name} must be a device tensor")
     if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise ValueError(f"{name} is on cuda:{dev}, the stream on {stream.device}")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 

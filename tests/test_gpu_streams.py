@@ -141,3 +141,60 @@ def test_a_round_given_a_stream():
             got = r.run(stream=handle)
         torch.cuda.synchronize()
         assert _same(_flat(got), want)
+
+
+def test_a_captured_fork_onto_a_given_stream():
+    """A capture whose calls are queued on a second stream that it has forked, replayed between eager calls."""
+    import torch
+
+    import rejection_sampling_verify_09_amd as sv
+
+    log("[streams] captured fork")
+    x = torch.randn((300, 512), device="cuda").bfloat16()
+    w = torch.randn((512,), device="cuda").bfloat16()
+    wide = torch.randn((1000, 512), device="cuda").bfloat16()
+    pres = torch.full((300,), 0.5, device="cuda")
+    side = torch.cuda.Stream()
+
+    def chain(stream):
+        here = torch.cuda.current_stream()
+        if stream is not None:
+            side.wait_stream(here)
+        y, _, _ = sv.rms_norm(x, w, stream=stream)
+        logits = sv.linear(y, wide, stream=stream)
+        out = sv.adjust_logits(logits, history=hist, presence_penalty=pres, stream=stream)
+        if stream is not None:
+            here.wait_stream(side)
+        return y + 0, logits + 0, out + 0
+
+    hist = torch.randint(0, 1000, (300, 40), device="cuda", dtype=torch.int32)
+    chain(None)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = chain(side)
+    for rep in range(4):
+        x.copy_(torch.randn((300, 512), device="cuda"))
+        hist.random_(0, 1000)
+        g.replay()
+        want = chain(side if rep % 2 else None)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), rep
+
+
+def test_a_stream_of_another_device_is_refused():
+    import torch
+
+    import rejection_sampling_verify_09_amd as sv
+
+    class Elsewhere(torch.cuda.Stream):
+        device = torch.device("cuda:1")
+
+    log("[streams] another device's stream")
+    x = torch.zeros((2, 64), device="cuda", dtype=torch.bfloat16)
+    s = Elsewhere()
+    for f in (lambda: sv.rms_norm(x, x[0], stream=s), lambda: sv.linear(x, x, stream=s),
+              lambda: sv.adjust_logits(x, stream=s)):
+        with pytest.raises(ValueError, match="stream on cuda:1"):
+            f()
