@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
     nd = a.cu[b + 1] - a.cu[b];
     row0 = d0 + (int64_t)b * a.bonus;
     nr = nd + a.bonus;
+    if ((int)(blockIdx.y * a.rgroup) >= nr) return;  // fewer groups of rows than the longest sequence has
   } else {
     d0 = (int64_t)b * a.K;
     nd = a.K;
@@ -215,7 +216,6 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
   const bool counts = a.rep || a.freq || a.pres;
   const bool table = counts || a.cub;
   const int r0 = blockIdx.y * a.rgroup, r1 = min(nr, r0 + a.rgroup);
-  if (r0 >= r1) return;  // a ragged batch's shorter sequences have fewer groups of rows
   const size_t pitch = (size_t)a.V * EB;
 
   // what the table takes, loaded ahead of the rows
@@ -251,17 +251,22 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
     masks(m, r0);
     fetch(r0);
   }
-  // the biases' tokens and values: a thread's first in registers (positions
+  // the sequence's ne biases, a thread's first in registers (positions are
   // unsigned: a few past the last one are formed, which 32 bits hold then)
-  uint32_t i0 = 0, i1 = 0;
+  const int32_t* btl = nullptr;
+  const float* bvl = nullptr;
+  uint32_t ne = 0;
   int btok0 = 0;
   float bval0 = 0.0f;
   if (a.cub) {
-    i0 = (uint32_t)min(max(a.cub[b], 0), a.nbias);
-    i1 = (uint32_t)min(max(a.cub[b + 1], 0), a.nbias);
-    if (i0 + t < i1) {
-      btok0 = a.btok[i0 + t];
-      bval0 = a.bval[i0 + t];
+    const int i0 = min(max(a.cub[b], 0), a.nbias);
+    const int i1 = min(a.cub[b + 1], a.nbias);
+    ne = (uint32_t)(max(i1, i0) - i0);
+    btl = a.btok + i0;
+    bvl = a.bval + i0;
+    if ((uint32_t)t < ne) {
+      btok0 = btl[t];
+      bval0 = bvl[t];
     }
   }
   if (table) {
@@ -317,14 +322,14 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
     // several biases of one token are added in the order they are listed, by
     // the thread that holds the first or, of a chain, its head; those of
     // E_BIASES tokens by a walk through the list
-    for (uint32_t i = i0 + t; i < i1; i += nt) {
-      const uint32_t j = (uint32_t)(i == i0 + t ? btok0 : a.btok[i]) - (uint32_t)v0;
+    for (uint32_t i = t; i < ne; i += nt) {
+      const uint32_t j = (uint32_t)(i == (uint32_t)t ? btok0 : btl[i]) - (uint32_t)v0;
       if (j >= (uint32_t)vn) continue;
       const int p = atomicAdd(&nbiased, 1);
       if (p < a.bcap) {
         bidx[p] = (int32_t)i;
         btoks[p] = (uint16_t)j;
-        bvals[p] = i == i0 + t ? bval0 : a.bval[i];
+        bvals[p] = i == (uint32_t)t ? bval0 : bvl[i];
         bnext[p] = (uint16_t)atomicExch(&bt[j], (uint32_t)p);
       }
     }
@@ -369,24 +374,24 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
       // too many: bt first takes the index of each token's first
       for (int i = t; i < S; i += nt) bt[i] = ~0u;
       __syncthreads();
-      for (uint32_t i = i0 + t; i < i1; i += nt) {
-        const uint32_t j = (uint32_t)a.btok[i] - (uint32_t)v0;
+      for (uint32_t i = t; i < ne; i += nt) {
+        const uint32_t j = (uint32_t)btl[i] - (uint32_t)v0;
         if (j >= (uint32_t)vn) continue;
         atomicMin(&bt[j], i);
         touch(j, atomicOr(&tab[j], E_BIAS));
       }
       __syncthreads();
-      for (uint32_t i = i0 + t; i < i1; i += nt) {
-        const uint32_t j = (uint32_t)a.btok[i] - (uint32_t)v0;
+      for (uint32_t i = t; i < ne; i += nt) {
+        const uint32_t j = (uint32_t)btl[i] - (uint32_t)v0;
         if (j < (uint32_t)vn && bt[j] != i) {
           atomicOr(&tab[j], E_BIASES);
           nordered = 1;
         }
       }
       __syncthreads();
-      for (uint32_t i = i0 + t; i < i1; i += nt) {
-        const uint32_t j = (uint32_t)a.btok[i] - (uint32_t)v0;
-        if (j < (uint32_t)vn && !(tab[j] & E_BIASES)) bt[j] = __float_as_uint(a.bval[i]);
+      for (uint32_t i = t; i < ne; i += nt) {
+        const uint32_t j = (uint32_t)btl[i] - (uint32_t)v0;
+        if (j < (uint32_t)vn && !(tab[j] & E_BIASES)) bt[j] = __float_as_uint(bvl[i]);
       }
     }
     __syncthreads();
@@ -397,12 +402,12 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
       // token is in it.
       const int piece = min(nt, a.bcap);
       uint32_t begun = 0;  // which of the thread's tokens have a sum
-      for (uint32_t base = i0; base < i1; base += piece) {
+      for (uint32_t base = 0; base < ne; base += piece) {
         const uint32_t i = base + t;
         uint32_t j = 0;
         bool mine = false;
-        if (t < piece && i < i1) {
-          j = (uint32_t)a.btok[i] - (uint32_t)v0;
+        if (t < piece && i < ne) {
+          j = (uint32_t)btl[i] - (uint32_t)v0;
           mine = j < (uint32_t)vn && (tab[j] & E_BIASES);
         }
         const uint64_t m = __ballot(mine);
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(ADJ_MAX_WG) adjust_kernel(AdjArgs a) {
         }
         if (mine) {
           btoks[at] = (uint16_t)j;
-          bvals[at] = a.bval[i];
+          bvals[at] = bvl[i];
         }
         __syncthreads();
         for (int p = 0; p < total; ++p) {

@@ -130,3 +130,26 @@ def test_long_histories_beside_long_lists_of_biases():
     for out in (None, lg):
         got = adjust_logits(lg, history=hist, presence_penalty=pres, bias=(cuda(cu), cuda(tok), cuda(val)), out=out)
         assert np.array_equal(got.cpu().numpy(), want)
+
+
+def test_offsets_outside_the_list_are_taken_as_its_ends():
+    """Negative and large offsets, and ones that run backwards, of a list inside a longer buffer."""
+    import torch
+
+    from rejection_sampling_verify_09_amd import adjust_logits
+
+    log("[adjust] bias offsets past the list's ends")
+    V, n = 50, 6
+    tok = torch.arange(100, device="cuda", dtype=torch.int32) % V
+    val = torch.arange(1, 101, device="cuda").float()
+    lo, hi = -(1 << 31), (1 << 31) - 1
+    for cu, ranges in (((-5, 3, 100), ((0, 3), (3, 6))), ((2, hi, hi), ((2, 6), (6, 6))), ((4, 1, 5), ((4, 4), (1, 5))),
+                       ((lo, lo, lo), ((0, 0), (0, 0))), ((3, lo, hi), ((3, 3), (0, 6))), ((7, lo, 6), ((6, 6), (0, 6)))):
+        want = np.zeros((2, V), dtype=np.float32)
+        for b, (i, k) in enumerate(ranges):
+            want[b, i:k] = np.arange(i + 1, k + 1)
+        lg = torch.zeros((2, V), device="cuda")
+        offsets = torch.tensor(cu, device="cuda", dtype=torch.int64).to(torch.int32)
+        for out in (None, lg):
+            got = adjust_logits(lg, bias=(offsets, tok[:n], val[:n]), out=out).cpu().numpy()
+            assert np.array_equal(got, want), cu
