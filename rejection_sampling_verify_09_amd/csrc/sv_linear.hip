@@ -13,11 +13,12 @@
 // to 448 x 448 a product of 7 is lost altogether, also where the large ones
 // cancel (2-norm of the error on normal values 1.5e-5 of the result, with
 // outlier columns 6e-5; so converted, 8e-8).  They are not used, and the
-// largest products take half again as long for it (448 x 128256 x 4096 to
-// bfloat16: 385 us, 235 with them).
+// largest products take more than half again as long for it (448 x 128256 x 4096
+// to bfloat16: 376 to 384 us, 235 with them).
 //
 // Two kernels: linear_rows_kernel for up to 16 rows, whose waves share k, and
-// linear_tile_kernel for more, and for many columns; pick_kernel chooses.  In both the weight is the matrix instruction's first operand, so
+// linear_tile_kernel for more, and for many columns; sv_linear_pick.hpp
+// chooses.  In both the weight is the matrix instruction's first operand, so
 // that a lane holds four consecutive columns of the output.
 #include "sv_linear_pick.hpp"
 #include "sv_ops.hpp"
@@ -265,11 +266,11 @@ __device__ __forceinline__ void wave_sync() {
 // The workgroups begin their rounds over k at different ones, each group of
 // about 256 columns at its own: where they all begin at 0, they ask for the
 // same bytes of every row at once, and rows a power of two apart keep only some
-// of the memory's channels busy (64 x 24576 x 4096 bfloat16 with 64 x 128 tiles:
-// 48.0 us from 0, 40.4 so; 16 x 32000 x 4096 e4m3: 27.2 and 24.2; rows of 4224
-// bytes: alike).  Where x is larger than an XCD's L2, all begin at 0, so that
-// the column panels read the same part of x (4096 x 16384 x 4096 e4m3: 264 us,
-// 275 otherwise).
+// of the memory's channels busy (64 x 24576 x 4096 bfloat16, the bare product
+// with 64 x 128 tiles: 48.0 us from 0, 40.0 so; 16 x 32000 x 4096 e4m3: 29.6 and
+// 25.4; rows of 4224 bytes: alike).  Where x is larger than an XCD's L2, all
+// begin at 0, so that the column panels read the same part of x (2048 x 8192 x
+// 8192 bfloat16: 258 us, 264 otherwise; five others of 1024 to 8192 rows: alike).
 __device__ __forceinline__ int first_round(const LinArgs& a, int n0, int rounds) {
   return a.turn ? (n0 >> 8) % rounds : 0;
 }
@@ -285,7 +286,7 @@ __device__ __forceinline__ int turned(int round, int first, int rounds) {
 // load), and a wave brings them into fragments through LDS of its own (16 x
 // 24576 x 4096 bfloat16 41 us, 50 with fragments loaded directly).  Bound by
 // the weight's bytes on long weights: 1 x 128256 x 4096 takes 164 us in
-// bfloat16 (6.4 TB/s) and 85 in e4m3 (6.2), 7 rows to float32 89; by the launch
+// bfloat16 (6.4 TB/s) and 84 in e4m3 (6.2), 7 rows to float32 89; by the launch
 // on short ones (1 x 4096 x 4096: 9.0 us).
 template <int MODE, int OUT, int NT, int MT, int W, int D>
 __global__ void __launch_bounds__(64 * W) linear_rows_kernel(LinArgs a) {
@@ -389,12 +390,14 @@ constexpr int LIN_XCD = 8;  // XCDs the workgroup ids are dealt over
 //
 // What bounds the largest tile (224 x 256, k blocks of 128 bytes, 8 waves, one
 // workgroup a compute unit): the matrix instructions, and in part beside them
-// LDS traffic (112 KB of rows, 64 KB of weights read, 60 KB written a round).
-// At 448 x 128256 x 4096: e4m3 to bfloat16 383 us (1.23 PFLOP/s), to float32
-// 381 (1.24), bfloat16 427 (1.10); the library's product of bfloat16 operands
-// takes 543, that of 8-bit ones, on the 8-bit instructions, 295.  The small tiles are bound by
-// the latency of a round (loads, LDS, barrier: 0.7 us), of which 333 x 5001 x
-// 2112 has 17 (17.4 us; the library 22.8).
+// LDS traffic (112 KB of rows, 64 KB of weights read, 60 KB written a round)
+// and, for e4m3, the conversions; by the counters the matrix units are busy 60%
+// of the time there and LDS 22%.  At 448 x 128256 x 4096: e4m3 to bfloat16 376
+// to 384 us (1.25 PFLOP/s), to float32 381 (1.24), bfloat16 422 (1.12); the
+// library's product of bfloat16 operands takes 543, that of 8-bit ones, on the
+// 8-bit instructions, 296.  The small tiles are bound by the latency of a round
+// (loads, LDS, barrier: 0.7 us), of which 333 x 5001 x 2112 has 17 (17.4 us; the
+// library 21 to 23).
 template <int MODE, int OUT, int MB, int NB, int WM, int WN, int WK, int D>
 __global__ void __launch_bounds__(64 * WM * WN * WK) linear_tile_kernel(LinArgs a) {
   constexpr int IN = MODE == L_BF16 ? T_BF16 : T_E4M3;

@@ -10,7 +10,7 @@ namespace sv {
 // The tiles to choose from: rows, columns, steps of k a round, workgroups a
 // compute unit holds, and the time of a round in nanoseconds, alone on its
 // compute unit (lat) and among others (thr), fitted to bfloat16 products of 32
-// to 1024 rows.  8-bit operands keep the order.
+// to 1024 rows; e4m3 operands take them in the same order (pick_tile).
 struct TileCost {
   int tm, tn, wk, per_cu;
   float lat, thr;
@@ -25,11 +25,12 @@ constexpr TileCost kTiles[] = {
 // most tiles, per_cu of them at a time, their rounds and 2.5 us around each
 // such turn.  Tiles of 32 rows are for products whose tiles all run at once:
 // in turns they reach less of the memory's bandwidth (32 x 24576 x 4096: 45 us,
-// 38 with 64 x 128).  Measured against each of them on 34 shapes and three type
-// combinations, the choice is 0.6% slower than the fastest in the mean, 15% at
-// most; 64 x 64 everywhere, for one, takes twice as long at 448 x 128256 x 2048
-// (471 against 225 us), and 224 x 256 five times as long at 128 x 4096 x 4096
-// (78 against 16 us).
+// 38 with 64 x 128).  Measured against each of them on 29 shapes, the choice is
+// behind the fastest by 0.9% in the mean for bfloat16 operands, 1.3 for e4m3 to
+// float32 and 0.7 for e4m3 to bfloat16, and by 15, 14 and 8% at most; 64 x 64
+// everywhere, for one, takes twice as long at 448 x 128256 x 2048 (471 against
+// 225 us), and 224 x 256 five times as long at 128 x 4096 x 4096 (78 against 16
+// us).
 inline int pick_tile(int64_t M, int64_t N, int64_t steps) {
   int best = -1;
   double least = 0.0;
@@ -63,7 +64,10 @@ inline int pick_kernel(int64_t M, int64_t N, int64_t kbytes) {
   // against 12.3), and 16 where they are longer (8192 bytes, 1 x 128256: 164
   // against 183 us).  Many columns with more than 8 long rows share the rows of
   // x in the tiles of larger products (16 x 128256 x 4096 bfloat16: 182 against
-  // 202 us; 8 rows 181 against 177, 1 row 177 against 164).
+  // 202 us; 8 rows 181 against 177, 1 row 177 against 164).  Between 24576 and
+  // 128256 columns the two are close: 16 rows of 4096 take 47 against 51 us at
+  // 32000 columns, 78 against 77 at 49152, 101 against 103 at 65536, and 9 rows,
+  // the other end, 47, 78 and 100 against 47, 71 and 93.
   if (N <= 8192) return ROWS_16;
   if (kbytes <= 4096) return ROWS_32;
   return M <= 8 || N <= 24576 ? ROWS_16 : pick_tile(M, N, steps);
