@@ -71,7 +71,7 @@ typedef enum {
 typedef enum {
   SV_F32 = 0,
   SV_BF16 = 1,
-  SV_E4M3 = 2 /* 8 bits, OCP e4m3 (no infinities): sv_rms_norm's output, sv_linear's operands */
+  SV_E4M3 = 2 /* 8 bits, OCP e4m3 (no infinities): the norms' output, sv_linear's operands */
 } sv_dtype;
 
 /* Activations of sv_linear's epilogue. */
@@ -90,9 +90,11 @@ typedef enum {
  * call with B <= 64, K <= 6 and V <= 128256, in any mode and dtype; a call
  * whose scratch would not fit returns SV_ERR_WORKSPACE. */
 #define SV_NOALLOC_SCRATCH_BYTES (32 << 20)
-#define SV_MAX_NORM_D 65536         /* widest row of sv_rms_norm              */
+#define SV_MAX_NORM_D 65536         /* widest row of the norms                */
 #define SV_MAX_LINEAR_K 65536       /* longest sum of sv_linear               */
 #define SV_MAX_HISTORY (1 << 21)    /* tokens per sequence, sv_adjust_logits  */
+#define SV_MAX_TOP 1024             /* entries of a list: sv_top_logits, sv_distill_loss */
+#define SV_MAX_DISTILL_V 1048576    /* vocabulary of sv_distill_loss          */
 /* sv_init flag: also size the stream's buffer of projection logits for
  * sv_spec_verify_lmhead. */
 #define SV_INIT_LMHEAD 1
@@ -553,6 +555,136 @@ int sv_adjust_logits_ragged(const void* logits, void* out_logits, const int32_t*
                             const uint32_t* mask, const int32_t* mask_index, int32_t B, int32_t total_draft,
                             int32_t max_k, int32_t bonus_rows, int32_t history_cap, int32_t num_bias,
                             int32_t mask_rows, int32_t V, int32_t dtype, void* stream);
+
+/*
+ * sv_layer_norm - layer norm with the residual's addition:
+ *   h = x + residual        (h = x without a residual)
+ *   out_j = (h_j - mean h) / sqrt(mean((h - mean h)^2) + eps) * weight_j
+ *           + bias_j
+ * As sv_rms_norm otherwise: float32 throughout, out rounded once, SV_E4M3 with
+ * a scale per row, h rounded to x's type where out_residual asks for it, the
+ * same shapes and limits, in place on x or residual, no scratch.  weight and
+ * bias [d] dtype may each be NULL (1 and 0).  A row whose sum or sum of squares
+ * about its mean is not finite comes out all NaN, its scale too.
+ */
+int sv_layer_norm(const void* x, const void* residual, const void* weight, const void* bias, float eps, void* out,
+                  float* out_scale, void* out_residual, int32_t rows, int32_t d, int32_t dtype, int32_t out_dtype,
+                  void* stream);
+
+/*
+ * sv_layer_norm_backward, sv_rms_norm_backward - gradients of the norms, for
+ * training what stands before the output projection.  With g_j = grad_j *
+ * weight_j, r = 1 / sqrt(mean((h - m)^2) + eps) and n_j = (h_j - m) r, where m =
+ * mean h (layer norm) or 0 (root mean square):
+ *   grad_h_j      = r (g_j - [mean g] - n_j mean(g n)) + grad_residual_j
+ *   grad_weight_j = sum over rows grad_j n_j
+ *   grad_bias_j   = sum over rows grad_j
+ * ([mean g]: layer norm only).  h is the norm's input after the residual's
+ * addition (the forward call's out_residual, or x without a residual); the
+ * row's statistics are formed from it again.  Everything is float32; grad_h is
+ * rounded once to its type.
+ *
+ * grad          [rows, d] dtype (SV_F32 or SV_BF16), device: the gradient of
+ *               the norm's output
+ * h             [rows, d] dtype, device
+ * weight        [d] dtype, device, or NULL (1)
+ * grad_residual [rows, d] dtype, device, or NULL: a gradient that arrives at h
+ *               by another way (the residual stream), added to grad_h
+ * grad_h        [rows, d] dtype, device: the gradient of x and of residual
+ * grad_weight, grad_bias  [d] float32, device, or NULL (not wanted)
+ * workspace     16-byte aligned device memory of workspace_bytes >=
+ *               sv_norm_backward_workspace(rows, d) (half of it is enough for one
+ *               of grad_weight and grad_bias, none for neither); its contents
+ *               before and after the call mean nothing.  Calls that may overlap
+ *               need one each.
+ *
+ * The sums over rows are formed in a fixed order: the same call gives the same
+ * bits.  grad_h may be grad, h or grad_residual itself (in place); any other
+ * overlap of what is written with another argument is SV_ERR_PARAM.  A row
+ * whose statistics are not finite gives NaN in its grad_h and in grad_weight.
+ * rows == 0 writes zeros to grad_weight and grad_bias.  1 <= d <= SV_MAX_NORM_D
+ * (else SV_ERR_SHAPE).  A workspace that is too small is SV_ERR_WORKSPACE.
+ * Nothing is allocated; calls may be captured.
+ *
+ * sv_norm_backward_workspace returns bytes, or SV_ERR_SHAPE.
+ */
+int64_t sv_norm_backward_workspace(int32_t rows, int32_t d);
+int sv_layer_norm_backward(const void* grad, const void* h, const void* weight, const void* grad_residual, float eps,
+                           void* grad_h, float* grad_weight, float* grad_bias, void* workspace, int64_t workspace_bytes,
+                           int32_t rows, int32_t d, int32_t dtype, void* stream);
+int sv_rms_norm_backward(const void* grad, const void* h, const void* weight, const void* grad_residual, float eps,
+                         void* grad_h, float* grad_weight, void* workspace, int64_t workspace_bytes, int32_t rows,
+                         int32_t d, int32_t dtype, void* stream);
+
+/*
+ * sv_top_logits - the k largest logits of each row, their tokens, and the
+ * row's log-sum-exp: what is kept of a target's logits to train a draft on
+ * (sv_distill_loss), or to report log-probabilities from (value / temperature -
+ * lse).
+ *
+ * logits      [rows, V] dtype (SV_F32 or SV_BF16), device
+ * out_values  [rows, k] float32, device: the logits themselves, largest first,
+ *             equal ones by ascending token (-0 and +0 are equal; NaN stands
+ *             before +inf)
+ * out_index   [rows, k] int32, device: their tokens
+ * out_lse     [rows] float32, device, or NULL: log sum_j exp(logit_j /
+ *             temperature) over the whole row; -inf for a row of -inf alone
+ *             (whose list is its first k tokens at -inf)
+ * temperature finite, >= FLT_MIN (used for out_lse alone)
+ *
+ * 1 <= k <= min(V, SV_MAX_TOP), 1 <= V <= SV_MAX_V, and rows * min(1024, V / 8
+ * or V / 4 in whole waves) threads within one launch (else SV_ERR_SHAPE).
+ * Overlap of an output with another argument is SV_ERR_PARAM.  rows == 0 does
+ * nothing.  Nothing is allocated and no scratch is used.
+ */
+int sv_top_logits(const void* logits, int32_t k, float temperature, float* out_values, int32_t* out_index,
+                  float* out_lse, int32_t rows, int32_t V, int32_t dtype, void* stream);
+
+/*
+ * sv_distill_loss - divergence of a draft's (the student's) distribution from
+ * its target's (the teacher's) top logits, and the gradient of the student's
+ * logits, in one call.  A draft is fine-tuned on its target's answers so that
+ * more of its tokens are accepted (page www.2kiu.com/news/5895634 section 4.1;
+ * page www.gsyq.cn/news/428210 section 3.3).  Of one row, with the list (i_j,
+ * t_j), j < k, and q = softmax(logits / temperature):
+ *   with top_lse:    p_j = exp(t_j / temperature - top_lse), and what the list
+ *                    leaves, r = max(0, 1 - sum_j p_j), is the rest of the
+ *                    vocabulary as one more outcome
+ *   without top_lse: p = softmax over the list of t_j / temperature, r = 0
+ *   R    = sum of q_v over the tokens v that are not listed
+ *   loss = weight * (sum_j p_j (log p_j - log q_{i_j}) + r (log r - log R))
+ *   grad_v = weight / temperature * (q_v - p_v)           v listed
+ *          = weight / temperature * (q_v / R) (R - r)     v not listed
+ *
+ * logits      [rows, V] dtype (SV_F32 or SV_BF16), device: the student's
+ * top_index   [rows, k] int32, device: the list's tokens, in any order; an
+ *             entry outside [0, V) is absent, whatever its value
+ * top_values  [rows, k] float32, device: the teacher's logits there
+ * top_lse     [rows] float32, device, or NULL: the teacher's log-sum-exp at
+ *             the same temperature, as sv_top_logits writes it
+ * weight      [rows] float32, device, or NULL (1): the row's share of the loss,
+ *             or the gradient that arrives at its loss.  0: a row to leave out,
+ *             whose logits are not looked at
+ * temperature finite, >= FLT_MIN
+ * out_loss    [rows] float32, device, or NULL
+ * out_grad    [rows, V] dtype, device, or NULL (one of the two is wanted); may
+ *             be logits itself (in place)
+ *
+ * A token listed twice counts with both its p, and its q once.  A row without a
+ * teacher (no entry above -inf, or a top_lse of -inf) has loss 0 and gradient 0.
+ * The student's logits may be -inf: q is 0 there, and the loss is +inf where p
+ * is not.  Where every token that is not listed is at -inf, their term is left
+ * out (r is then no more than the rounding of top_lse).  NaN and +inf logits make
+ * the row's loss and gradient NaN.  The list's sums and the loss are float64,
+ * the sums over the vocabulary float32; loss and gradient are rounded once.
+ * 1 <= k <= SV_MAX_TOP, 1 <= V <= SV_MAX_DISTILL_V, and threads within one
+ * launch as for sv_top_logits (else SV_ERR_SHAPE).  Any overlap of an output
+ * with another argument but out_grad == logits is SV_ERR_PARAM.  rows == 0 does
+ * nothing.  Nothing is allocated and no scratch is used.
+ */
+int sv_distill_loss(const void* logits, const int32_t* top_index, const float* top_values, const float* top_lse,
+                    const float* weight, float temperature, float* out_loss, void* out_grad, int32_t rows, int32_t V,
+                    int32_t k, int32_t dtype, void* stream);
 
 /*
  * sv_read_floor - measurement aid, not part of the verification: reads the

@@ -67,6 +67,18 @@ def lib() -> ctypes.CDLL:
         L.sv_adjust_logits.restype = ctypes.c_int
         L.sv_adjust_logits_ragged.argtypes = [vp] * 15 + [i32] * 9 + [vp]
         L.sv_adjust_logits_ragged.restype = ctypes.c_int
+        L.sv_layer_norm.argtypes = [vp, vp, vp, vp, f32, vp, vp, vp, i32, i32, i32, i32, vp]
+        L.sv_layer_norm.restype = ctypes.c_int
+        L.sv_norm_backward_workspace.argtypes = [i32, i32]
+        L.sv_norm_backward_workspace.restype = ctypes.c_int64
+        L.sv_layer_norm_backward.argtypes = [vp, vp, vp, vp, f32, vp, vp, vp, vp, ctypes.c_int64, i32, i32, i32, vp]
+        L.sv_layer_norm_backward.restype = ctypes.c_int
+        L.sv_rms_norm_backward.argtypes = [vp, vp, vp, vp, f32, vp, vp, vp, ctypes.c_int64, i32, i32, i32, vp]
+        L.sv_rms_norm_backward.restype = ctypes.c_int
+        L.sv_top_logits.argtypes = [vp, i32, f32, vp, vp, vp, i32, i32, i32, vp]
+        L.sv_top_logits.restype = ctypes.c_int
+        L.sv_distill_loss.argtypes = [vp, vp, vp, vp, vp, f32, vp, vp, i32, i32, i32, i32, vp]
+        L.sv_distill_loss.restype = ctypes.c_int
         L.sv_dynk_create.argtypes = [i32, i32, ctypes.c_double, ctypes.c_double, i32, i32, i32]
         L.sv_dynk_create.restype = vp
         L.sv_dynk_observe.argtypes = [vp, vp, vp, vp]
@@ -685,6 +697,222 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor | None = None, his
     if st != SV_OK:
         raise SpecVerifyError(st, what)
     return out
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+               residual: torch.Tensor | None = None, eps: float = 1e-5, out_dtype: torch.dtype | None = None,
+               out: torch.Tensor | None = None, out_scale: torch.Tensor | None = None,
+               out_residual: torch.Tensor | None = None, stream=None):
+    """Layer norm of the last dimension with the residual's addition: h = x +
+    residual, out = (h - mean h) * weight / sqrt(mean((h - mean h)^2) + eps) +
+    bias.
+
+    x [..., d] float32 or bfloat16, weight [d] (1 by default), bias [d] (0 by
+    default) and residual [..., d] of x's type; out_dtype float32, bfloat16
+    (x's type by default) or float8_e4m3fn (then with one float32 scale per
+    row: the row is out * out_scale).  Returns (out, out_scale [...] or None, h
+    rounded to x's type or None without a residual).  out and out_residual may
+    be x or residual (in place)."""
+    code = _code(x.dtype, "x", _FLOATS)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    ocode = _code(out_dtype, "out_dtype", _CODES)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., d]")
+    d = x.shape[-1]
+    rows = x.numel() // d
+    _int32(rows, d)
+    dev = x.get_device()
+    wp = _arg(weight, "weight", x.dtype, (d,), dev)
+    bp = _arg(bias, "bias", x.dtype, (d,), dev)
+    rp = _arg(residual, "residual", x.dtype, x.shape, dev)
+    if residual is None and out_residual is not None:
+        raise ValueError("out_residual needs a residual")
+    if ocode != SV_E4M3 and out_scale is not None:
+        raise ValueError("out_scale goes with out_dtype float8_e4m3fn")
+    op = _arg(out, "out", out_dtype, x.shape, dev)
+    sp = _arg(out_scale, "out_scale", torch.float32, x.shape[:-1], dev)
+    hp = _arg(out_residual, "out_residual", x.dtype, x.shape, dev)
+    xp = _arg(x, "x", x.dtype, x.shape, dev)
+    s = _stream_on(dev, "x", stream)
+    if out is None:
+        out = _new(stream, dev, torch.empty_like, x, dtype=out_dtype)
+        op = out.data_ptr()
+    if ocode == SV_E4M3 and out_scale is None:
+        out_scale = _new(stream, dev, x.new_empty, x.shape[:-1], dtype=torch.float32)
+        sp = out_scale.data_ptr()
+    if residual is not None and out_residual is None:
+        out_residual = _new(stream, dev, torch.empty_like, x)
+        hp = out_residual.data_ptr()
+    st = lib().sv_layer_norm(xp, rp, wp, bp, float(eps), op, sp, hp, rows, d, code, ocode, s)
+    if st != SV_OK:
+        raise SpecVerifyError(st, "sv_layer_norm")
+    return out, out_scale, out_residual
+
+
+def _norm_backward(center: bool, grad, h, weight, grad_residual, eps, with_weight, with_bias, out, out_weight, out_bias,
+                   stream):
+    code = _code(h.dtype, "h", _FLOATS)
+    if h.dim() < 1 or h.shape[-1] < 1:
+        raise ValueError("h must be [..., d]")
+    d = h.shape[-1]
+    rows = h.numel() // d
+    _int32(rows, d)
+    dev = h.get_device()
+    gp = _arg(grad, "grad", h.dtype, h.shape, dev)
+    wp = _arg(weight, "weight", h.dtype, (d,), dev)
+    rp = _arg(grad_residual, "grad_residual", h.dtype, h.shape, dev)
+    for t, name, on in ((out_weight, "weight", with_weight), (out_bias, "bias", with_bias)):
+        if t is not None and not on:
+            raise ValueError(f"out_{name} goes with with_{name}")
+    op = _arg(out, "out", h.dtype, h.shape, dev)
+    owp = _arg(out_weight, "out_weight", torch.float32, (d,), dev)
+    obp = _arg(out_bias, "out_bias", torch.float32, (d,), dev)
+    hp = _arg(h, "h", h.dtype, h.shape, dev)
+    s = _stream_on(dev, "h", stream)
+    if out is None:
+        out = _new(stream, dev, torch.empty_like, h)
+        op = out.data_ptr()
+    if with_weight and out_weight is None:
+        out_weight = _new(stream, dev, h.new_empty, (d,), dtype=torch.float32)
+        owp = out_weight.data_ptr()
+    if with_bias and out_bias is None:
+        out_bias = _new(stream, dev, h.new_empty, (d,), dtype=torch.float32)
+        obp = out_bias.data_ptr()
+    L = lib()
+    nbytes = max(L.sv_norm_backward_workspace(rows, d), 0) * ((1 if with_weight else 0) + (1 if with_bias else 0)) // 2
+    ws = None
+    if nbytes:
+        # on the call's own stream: handed out again only behind the call
+        ws = _new(stream, dev, h.new_empty, (nbytes,), dtype=torch.uint8)
+    wsp = None if ws is None else ws.data_ptr()
+    if center:
+        st = L.sv_layer_norm_backward(gp, hp, wp, rp, float(eps), op, owp, obp, wsp, nbytes, rows, d, code, s)
+    else:
+        st = L.sv_rms_norm_backward(gp, hp, wp, rp, float(eps), op, owp, wsp, nbytes, rows, d, code, s)
+    if st != SV_OK:
+        raise SpecVerifyError(st, "sv_layer_norm_backward" if center else "sv_rms_norm_backward")
+    return out, out_weight, out_bias
+
+
+def layer_norm_backward(grad: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None = None,
+                        grad_residual: torch.Tensor | None = None, eps: float = 1e-5, with_weight: bool = True,
+                        with_bias: bool = True, out: torch.Tensor | None = None,
+                        out_weight: torch.Tensor | None = None, out_bias: torch.Tensor | None = None, stream=None):
+    """Gradients of layer_norm: of its input and, summed over the rows, of its
+    weight and bias.
+
+    grad [..., d]: the gradient of layer_norm's output; h [..., d]: its input
+    after the residual's addition (the h that layer_norm returns, or x without
+    a residual); weight [d] (1 by default); grad_residual [..., d]: what
+    arrives at h through the residual stream, added.  All float32 or all
+    bfloat16.  Returns (grad_h [..., d] of h's type, the gradient of x and of
+    residual; grad_weight [d] float32 or None; grad_bias [d] float32 or None).
+    with_weight, with_bias: whether those are wanted (False for a frozen
+    norm).  out may be grad, h or grad_residual (in place)."""
+    return _norm_backward(True, grad, h, weight, grad_residual, eps, with_weight, with_bias, out, out_weight, out_bias,
+                          stream)
+
+
+def rms_norm_backward(grad: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None = None,
+                      grad_residual: torch.Tensor | None = None, eps: float = 1e-6, with_weight: bool = True,
+                      out: torch.Tensor | None = None, out_weight: torch.Tensor | None = None, stream=None):
+    """Gradients of rms_norm, as layer_norm_backward without the bias.  Returns
+    (grad_h [..., d] of h's type, grad_weight [d] float32 or None)."""
+    return _norm_backward(False, grad, h, weight, grad_residual, eps, with_weight, False, out, out_weight, None,
+                          stream)[:2]
+
+
+def top_logits(logits: torch.Tensor, k: int, temperature: float = 1.0, with_lse: bool = True,
+               out_values: torch.Tensor | None = None, out_index: torch.Tensor | None = None,
+               out_lse: torch.Tensor | None = None, stream=None):
+    """The k largest logits of every row of ``logits`` [..., V] (float32 or
+    bfloat16): (values [..., k] float32, largest first and equal ones by
+    ascending token; index [..., k] int32, their tokens; lse [...] float32, the
+    log-sum-exp of logits / temperature over the whole row, or None).
+
+    What distill_loss takes of a target's logits; values / temperature - lse
+    are log-probabilities.  1 <= k <= min(V, 1024)."""
+    code = _code(logits.dtype, "logits", _FLOATS)
+    if logits.dim() < 1 or logits.shape[-1] < 1:
+        raise ValueError("logits must be [..., V]")
+    V = logits.shape[-1]
+    rows = logits.numel() // V
+    k = int(k)
+    if k < 1:
+        raise ValueError("k must be at least 1")
+    _int32(rows, V, k)
+    if not with_lse and out_lse is not None:
+        raise ValueError("out_lse goes with with_lse")
+    lead = logits.shape[:-1]
+    dev = logits.get_device()
+    vp = _arg(out_values, "out_values", torch.float32, lead + (k,), dev)
+    ip = _arg(out_index, "out_index", torch.int32, lead + (k,), dev)
+    sp = _arg(out_lse, "out_lse", torch.float32, lead, dev)
+    lp = _arg(logits, "logits", logits.dtype, logits.shape, dev)
+    s = _stream_on(dev, "logits", stream)
+    if out_values is None:
+        out_values = _new(stream, dev, logits.new_empty, lead + (k,), dtype=torch.float32)
+        vp = out_values.data_ptr()
+    if out_index is None:
+        out_index = _new(stream, dev, logits.new_empty, lead + (k,), dtype=torch.int32)
+        ip = out_index.data_ptr()
+    if with_lse and out_lse is None:
+        out_lse = _new(stream, dev, logits.new_empty, lead, dtype=torch.float32)
+        sp = out_lse.data_ptr()
+    st = lib().sv_top_logits(lp, k, float(temperature), vp, ip, sp, rows, V, code, s)
+    if st != SV_OK:
+        raise SpecVerifyError(st, "sv_top_logits")
+    return out_values, out_index, out_lse
+
+
+def distill_loss(logits: torch.Tensor, top_index: torch.Tensor, top_values: torch.Tensor,
+                 top_lse: torch.Tensor | None = None, temperature: float = 1.0, weight: torch.Tensor | None = None,
+                 with_loss: bool = True, with_grad: bool = False, out_loss: torch.Tensor | None = None,
+                 out_grad: torch.Tensor | None = None, stream=None):
+    """Divergence of a draft's distributions from its target's top logits, and
+    the gradient of the draft's logits.
+
+    logits [..., V] float32 or bfloat16: the draft's; top_index [..., k] int32
+    (entries outside [0, V): absent) and top_values [..., k] float32: the
+    target's list, as top_logits returns it; top_lse [...] float32: the
+    target's log-sum-exp at the same temperature: what the list leaves is then
+    one more outcome, otherwise the target is its list alone; weight [...]
+    float32: each row's share of the loss, or the gradient that arrives at it
+    (0: the row is left out).  Returns (loss [...] float32 or None, the
+    gradient of the sum of loss with respect to logits, of its shape and type,
+    or None): both in one pass with with_grad, the gradient alone with
+    with_loss=False.  out_grad may be logits (in place)."""
+    code = _code(logits.dtype, "logits", _FLOATS)
+    if logits.dim() < 1 or logits.shape[-1] < 1 or top_index.dim() < 1 or top_index.shape[-1] < 1:
+        raise ValueError("logits must be [..., V] and top_index [..., k]")
+    V, k = logits.shape[-1], top_index.shape[-1]
+    rows = logits.numel() // V
+    _int32(rows, V, k)
+    if not with_loss and not with_grad:
+        raise ValueError("with_loss or with_grad")
+    if (out_loss is not None and not with_loss) or (out_grad is not None and not with_grad):
+        raise ValueError("out_loss goes with with_loss, out_grad with with_grad")
+    lead = logits.shape[:-1]
+    dev = logits.get_device()
+    f32 = torch.float32
+    ip = _arg(top_index, "top_index", torch.int32, lead + (k,), dev)
+    vp = _arg(top_values, "top_values", f32, lead + (k,), dev)
+    sp = _arg(top_lse, "top_lse", f32, lead, dev)
+    wp = _arg(weight, "weight", f32, lead, dev)
+    op = _arg(out_loss, "out_loss", f32, lead, dev)
+    gp = _arg(out_grad, "out_grad", logits.dtype, logits.shape, dev)
+    lp = _arg(logits, "logits", logits.dtype, logits.shape, dev)
+    s = _stream_on(dev, "logits", stream)
+    if with_loss and out_loss is None:
+        out_loss = _new(stream, dev, logits.new_empty, lead, dtype=f32)
+        op = out_loss.data_ptr()
+    if with_grad and out_grad is None:
+        out_grad = _new(stream, dev, torch.empty_like, logits)
+        gp = out_grad.data_ptr()
+    st = lib().sv_distill_loss(lp, ip, vp, sp, wp, float(temperature), op, gp, rows, V, k, code, s)
+    if st != SV_OK:
+        raise SpecVerifyError(st, "sv_distill_loss")
+    return out_loss, out_grad
 
 
 class DraftLengthController:

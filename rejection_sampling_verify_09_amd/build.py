@@ -10,8 +10,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libspecverify.so")
-SOURCES = ["sv_kernels.hip", "sv_api.hip", "sv_lmhead.hip", "sv_norm.hip", "sv_linear.hip", "sv_adjust.hip",
-           "sv_dynk.cpp"]
+SOURCES = ["sv_kernels.hip", "sv_api.hip", "sv_lmhead.hip", "sv_norm.hip", "sv_layer_norm.hip", "sv_linear.hip",
+           "sv_adjust.hip", "sv_top.hip", "sv_distill.hip", "sv_dynk.cpp"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

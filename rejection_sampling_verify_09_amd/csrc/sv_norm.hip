@@ -32,57 +32,6 @@ struct NormArgs {
   float eps;
 };
 
-// Eight elements at p as floats, n of them (the others 0) where n < 8.  AL: p
-// is 16-byte aligned; otherwise aligned to the element (the loads and stores
-// are the same 16-byte ones, which the hardware splits where they cross).
-template <int T, bool AL>
-__device__ __forceinline__ void load8(const char* p, float (&f)[8], int n) {
-  if (AL || n >= 8) {
-    uint4 a, b;
-    __builtin_memcpy(&a, AL ? __builtin_assume_aligned(p, 16) : p, 16);
-    if (T == T_F32) {
-      __builtin_memcpy(&b, AL ? __builtin_assume_aligned(p + 16, 16) : p + 16, 16);
-      f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z), f[3] = __uint_as_float(a.w);
-      f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
-    } else {
-      f[0] = bf16_lo(a.x), f[1] = bf16_hi(a.x), f[2] = bf16_lo(a.y), f[3] = bf16_hi(a.y);
-      f[4] = bf16_lo(a.z), f[5] = bf16_hi(a.z), f[6] = bf16_lo(a.w), f[7] = bf16_hi(a.w);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      f[k] = 0.0f;
-      if (k < n)
-        f[k] = T == T_F32 ? reinterpret_cast<const float*>(p)[k]
-                          : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[k] << 16);
-    }
-  }
-}
-template <int T, bool AL>
-__device__ __forceinline__ void store8(char* p, const float (&f)[8], int n) {
-  if (AL || n >= 8) {
-    if (T == T_F32) {
-      const float4 a = make_float4(f[0], f[1], f[2], f[3]), b = make_float4(f[4], f[5], f[6], f[7]);
-      __builtin_memcpy(AL ? __builtin_assume_aligned(p, 16) : p, &a, 16);
-      __builtin_memcpy(AL ? __builtin_assume_aligned(p + 16, 16) : p + 16, &b, 16);
-    } else if (T == T_BF16) {
-      const uint4 a = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-      __builtin_memcpy(AL ? __builtin_assume_aligned(p, 16) : p, &a, 16);
-    } else {
-      const uint2 a = make_uint2(pack_e4m3(f[0], f[1], f[2], f[3]), pack_e4m3(f[4], f[5], f[6], f[7]));
-      __builtin_memcpy(AL ? __builtin_assume_aligned(p, 8) : p, &a, 8);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (k >= n) continue;
-      if (T == T_F32) reinterpret_cast<float*>(p)[k] = f[k];
-      if (T == T_BF16) reinterpret_cast<uint16_t*>(p)[k] = to_bf16(f[k]);
-      if (T == T_E4M3) reinterpret_cast<uint8_t*>(p)[k] = (uint8_t)pack_e4m3(f[k], f[k], f[k], f[k]);
-    }
-  }
-}
-
 // VPT runs of 8 elements a thread.  blockDim.x threads take a row (whole
 // waves) and blockDim.y rows share a workgroup (only rows of one wave, which
 // then need no barrier).  AL: 16-byte aligned rows of a multiple of 8.

@@ -1,0 +1,271 @@
+"""GPU parity of distill_loss with the float64 oracle.
+
+u = 2^-24.  The list's part is float64 on the device.  The sum S over the
+tokens that are not listed is float32: off by e_S = (4 E + D + 4) u of itself, as
+for top_logits (E: the mean of |x - m| / T over them).  So R is off by R e_S, a
+listed token's q by q e_S, and an unlisted one's share q / R by e_S, its own
+exponential (4 u |x - m| / T + 2 u) and the product's roundings (3 u).  That gives
+for the gradient (times w / T) share (R e_S + |R - r| (e_S + 4 u |x - m| / T + 5 u))
+or q e_S, plus u of q + p, and half a step of its type; for the loss w (2 e_S +
+2^-40) and u of itself.  Exponentials below 2^-126 may come out as 0."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import fine_tune as ref
+from tests.harness import log
+from tests.test_gpu_top import U, _t, sum_bound
+
+pytestmark = pytest.mark.gpu
+
+HALF = {"f32": U, "bf16": 2.0 ** -8}
+
+
+def check(x, index, values, lse=None, T=1.0, weight=None, rows=None):
+    """All three ways of calling, against the oracle; returns (loss, grad)."""
+    import torch
+
+    from rejection_sampling_verify_09_amd import distill_loss
+
+    dtype = "f32" if x.dtype == torch.float32 else "bf16"
+    kw = dict(top_lse=lse, temperature=T, weight=weight)
+    loss, grad = distill_loss(x, index, values, with_grad=True, **kw)
+    only, none = distill_loss(x, index, values, **kw)
+    assert none is None and torch.equal(only.nan_to_num(), loss.nan_to_num())
+    none, back = distill_loss(x, index, values, with_loss=False, with_grad=True, **kw)
+    assert none is None and torch.equal(back.nan_to_num(), grad.nan_to_num())
+    place = x.clone()
+    _, g = distill_loss(place, index, values, with_grad=True, out_grad=place, **kw)
+    assert g.data_ptr() == place.data_ptr() and torch.equal(place.nan_to_num(), grad.nan_to_num())
+    V = x.shape[-1]
+    xs, li, gr = x.float().cpu().numpy().astype(np.float64), loss.cpu().numpy(), grad.float().cpu().numpy()
+    idx, val = index.cpu().numpy(), values.cpu().numpy().astype(np.float64)
+    ls = None if lse is None else lse.cpu().numpy().astype(np.float64)
+    ws = np.ones(x.shape[0]) if weight is None else weight.cpu().numpy().astype(np.float64)
+    worst = 0.0
+    for r in range(x.shape[0]) if rows is None else rows:
+        want, g, d = ref.distill_row(xs[r], idx[r], val[r], None if ls is None else ls[r], float(np.float32(T)), ws[r])
+        if d is None:
+            assert li[r] == 0 and not gr[r].any(), r
+            continue
+        w = abs(ws[r])
+        eS = sum_bound(xs[r][~d["listed"]], T, V, dtype) if d["rest"] > -np.inf else 0.0
+        if math.isinf(want):
+            assert li[r] == np.sign(ws[r]) * np.inf, (r, li[r])
+        else:
+            tol = w * (2 * eS + 2.0 ** -40) + U * abs(want)
+            assert abs(float(li[r]) - want) <= tol, (r, li[r], want, tol)
+            worst = max(worst, abs(float(li[r]) - want) / tol)
+        with np.errstate(invalid="ignore", over="ignore"):
+            m = np.max(xs[r][~d["listed"]], initial=-np.inf)
+            t = np.where(d["share"] > 0, np.abs(xs[r] - m) / T, 0.0)
+        e = np.where(d["listed"], d["q"] * eS, d["share"] * (d["R"] * eS + abs(d["R"] - d["r"]) * (eS + 4 * U * t + 5 * U)))
+        mass = np.zeros(V)
+        for i, p in zip(idx[r][(idx[r] >= 0) & (idx[r] < V)], d["p"]):
+            mass[i] += p
+        e = w / T * (e + U * (np.where(d["listed"], d["q"], 0.0) + mass) + 2.0 ** -120)
+        e = e + HALF[dtype] * (np.abs(g) + e) + 2.0 ** -133
+        err = np.abs(gr[r].astype(np.float64) - g)
+        assert np.all(err <= e), (r, np.max(err / e), np.argwhere(err > e)[:4].ravel(), gr[r][err > e][:4], g[err > e][:4])
+        worst = max(worst, float(np.max(err / e)))
+    log(f"   worst err / bound {worst:.3g}")
+    return loss, grad
+
+
+def teacher(rows, V, k, dtype, T, g, spread=2.0, near=0.7):
+    """(student's logits, index, values, lse) as a program makes them."""
+    import torch
+
+    from rejection_sampling_verify_09_amd import top_logits
+
+    t = torch.randn((rows, V), device="cuda", generator=g) * spread
+    values, index, lse = top_logits(t.to(_t(dtype)), min(k, V), temperature=T)
+    return (t + torch.randn((rows, V), device="cuda", generator=g) * near).to(_t(dtype)), index, values, lse
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V,k", [
+    (1, 1, 1), (3, 2, 1), (3, 5, 5), (2, 63, 10), (4, 64, 63), (3, 100, 20), (5, 513, 1), (2, 520, 64), (3, 1000, 256),
+    (2, 1500, 1024), (3, 4104, 64), (2, 8193, 20), (90, 2049, 7), (3, 24979, 33), (2, 32000, 8), (3, 128256, 64),
+    (2, 128256, 1024), (2, 152064, 256), (1, 262145, 100), (1, 1048576, 50)])
+def test_matches_the_oracle(rows, V, k, dtype):
+    import torch
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V * 1009 + k)
+    for T, rest, near in ((1.0, True, 0.7), (2.0, False, 0.7), (0.6, True, 0.0)):
+        log(f"[distill] rows={rows} V={V} k={k} {dtype} T={T} rest={rest} near={near}")
+        x, index, values, lse = teacher(rows, V, k, dtype, T, g, near=near)
+        weight = torch.rand((rows,), device="cuda", generator=g) if rest else None
+        check(x, index, values, lse if rest else None, T, weight)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,k", [(70, 12), (4099, 64), (128256, 130)])
+def test_lists(V, k, dtype, rest):
+    """Absent entries, tokens twice and more often, in any order, teachers with
+    nothing, masked by -inf and by the lowest value; rows of weight 0."""
+    import torch
+
+    log(f"[distill] lists V={V} k={k} {dtype} rest={rest}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V + k)
+    rows, inf = 12, float("inf")
+    x, index, values, lse = teacher(rows, V, k, dtype, 1.0, g)
+    order = torch.randperm(k, device="cuda", generator=g)
+    index, values = index[:, order].contiguous(), values[:, order].contiguous()
+    index[0, ::3] = -1
+    values[0, ::3] = float("nan")          # whatever an absent entry holds
+    index[1, 5], index[1, 6], index[1, 7] = V, 2 ** 31 - 1, -2 ** 31
+    index[2, 1] = index[2, 0]              # twice
+    index[3] = index[3, 0]                 # one token alone, k times
+    values[3] = values[3, 0] - math.log(k)
+    index[4] = -1                          # nobody
+    values[5, 2:] = -inf                   # masked: the others have the mass
+    values[6] = -inf                       # nothing left
+    lse[6] = -inf
+    values[7, 3:] = torch.finfo(torch.float32).min
+    index[8, k // 2:] = index[8, :k - k // 2]  # pairs, the second with a value of its own
+    values[8, k // 2:] -= 1.0
+    weight = torch.rand((rows,), device="cuda", generator=g) + 0.5
+    weight[9] = 0.0
+    x[9, ::2] = float("nan")               # a row left out is not looked at
+    weight[10] = -1.5                      # a gradient that arrives from above has any sign
+    if rest:
+        lse[5] = torch.logsumexp(values[5, :2], 0) + 0.1
+        lse[8] += math.log(2.0)
+    loss, grad = check(x, index, values, lse if rest else None, 1.0, weight)
+    assert loss[9].item() == 0 and not grad[9].any() and loss[6].item() == 0 and not grad[6].any()
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [66, 5001, 128256])
+def test_students(V, dtype, rest):
+    """Masked student logits, a student that is sure of itself, and one with
+    nothing left."""
+    import torch
+
+    log(f"[distill] students V={V} {dtype} rest={rest}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    rows, k, inf = 9, 16, float("inf")
+    x, index, values, lse = teacher(rows, V, k, dtype, 1.0, g)
+    listed = torch.zeros((rows, V), device="cuda", dtype=torch.bool).scatter_(1, index.long(), True)
+    x[0] = torch.where(listed[0], x[0], -inf)      # nothing but the list
+    x[1] = torch.where(listed[1], -inf, x[1])      # nothing of the list
+    x[2, index[2, 3].long()] = -inf                # one listed token masked: infinite divergence
+    x[3] = -inf                                    # no softmax at all
+    x[4, index[4, 0].long()] += 300.0              # the rest's mass is below float32's range
+    x[5] = torch.where(listed[5], x[5] - 300.0, x[5])  # the list's is
+    x[6, ::3] = -inf
+    x[6, index[6].long()] = values[6].to(x.dtype)
+    x[7] = torch.finfo(x.dtype).min                # masked by the lowest value
+    x[7, index[7].long()] = values[7].to(x.dtype)
+    loss, grad = check(x, index, values, lse if rest else None)
+    assert loss[2].item() == inf and loss[3].item() == inf and torch.isfinite(grad).all()
+    for bad in (float("nan"), inf):
+        for at in (int(index[8, 2]), int((~listed[8]).nonzero()[5])):
+            z = x.clone()
+            z[8, at] = bad
+            from rejection_sampling_verify_09_amd import distill_loss
+
+            lz, gz = distill_loss(z, index, values, top_lse=lse if rest else None, with_grad=True)
+            assert torch.isnan(lz[8]) and torch.isnan(gz[8]).all()
+            assert torch.equal(lz[:8], loss[:8]) and torch.equal(gz[:8], grad[:8])
+
+
+@pytest.mark.parametrize("T", [1e-3, 0.05, 20.0, 1e6])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_temperatures(T, dtype):
+    import torch
+
+    log(f"[distill] T={T} {dtype}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x, index, values, lse = teacher(4, 3001, 32, dtype, T, g)
+    check(x, index, values, lse, T)
+    check(x, index, values, None, T)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_gradient_is_the_loss_s_difference(dtype):
+    """The device's own loss, in float64 steps of the logits that their type
+    holds: central differences with steps of 2^-4 (second order: the third
+    derivative of the loss, below w / T^3, times h^2 / 6)."""
+    import torch
+
+    from rejection_sampling_verify_09_amd import distill_loss
+
+    log(f"[distill] differences {dtype}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    V, k, h = 40, 6, 2.0 ** -4
+    x = (torch.randn((1, V), device="cuda", generator=g) * 2).mul(16).round().div(16).to(_t(dtype)).clamp(-7, 7)
+    t = torch.randn((1, V), device="cuda", generator=g) * 2
+    values, index = t.topk(k, 1)
+    index = index.int()
+    for lse in (None, t.logsumexp(1)):
+        _, grad = distill_loss(x, index, values, top_lse=lse, with_grad=True)
+        step = torch.eye(V, device="cuda").to(x.dtype) * h
+        up, down = x + step, x - step
+        assert torch.equal((up.float() - down.float()), 2 * step.float())  # exact steps
+        many = lambda v: None if v is None else v.expand(V, *v.shape[1:]).contiguous()  # noqa: E731
+        a, _ = distill_loss(up, many(index), many(values), top_lse=many(lse))
+        b, _ = distill_loss(down, many(index), many(values), top_lse=many(lse))
+        diff = (a.double() - b.double()) / (2 * h)
+        # losses of up to 8, rounded to 2^-22, over 2 h; the differences' own error h^2 / 6; the gradient's half step
+        tol = 2 * 2.0 ** -22 / (2 * h) + h * h / 6 + HALF[dtype] * grad[0].double().abs()
+        assert torch.all((diff - grad[0].double()).abs() <= tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1000, 24979, 128256])
+def test_misaligned_rows_and_margins(V, dtype):
+    import torch
+
+    from rejection_sampling_verify_09_amd import distill_loss
+
+    log(f"[distill] misaligned V={V} {dtype}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    t, rows, k = _t(dtype), 5, 48
+    x, index, values, lse = teacher(rows, V, k, dtype, 1.0, g)
+    want = distill_loss(x, index, values, top_lse=lse, with_grad=True)
+    buf = torch.full((rows * V + 32,), 1e30, device="cuda", dtype=t)
+    buf[1:1 + rows * V] = x.view(-1)
+    og = torch.full((rows * V + 32,), 7.0, device="cuda", dtype=t)
+    ol = torch.full((rows + 9,), 7.0, device="cuda")
+    got = distill_loss(buf[1:1 + rows * V].view(rows, V), index, values, top_lse=lse, with_grad=True,
+                       out_loss=ol[1:1 + rows], out_grad=og[1:1 + rows * V].view(rows, V))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert og[0].item() == 7 and (og[1 + rows * V:] == 7).all() and ol[0].item() == 7 and (ol[1 + rows:] == 7).all()
+    assert (buf[1 + rows * V:] == buf[0]).all()
+
+
+def test_empty_batches_and_leading_dimensions():
+    import torch
+
+    from rejection_sampling_verify_09_amd import distill_loss
+
+    i32 = torch.int32
+    loss, grad = distill_loss(torch.empty((0, 50), device="cuda"), torch.empty((0, 3), device="cuda", dtype=i32),
+                              torch.empty((0, 3), device="cuda"), with_grad=True)
+    assert loss.shape == (0,) and grad.shape == (0, 50)
+    x, v = torch.randn((2, 3, 50), device="cuda"), torch.randn((2, 3, 4), device="cuda")
+    i = torch.randint(0, 50, (2, 3, 4), device="cuda", dtype=i32)
+    loss, grad = distill_loss(x, i, v, with_grad=True)
+    flat = distill_loss(x.view(6, 50), i.view(6, 4), v.view(6, 4), with_grad=True)
+    assert torch.equal(loss.view(6), flat[0]) and torch.equal(grad.view(6, 50), flat[1]) and loss.shape == (2, 3)
+
+
+def test_more_rows_than_compute_units_hold():
+    import torch
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    log("[distill] 20000 rows of 300")
+    x, index, values, lse = teacher(20000, 300, 12, "bf16", 1.0, g)
+    check(x, index, values, lse, rows=list(range(0, 20000, 1999)) + [19999])
