@@ -17,6 +17,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 namespace sv {
 
@@ -34,22 +35,30 @@ struct LayerArgs {
   float eps;
 };
 
-// Sums of A values over the workgroup's nw waves, in a fixed order; part:
-// [A * 16] floats that nothing else uses until the next barrier but one.
+// Sums of A values over the nw waves that share `part` (A * 16 floats, which
+// nothing else uses until the next barrier but one), in a fixed order, to all of
+// their threads.  Waves first; then each lane takes one wave's sum and 16 lanes
+// add theirs, instead of every lane adding all of them.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += __uint_as_float(dpp_mov<DPP_QP_1032>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_mov<DPP_QP_2301>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_mov<DPP_HALF_MIRROR>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_mov<DPP_MIRROR>(__float_as_uint(v)));
+  return v;
+}
 template <int A>
 __device__ __forceinline__ void group_sum(float (&v)[A], float* part, int nw) {
 #pragma unroll
   for (int i = 0; i < A; ++i) v[i] = dpp_wave_fsum(v[i]);
   if (nw == 1) return;
-  if ((threadIdx.x & 63) == 0)
+  const int lane = threadIdx.x & 63;
+  if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < A; ++i) part[i * 16 + (threadIdx.x >> 6)] = v[i];
+    for (int i = 0; i < A; ++i) part[(threadIdx.x >> 6) * A + i] = v[i];
   __syncthreads();
+  const int w = lane & 15;
 #pragma unroll
-  for (int i = 0; i < A; ++i) {
-    v[i] = 0.0f;
-    for (int k = 0; k < nw; ++k) v[i] += part[i * 16 + k];
-  }
+  for (int i = 0; i < A; ++i) v[i] = row16_sum(w < nw ? part[w * A + i] : 0.0f);
 }
 
 // VPT runs of 8 elements a thread.  blockDim.x threads take a row (whole
@@ -204,82 +213,334 @@ struct BackArgs {
   const void* w;
   const void* dres;
   void* dh;
-  float* dw;  // [groups][d] sums over each workgroup's rows, or NULL
+  float* dw;  // [groups][stride] sums over each workgroup's rows, or NULL
   float* db;
-  int32_t rows, d;
+  int32_t rows, d, stride;
   float eps;
 };
 
-// A workgroup takes rows blockIdx.x, blockIdx.x + gridDim.x, ..; its sums for
-// the weights stand in its own part of the workspace.
-template <int IN, bool CENTER>
+// What the sums over one row give: the factors of
+// dh = r (g - gm - (c - left) r gn).
+struct RowBack {
+  float left, r, gm, gn;
+  // mom: sums of c, c^2, g and g c
+  template <bool CENTER>
+  __device__ __forceinline__ void set(const float (&mom)[4], float n, float eps) {
+    left = CENTER ? mom[0] / n : 0.0f;
+    const float var = fmaxf(mom[1] / n - left * left, 0.0f) + eps;
+    r = mom[1] < INFINITY && var < INFINITY ? rsqrtf(var) : NAN;
+    const float g = mom[2] / n;
+    gm = CENTER ? g : 0.0f;
+    gn = (mom[3] / n - left * g) * r;
+  }
+};
+
+// Eight elements as they lie in memory: half the registers of floats for
+// bfloat16, so that the next row can be on its way.
+template <int IN>
+struct Raw8 {
+  uint4 v[IN == T_F32 ? 2 : 1];
+  template <bool AL>
+  __device__ __forceinline__ void load(const char* p, int n) {
+    if (AL || n >= 8) {
+      __builtin_memcpy(v, AL ? __builtin_assume_aligned(p, 16) : p, sizeof(v));
+    } else {
+      uint32_t u[sizeof(v) / 4];
+#pragma unroll
+      for (int i = 0; i < (int)(sizeof(v) / 4); ++i) u[i] = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < n) {
+          if (IN == T_F32)
+            u[k] = reinterpret_cast<const uint32_t*>(p)[k];
+          else
+            u[k / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[k] << (k % 2 * 16);
+        }
+      __builtin_memcpy(v, u, sizeof(v));
+    }
+  }
+  __device__ __forceinline__ float operator[](int k) const {
+    uint32_t u[sizeof(v) / 4];
+    __builtin_memcpy(u, v, sizeof(v));
+    return IN == T_F32 ? __uint_as_float(u[k]) : k & 1 ? bf16_hi(u[k / 2]) : bf16_lo(u[k / 2]);
+  }
+};
+
+// One pass: blockDim.x threads take a row, VPT runs of 8 columns each, and keep
+// their columns' sums for the weights in registers over all of their rows;
+// blockDim.y rows are under way in a workgroup, and their sums are joined at
+// the end.  Rows (blockIdx.x + i gridDim.x) blockDim.y + threadIdx.y.  The next
+// row is loaded before this one's reductions.
+template <int IN, bool CENTER, int VPT, bool AL, bool RES>
 __global__ void __launch_bounds__(1024) norm_backward_kernel(BackArgs a) {
-  __shared__ float part[2][5][16];
+  extern __shared__ __attribute__((aligned(16))) float smem[];
+  const int t = threadIdx.x, nt = blockDim.x, nw = nt >> 6, ny = blockDim.y;
+  float* part = smem + threadIdx.y * 160;  // [2][16 + 4 * 16]
+  constexpr int IB = IN == T_F32 ? 4 : 2;
+  const float n = (float)a.d;
+  const char *hp = static_cast<const char*>(a.h), *dyp = static_cast<const char*>(a.dy),
+             *rp = static_cast<const char*>(a.dres);
+  Raw8<IN> w[VPT], h[VPT], dy[VPT], dr[RES ? VPT : 1];
+  float sw[VPT][8], sb[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int j = (t + i * nt) * 8;
+    w[i] = Raw8<IN>{};
+    if (a.w && j < a.d) w[i].template load<AL>(static_cast<const char*>(a.w) + (size_t)j * IB, a.d - j);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sw[i][k] = sb[i][k] = 0.0f;
+  }
+  auto fetch = [&](int row) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int j = (t + i * nt) * 8;
+      const size_t at = ((size_t)row * a.d + j) * IB;
+      h[i] = dy[i] = Raw8<IN>{};
+      if (RES) dr[i] = Raw8<IN>{};
+      if (j < a.d && row < a.rows) {
+        h[i].template load<AL>(hp + at, a.d - j);
+        dy[i].template load<AL>(dyp + at, a.d - j);
+        if (RES) dr[i].template load<AL>(rp + at, a.d - j);
+      }
+    }
+  };
+  int row = blockIdx.x * ny + threadIdx.y;
+  const int step = gridDim.x * ny;
+  fetch(row);
+  // every row of the workgroup's turns, so that all of its waves meet at the barriers
+  for (int turn = 0, first = blockIdx.x * ny; first < a.rows; first += step, row += step, turn ^= 1) {
+    float c[VPT][8], g[VPT][8], mom[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float mean = 0.0f;
+    if (CENTER) {
+      float sum[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[0] += h[i][k];
+      group_sum(sum, part + turn * 80, nw);
+      mean = sum[0] / n;
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int j = (t + i * nt) * 8;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        c[i][k] = h[i][k];
+        if (CENTER) c[i][k] = (AL ? j < a.d : j + k < a.d) ? c[i][k] - mean : 0.0f;
+        g[i][k] = a.w ? dy[i][k] * w[i][k] : dy[i][k];
+        mom[1] += c[i][k] * c[i][k];
+        mom[3] += g[i][k] * c[i][k];
+        if (CENTER) mom[0] += c[i][k], mom[2] += g[i][k];
+      }
+    }
+    group_sum(mom, part + turn * 80 + 16, nw);
+    RowBack f;
+    f.template set<CENTER>(mom, n, a.eps);
+    const bool mine = row < a.rows;
+    Raw8<IN> dyc[VPT], drc[RES ? VPT : 1];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      dyc[i] = dy[i];
+      if (RES) drc[i] = dr[i];
+    }
+    const size_t base = (size_t)row * a.d;
+    if (first + step < a.rows) fetch(row + step);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int j = (t + i * nt) * 8;
+      if (mine && j < a.d) {
+        float o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float v = (c[i][k] - f.left) * f.r;
+          sw[i][k] += dyc[i][k] * v;
+          if (CENTER) sb[i][k] += dyc[i][k];
+          o[k] = f.r * (g[i][k] - f.gm - v * f.gn);
+          if (RES) o[k] += drc[i][k];
+        }
+        store8<IN, AL>(static_cast<char*>(a.dh) + (base + j) * IB, o, a.d - j);
+      }
+    }
+  }
+  if (!a.dw && !a.db) return;
+  // rows of the workgroup, then the workgroup's part of the workspace
+  if (ny > 1) {
+    float* join = smem + ny * 160 + (size_t)t * (VPT * 8);
+    for (int y = 1; y < ny; ++y) {
+      __syncthreads();
+      if ((int)threadIdx.y == y)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            join[i * 8 + k] = sw[i][k];
+            if (CENTER) join[(size_t)nt * VPT * 8 + i * 8 + k] = sb[i][k];
+          }
+      __syncthreads();
+      if (threadIdx.y == 0)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            sw[i][k] += join[i * 8 + k];
+            if (CENTER) sb[i][k] += join[(size_t)nt * VPT * 8 + i * 8 + k];
+          }
+    }
+    if (threadIdx.y != 0) return;
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int j = (t + i * nt) * 8;
+    if (j < a.d) {
+      const size_t at = (size_t)blockIdx.x * a.stride + j;
+      if (a.dw) store8<T_F32, false>(reinterpret_cast<char*>(a.dw + at), sw[i], a.d - j);
+      if (CENTER && a.db) store8<T_F32, false>(reinterpret_cast<char*>(a.db + at), sb[i], a.d - j);
+    }
+  }
+}
+
+// Rows too wide for that (above 16384 columns): a workgroup takes a row at a
+// time, reads it again for each step, and keeps the sums for the weights in its
+// part of the workspace.
+template <int IN, bool CENTER>
+__global__ void __launch_bounds__(1024) norm_backward_wide_kernel(BackArgs a) {
+  __shared__ float part[2][80];
   const int t = threadIdx.x, nt = blockDim.x, nw = nt >> 6;
   constexpr int IB = IN == T_F32 ? 4 : 2;
   const float n = (float)a.d;
-  float* dw = a.dw ? a.dw + (size_t)blockIdx.x * a.d : nullptr;
-  float* db = a.db ? a.db + (size_t)blockIdx.x * a.d : nullptr;
+  float* dw = a.dw ? a.dw + (size_t)blockIdx.x * a.stride : nullptr;
+  float* db = a.db ? a.db + (size_t)blockIdx.x * a.stride : nullptr;
   int turn = 0;
   for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
     const size_t base = (size_t)row * a.d;
     const char* hp = static_cast<const char*>(a.h) + base * IB;
     const char* dyp = static_cast<const char*>(a.dy) + base * IB;
+    const char* wp = static_cast<const char*>(a.w);
     float mean = 0.0f;
     if (CENTER) {
       float sum[1] = {0.0f};
-      for (int j = t; j < a.d; j += nt) sum[0] += load1<IN>(hp, j);
-      group_sum(sum, part[turn][0], nw);
+      for (int j = t * 8; j < a.d; j += nt * 8) {
+        float h[8];
+        load8<IN, false>(hp + (size_t)j * IB, h, a.d - j);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[0] += h[k];
+      }
+      group_sum(sum, part[turn], nw);
       mean = sum[0] / n;
     }
-    // sums of c, c^2, g and g c for c = h - mean
     float mom[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = t; j < a.d; j += nt) {
-      const float c = load1<IN>(hp, j) - mean;
-      const float g = load1<IN>(dyp, j) * (a.w ? load1<IN>(static_cast<const char*>(a.w), j) : 1.0f);
-      mom[0] += c;
-      mom[1] += c * c;
-      mom[2] += g;
-      mom[3] += g * c;
+    float h[8], dy[8], w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = 1.0f;
+    for (int j = t * 8; j < a.d; j += nt * 8) {
+      load8<IN, false>(hp + (size_t)j * IB, h, a.d - j);
+      load8<IN, false>(dyp + (size_t)j * IB, dy, a.d - j);
+      if (wp) load8<IN, false>(wp + (size_t)j * IB, w, a.d - j);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float c = j + k < a.d ? h[k] - mean : 0.0f, g = dy[k] * w[k];
+        mom[0] += c;
+        mom[1] += c * c;
+        mom[2] += g;
+        mom[3] += g * c;
+      }
     }
-    group_sum(mom, part[turn][1], nw);
-    const float left = CENTER ? mom[0] / n : 0.0f;
-    const float var = fmaxf(mom[1] / n - left * left, 0.0f) + a.eps;
-    const float r = mom[1] < INFINITY && var < INFINITY ? rsqrtf(var) : NAN;
-    const float gm = CENTER ? mom[2] / n : 0.0f;
-    const float gn = (mom[3] / n - left * (mom[2] / n)) * r;
-    for (int j = t; j < a.d; j += nt) {
-      const float v = (load1<IN>(hp, j) - mean - left) * r;
-      const float dy = load1<IN>(dyp, j);
-      const float g = dy * (a.w ? load1<IN>(static_cast<const char*>(a.w), j) : 1.0f);
-      float dh = r * (g - gm - v * gn);
-      if (a.dres) dh += load1<IN>(static_cast<const char*>(a.dres) + base * IB, j);
-      store1<IN>(static_cast<char*>(a.dh) + base * IB, j, dh);
-      if (dw) dw[j] = (row < (int)gridDim.x ? 0.0f : dw[j]) + dy * v;
-      if (db) db[j] = (row < (int)gridDim.x ? 0.0f : db[j]) + dy;
+    group_sum(mom, part[turn] + 16, nw);
+    RowBack f;
+    f.template set<CENTER>(mom, n, a.eps);
+    for (int j = t * 8; j < a.d; j += nt * 8) {
+      float o[8], sw[8], sb[8];
+      load8<IN, false>(hp + (size_t)j * IB, h, a.d - j);
+      load8<IN, false>(dyp + (size_t)j * IB, dy, a.d - j);
+      if (wp) load8<IN, false>(wp + (size_t)j * IB, w, a.d - j);
+      if (a.dres) load8<IN, false>(static_cast<const char*>(a.dres) + (base + j) * IB, o, a.d - j);
+      const bool begun = row >= (int)gridDim.x;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sw[k] = sb[k] = 0.0f;
+      if (begun && dw) load8<T_F32, false>(reinterpret_cast<char*>(dw + j), sw, a.d - j);
+      if (begun && db) load8<T_F32, false>(reinterpret_cast<char*>(db + j), sb, a.d - j);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float v = (h[k] - mean - f.left) * f.r, g = dy[k] * w[k];
+        const float dh = f.r * (g - f.gm - v * f.gn);
+        o[k] = a.dres ? dh + o[k] : dh;
+        sw[k] += dy[k] * v;
+        sb[k] += dy[k];
+      }
+      store8<IN, false>(static_cast<char*>(a.dh) + (base + j) * IB, o, a.d - j);
+      if (dw) store8<T_F32, false>(reinterpret_cast<char*>(dw + j), sw, a.d - j);
+      if (db) store8<T_F32, false>(reinterpret_cast<char*>(db + j), sb, a.d - j);
     }
   }
 }
 
-// Column sums of the workgroups' parts, in their order.
-__global__ void __launch_bounds__(256) norm_backward_sum_kernel(const float* wp, const float* bp, float* dw, float* db,
-                                                                int groups, int d) {
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  if (j >= d) return;
-  if (dw) {
-    float s = 0.0f;
-    for (int g = 0; g < groups; ++g) s += wp[(size_t)g * d + j];
-    dw[j] = s;
-  }
-  if (db) {
-    float s = 0.0f;
-    for (int g = 0; g < groups; ++g) s += bp[(size_t)g * d + j];
-    db[j] = s;
-  }
+// Column sums of the workgroups' parts: 64 columns a workgroup, 16 threads of 4
+// columns side by side and 64 parts at a time, joined in a fixed order.
+__global__ void __launch_bounds__(1024) norm_backward_sum_kernel(const float* wp, const float* bp, float* dw, float* db,
+                                                                 int groups, int d, int stride) {
+  __shared__ float4 join[16][16];
+  const float* p = blockIdx.y ? bp : wp;
+  float* out = blockIdx.y ? db : dw;
+  if (!out) return;
+  const int q = threadIdx.x & 15, at = threadIdx.x >> 4, j = blockIdx.x * 64 + q * 4;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (j < d)
+    for (int g = at; g < groups; g += 64) {
+      const float4 v = *reinterpret_cast<const float4*>(p + (size_t)g * stride + j);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+#pragma unroll
+  for (int o = 16; o < 64; o <<= 1)
+    s.x += __shfl_xor(s.x, o), s.y += __shfl_xor(s.y, o), s.z += __shfl_xor(s.z, o), s.w += __shfl_xor(s.w, o);
+  if ((threadIdx.x & 63) < 16) join[threadIdx.x >> 6][q] = s;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  const int col = blockIdx.x * 64 + threadIdx.x;
+  if (col >= d) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v += reinterpret_cast<const float*>(join[i])[threadIdx.x];
+  out[col] = v;
 }
 
-// Workgroups of the backward pass: what the workspace holds a part for.
-int back_groups(int rows) { return std::min(rows, 512); }
+// A row's threads and runs, rows a workgroup, and workgroups: what the workspace
+// holds a part for.
+struct BackPlan {
+  int nt, ny, vpt, groups, stride;
+  bool wide;
+  BackPlan(int rows, int d) {
+    const int nv = (d + 7) / 8;
+    wide = nv > 2048;
+    vpt = nv > 1024 ? 2 : 1;
+    nt = std::min(1024, ((nv + vpt - 1) / vpt + 63) / 64 * 64);
+    ny = wide || nt >= 512 ? 1 : std::min(8, 512 / nt);
+    const int turns = (rows + ny - 1) / ny;
+    groups = turns <= 4 ? std::min(turns, 1) : std::min(turns, 512);
+    stride = (d + 3) / 4 * 4;
+  }
+  size_t lds() const { return ((size_t)ny * 160 + (ny > 1 ? (size_t)nt * vpt * 16 : 0)) * 4; }
+};
+
+template <int IN, bool CENTER>
+hipError_t launch_back(const BackArgs& a, const BackPlan& l, hipStream_t s) {
+  const dim3 grid((unsigned)l.groups), wg((unsigned)l.nt, (unsigned)l.ny);
+  if (l.wide) {
+    hipLaunchKernelGGL((norm_backward_wide_kernel<IN, CENTER>), grid, wg, 0, s, a);
+    return hipGetLastError();
+  }
+  const bool al = a.d % 8 == 0 && is_aligned(a.dy, 16) && is_aligned(a.h, 16) && is_aligned(a.w, 16) &&
+                  is_aligned(a.dres, 16) && is_aligned(a.dh, 16);
+  auto go = [&](auto vpt, auto aligned, auto res) {
+    hipLaunchKernelGGL((norm_backward_kernel<IN, CENTER, decltype(vpt)::value, decltype(aligned)::value, decltype(res)::value>),
+                       grid, wg, l.lds(), s, a);
+  };
+  auto pick = [&](auto vpt, auto aligned) {
+    a.dres ? go(vpt, aligned, std::true_type{}) : go(vpt, aligned, std::false_type{});
+  };
+  auto width = [&](auto vpt) { al ? pick(vpt, std::true_type{}) : pick(vpt, std::false_type{}); };
+  l.vpt == 1 ? width(std::integral_constant<int, 1>{}) : width(std::integral_constant<int, 2>{});
+  return hipGetLastError();
+}
 
 int norm_backward(bool center, const void* grad, const void* h, const void* weight, const void* grad_residual, float eps,
                   void* grad_h, float* grad_weight, float* grad_bias, void* workspace, int64_t workspace_bytes,
@@ -287,9 +548,10 @@ int norm_backward(bool center, const void* grad, const void* h, const void* weig
   if (rows < 0 || d < 1 || d > SV_MAX_NORM_D) return SV_ERR_SHAPE;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
   if (!(eps > 0.0f) || !std::isfinite(eps)) return SV_ERR_PARAM;
-  const int groups = back_groups(rows);
+  const BackPlan l(rows, d);
+  const int groups = l.groups;
   const size_t ie = (size_t)type_bytes(dtype), nin = (size_t)rows * (size_t)d * ie, nw = (size_t)d * ie;
-  const size_t np = (size_t)d * 4, one = (size_t)groups * np;
+  const size_t np = (size_t)d * 4, one = (size_t)groups * (size_t)l.stride * 4;
   const size_t ws = groups > 1 ? one * ((grad_weight ? 1 : 0) + (grad_bias ? 1 : 0)) : 0;
   if (rows > 0 && (!grad || !h || !grad_h)) return SV_ERR_NULL;
   if (ws && !workspace) return SV_ERR_NULL;
@@ -323,25 +585,15 @@ int norm_backward(bool center, const void* grad, const void* h, const void* weig
   char* part = static_cast<char*>(workspace);
   a.dw = !grad_weight ? nullptr : groups > 1 ? reinterpret_cast<float*>(part) : grad_weight;
   a.db = !grad_bias ? nullptr : groups > 1 ? reinterpret_cast<float*>(part + (grad_weight ? one : 0)) : grad_bias;
+  a.stride = l.stride;
   if (rows > 0) {
-    const dim3 grid((unsigned)groups), wg((unsigned)std::min(1024, (d + 63) / 64 * 64));
-    if (center) {
-      if (dtype == SV_F32)
-        hipLaunchKernelGGL((norm_backward_kernel<T_F32, true>), grid, wg, 0, s, a);
-      else
-        hipLaunchKernelGGL((norm_backward_kernel<T_BF16, true>), grid, wg, 0, s, a);
-    } else {
-      if (dtype == SV_F32)
-        hipLaunchKernelGGL((norm_backward_kernel<T_F32, false>), grid, wg, 0, s, a);
-      else
-        hipLaunchKernelGGL((norm_backward_kernel<T_BF16, false>), grid, wg, 0, s, a);
-    }
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = center ? (dtype == SV_F32 ? launch_back<T_F32, true>(a, l, s) : launch_back<T_BF16, true>(a, l, s))
+                                : (dtype == SV_F32 ? launch_back<T_F32, false>(a, l, s) : launch_back<T_BF16, false>(a, l, s));
     if (e != hipSuccess) return SV_ERR_HIP;
   }
   if (groups != 1 && (grad_weight || grad_bias)) {
-    hipLaunchKernelGGL(norm_backward_sum_kernel, dim3((unsigned)((d + 255) / 256)), dim3(256), 0, s, a.dw, a.db,
-                       grad_weight, grad_bias, groups, d);
+    hipLaunchKernelGGL(norm_backward_sum_kernel, dim3((unsigned)((d + 63) / 64), grad_bias ? 2 : 1), dim3(1024), 0, s, a.dw,
+                       a.db, grad_weight, grad_bias, groups, d, l.stride);
     if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
   }
   return SV_OK;
@@ -403,8 +655,8 @@ extern "C" int sv_layer_norm(const void* x, const void* residual, const void* we
 
 extern "C" int64_t sv_norm_backward_workspace(int32_t rows, int32_t d) {
   if (rows < 0 || d < 1 || d > SV_MAX_NORM_D) return SV_ERR_SHAPE;
-  const int groups = back_groups(rows);
-  return groups > 1 ? (int64_t)groups * d * 8 : 0;
+  const BackPlan l(rows, d);
+  return l.groups > 1 ? (int64_t)l.groups * l.stride * 8 : 0;
 }
 
 extern "C" int sv_layer_norm_backward(const void* grad, const void* h, const void* weight, const void* grad_residual,
