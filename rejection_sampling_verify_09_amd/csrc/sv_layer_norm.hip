@@ -35,8 +35,8 @@ struct LayerArgs {
   float eps;
 };
 
-// Sums of A values over the nw waves that share `part` (A * 16 floats, which
-// nothing else uses until the next barrier but one), in a fixed order, to all of
+// Sums of A values over the nw waves that share `part` (A * 16 floats, 16-byte
+// aligned, which nothing else uses until the next barrier but one), in a fixed order, to all of
 // their threads.  Waves first; then each lane takes one wave's sum and 16 lanes
 // add theirs, instead of every lane adding all of them.
 __device__ __forceinline__ float row16_sum(float v) {
@@ -52,13 +52,13 @@ __device__ __forceinline__ void group_sum(float (&v)[A], float* part, int nw) {
   for (int i = 0; i < A; ++i) v[i] = dpp_wave_fsum(v[i]);
   if (nw == 1) return;
   const int lane = threadIdx.x & 63;
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < A; ++i) part[(threadIdx.x >> 6) * A + i] = v[i];
+  if (lane == 0) __builtin_memcpy(__builtin_assume_aligned(part + (threadIdx.x >> 6) * A, 4 * A), v, sizeof(v));
   __syncthreads();
   const int w = lane & 15;
+  float o[A];
+  __builtin_memcpy(o, __builtin_assume_aligned(part + min(w, nw - 1) * A, 4 * A), sizeof(o));
 #pragma unroll
-  for (int i = 0; i < A; ++i) v[i] = row16_sum(w < nw ? part[w * A + i] : 0.0f);
+  for (int i = 0; i < A; ++i) v[i] = row16_sum(w < nw ? o[i] : 0.0f);
 }
 
 // VPT runs of 8 elements a thread.  blockDim.x threads take a row (whole
@@ -70,7 +70,7 @@ __device__ __forceinline__ void group_sum(float (&v)[A], float* part, int nw) {
 // each other keeps the bits of their differences.
 template <int IN, int OUT, int VPT, bool AL>
 __global__ void __launch_bounds__(1024) layer_norm_kernel(LayerArgs a) {
-  __shared__ float part[4][16];
+  __shared__ __attribute__((aligned(16))) float part[4][16];
   const int t = threadIdx.x, nt = blockDim.x, nw = nt >> 6;
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= a.rows) return;  // blockDim.y > 1: no barrier follows
@@ -98,14 +98,14 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(LayerArgs a) {
       }
     }
   }
-  const float n = (float)a.d;
+  const float inv = 1.0f / (float)a.d;
   float sum[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum[0] += h[i][k];
   group_sum(sum, part[0], nw);
-  const float mean = sum[0] / n;
+  const float mean = sum[0] * inv;
   float mom[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -115,13 +115,13 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(LayerArgs a) {
     for (int k = 0; k < 8; ++k) {
       h[i][k] = (AL ? j < a.d : j + k < a.d) ? h[i][k] - mean : 0.0f;
       mom[0] += h[i][k];
-      mom[1] += h[i][k] * h[i][k];
+      mom[1] = __builtin_fmaf(h[i][k], h[i][k], mom[1]);
     }
   }
   group_sum(mom, part[1], nw);
-  const float left = mom[0] / n;
+  const float left = mom[0] * inv;
   // a row whose sum is not finite comes out all NaN instead of as zeros
-  const float var = fmaxf(mom[1] / n - left * left, 0.0f) + a.eps;
+  const float var = fmaxf(mom[1] * inv - left * left, 0.0f) + a.eps;
   const float r = mom[1] < INFINITY && var < INFINITY ? rsqrtf(var) : NAN;
   float m = 0.0f;
 #pragma unroll
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(LayerArgs a) {
       if (a.b) load8<IN, AL>(static_cast<const char*>(a.b) + (size_t)j * IB, b, a.d - j);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        h[i][k] = (h[i][k] - left) * r * w[k] + b[k];
+        h[i][k] = __builtin_fmaf((h[i][k] - left) * r, w[k], b[k]);
         if (AL || j + k < a.d) m = fmaxf(m, fabsf(h[i][k]));
       }
       if (OUT != T_E4M3) store8<OUT, AL>(static_cast<char*>(a.out) + (base + j) * OB, h[i], a.d - j);
@@ -223,41 +223,30 @@ struct BackArgs {
 // dh = r (g - gm - (c - left) r gn).
 struct RowBack {
   float left, r, gm, gn;
-  // mom: sums of c, c^2, g and g c
+  // mom: sums of c^2 and g c, and, with a mean, of c and g
   template <bool CENTER>
-  __device__ __forceinline__ void set(const float (&mom)[4], float n, float eps) {
-    left = CENTER ? mom[0] / n : 0.0f;
-    const float var = fmaxf(mom[1] / n - left * left, 0.0f) + eps;
-    r = mom[1] < INFINITY && var < INFINITY ? rsqrtf(var) : NAN;
-    const float g = mom[2] / n;
-    gm = CENTER ? g : 0.0f;
-    gn = (mom[3] / n - left * g) * r;
+  __device__ __forceinline__ void set(const float (&mom)[CENTER ? 4 : 2], float inv, float eps) {
+    left = CENTER ? mom[CENTER ? 2 : 0] * inv : 0.0f;
+    gm = CENTER ? mom[CENTER ? 3 : 0] * inv : 0.0f;
+    const float var = fmaxf(mom[0] * inv - left * left, 0.0f) + eps;
+    r = mom[0] < INFINITY && var < INFINITY ? rsqrtf(var) : NAN;
+    gn = (mom[1] * inv - left * gm) * r;
   }
+  // n_j, and dh_j of it and of dy_j w_j
+  __device__ __forceinline__ float unit(float c) const { return (c - left) * r; }
+  __device__ __forceinline__ float grad(float g, float v) const { return r * __builtin_fmaf(-v, gn, g - gm); }
 };
 
-// Eight elements as they lie in memory: half the registers of floats for
-// bfloat16, so that the next row can be on its way.
+// Eight elements as they lie in memory, at any alignment: half the registers
+// of floats for bfloat16, so that the next row can be on its way.
 template <int IN>
 struct Raw8 {
   uint4 v[IN == T_F32 ? 2 : 1];
-  template <bool AL>
-  __device__ __forceinline__ void load(const char* p, int n) {
-    if (AL || n >= 8) {
-      __builtin_memcpy(v, AL ? __builtin_assume_aligned(p, 16) : p, sizeof(v));
-    } else {
-      uint32_t u[sizeof(v) / 4];
-#pragma unroll
-      for (int i = 0; i < (int)(sizeof(v) / 4); ++i) u[i] = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n) {
-          if (IN == T_F32)
-            u[k] = reinterpret_cast<const uint32_t*>(p)[k];
-          else
-            u[k / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[k] << (k % 2 * 16);
-        }
-      __builtin_memcpy(v, u, sizeof(v));
-    }
+  __device__ __forceinline__ void load(const char* p) { __builtin_memcpy(v, p, sizeof(v)); }
+  __device__ __forceinline__ void ones() {
+    const uint32_t u = IN == T_F32 ? 0x3F800000u : 0x3F803F80u;
+    v[0] = make_uint4(u, u, u, u);
+    if (IN == T_F32) v[1] = v[0];
   }
   __device__ __forceinline__ float operator[](int k) const {
     uint32_t u[sizeof(v) / 4];
@@ -266,102 +255,140 @@ struct Raw8 {
   }
 };
 
-// One pass: blockDim.x threads take a row, VPT runs of 8 columns each, and keep
-// their columns' sums for the weights in registers over all of their rows;
-// blockDim.y rows are under way in a workgroup, and their sums are joined at
-// the end.  Rows (blockIdx.x + i gridDim.x) blockDim.y + threadIdx.y.  The next
-// row is loaded before this one's reductions.
-template <int IN, bool CENTER, int VPT, bool AL, bool RES>
+// One pass over rows of 8 to 16384 columns: blockDim.x threads take a row, VPT
+// runs of 8 columns each, and keep their columns' sums for the weights in
+// registers over all of their rows; blockDim.y rows are under way in a
+// workgroup, and their sums are joined at the end.  Rows (blockIdx.x + i
+// gridDim.x) blockDim.y + threadIdx.y.
+//
+// The next row's loads are issued before this row's second reduction is used,
+// and stay in flight over the stores: no load and no store stands in a branch,
+// since at a branch's end the compiler has to wait for all of them.  So a run
+// that would end past the row begins earlier: it reads, forms and writes some
+// of its neighbour's columns once more, with the same result, and leaves them
+// out of its sums.
+template <int IN, bool CENTER, int VPT, bool RES>
 __global__ void __launch_bounds__(1024) norm_backward_kernel(BackArgs a) {
   extern __shared__ __attribute__((aligned(16))) float smem[];
   const int t = threadIdx.x, nt = blockDim.x, nw = nt >> 6, ny = blockDim.y;
   float* part = smem + threadIdx.y * 160;  // [2][16 + 4 * 16]
-  constexpr int IB = IN == T_F32 ? 4 : 2;
-  const float n = (float)a.d;
+  constexpr int IB = IN == T_F32 ? 4 : 2, S = CENTER ? 4 : 2;
+  constexpr bool AHEAD = VPT == 1;  // two runs a thread have no registers for another row
+  const float inv = 1.0f / (float)a.d;
   const char *hp = static_cast<const char*>(a.h), *dyp = static_cast<const char*>(a.dy),
              *rp = static_cast<const char*>(a.dres);
   Raw8<IN> w[VPT], h[VPT], dy[VPT], dr[RES ? VPT : 1];
   float sw[VPT][8], sb[VPT][8];
+  int js[VPT], skip[VPT];  // the run's first column, and how many of its columns are the neighbour's
+  bool edge = false;       // one of the wave's has some
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int j = (t + i * nt) * 8;
-    w[i] = Raw8<IN>{};
-    if (a.w && j < a.d) w[i].template load<AL>(static_cast<const char*>(a.w) + (size_t)j * IB, a.d - j);
+    js[i] = min(j, a.d - 8);
+    skip[i] = min(j - js[i], 8);
+    w[i].ones();
+    if (a.w) w[i].load(static_cast<const char*>(a.w) + (size_t)js[i] * IB);
+    edge |= __any(skip[i] != 0) != 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) sw[i][k] = sb[i][k] = 0.0f;
   }
   auto fetch = [&](int row) {
+    const size_t base = (size_t)min(row, a.rows - 1) * a.d;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int j = (t + i * nt) * 8;
-      const size_t at = ((size_t)row * a.d + j) * IB;
-      h[i] = dy[i] = Raw8<IN>{};
-      if (RES) dr[i] = Raw8<IN>{};
-      if (j < a.d && row < a.rows) {
-        h[i].template load<AL>(hp + at, a.d - j);
-        dy[i].template load<AL>(dyp + at, a.d - j);
-        if (RES) dr[i].template load<AL>(rp + at, a.d - j);
-      }
+      const size_t at = (base + js[i]) * IB;
+      h[i].load(hp + at);
+      dy[i].load(dyp + at);
+      if (RES) dr[i].load(rp + at);
     }
   };
-  int row = blockIdx.x * ny + threadIdx.y;
+  int row = blockIdx.x * ny + threadIdx.y, turn = 0;
   const int step = gridDim.x * ny;
-  fetch(row);
-  // every row of the workgroup's turns, so that all of its waves meet at the barriers
-  for (int turn = 0, first = blockIdx.x * ny; first < a.rows; first += step, row += step, turn ^= 1) {
-    float c[VPT][8], g[VPT][8], mom[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  // all: each of the workgroup's rows is there (mine: this one is)
+  auto body = [&](auto all, bool mine) {
+    if (!AHEAD) fetch(row);
+    float c[VPT][8], mom[S];
     float mean = 0.0f;
     if (CENTER) {
       float sum[1] = {0.0f};
 #pragma unroll
-      for (int i = 0; i < VPT; ++i)
+      for (int i = 0; i < VPT; ++i) {
+        float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum[0] += h[i][k];
+        for (int k = 0; k < 8; ++k) v += h[i][k];
+        if (edge) {
+          v = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v += k >= skip[i] ? h[i][k] : 0.0f;
+        }
+        sum[0] += v;
+      }
       group_sum(sum, part + turn * 80, nw);
-      mean = sum[0] / n;
+      mean = sum[0] * inv;
     }
+#pragma unroll
+    for (int i = 0; i < S; ++i) mom[i] = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int j = (t + i * nt) * 8;
+      float v[S];
+      auto add = [&](float cc, float g) {
+        v[0] = __builtin_fmaf(cc, cc, v[0]);
+        v[1] = __builtin_fmaf(g, cc, v[1]);
+        if (CENTER) v[S - 2] += cc, v[S - 1] += g;
+      };
+#pragma unroll
+      for (int k = 0; k < S; ++k) v[k] = 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        c[i][k] = h[i][k];
-        if (CENTER) c[i][k] = (AL ? j < a.d : j + k < a.d) ? c[i][k] - mean : 0.0f;
-        g[i][k] = a.w ? dy[i][k] * w[i][k] : dy[i][k];
-        mom[1] += c[i][k] * c[i][k];
-        mom[3] += g[i][k] * c[i][k];
-        if (CENTER) mom[0] += c[i][k], mom[2] += g[i][k];
+        c[i][k] = h[i][k] - mean;
+        add(c[i][k], dy[i][k] * w[i][k]);
       }
+      if (edge) {
+#pragma unroll
+        for (int k = 0; k < S; ++k) v[k] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) add(k >= skip[i] ? c[i][k] : 0.0f, k >= skip[i] ? dy[i][k] * w[i][k] : 0.0f);
+      }
+#pragma unroll
+      for (int k = 0; k < S; ++k) mom[k] += v[k];
     }
-    group_sum(mom, part + turn * 80 + 16, nw);
-    RowBack f;
-    f.template set<CENTER>(mom, n, a.eps);
-    const bool mine = row < a.rows;
     Raw8<IN> dyc[VPT], drc[RES ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       dyc[i] = dy[i];
       if (RES) drc[i] = dr[i];
     }
-    const size_t base = (size_t)row * a.d;
-    if (first + step < a.rows) fetch(row + step);
+    if (AHEAD) fetch(row + step);
+    group_sum(mom, part + turn * 80 + 16, nw);
+    RowBack f;
+    f.template set<CENTER>(mom, inv, a.eps);
+    if (decltype(all)::value || mine) {
+      const size_t base = (size_t)row * a.d;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int j = (t + i * nt) * 8;
-      if (mine && j < a.d) {
+      for (int i = 0; i < VPT; ++i) {
         float o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float v = (c[i][k] - f.left) * f.r;
-          sw[i][k] += dyc[i][k] * v;
-          if (CENTER) sb[i][k] += dyc[i][k];
-          o[k] = f.r * (g[i][k] - f.gm - v * f.gn);
+          const float v = f.unit(c[i][k]), dyk = dyc[i][k];
+          sw[i][k] = __builtin_fmaf(dyk, v, sw[i][k]);
+          if (CENTER) sb[i][k] += dyk;
+          o[k] = f.grad(dyk * w[i][k], v);
           if (RES) o[k] += drc[i][k];
         }
-        store8<IN, AL>(static_cast<char*>(a.dh) + (base + j) * IB, o, a.d - j);
+        store8<IN, false>(static_cast<char*>(a.dh) + (base + js[i]) * IB, o, 8);
       }
     }
+    row += step;
+    turn ^= 1;
+  };
+  int first = blockIdx.x * ny;
+  if (AHEAD) {
+    fetch(row);
+    // all of it: in the loop each wait can then count on the store behind the loads
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   }
+  for (; first + ny <= a.rows; first += step) body(std::true_type{}, true);
+  if (first < a.rows) body(std::false_type{}, row < a.rows);
   if (!a.dw && !a.db) return;
   // rows of the workgroup, then the workgroup's part of the workspace
   if (ny > 1) {
@@ -390,24 +417,22 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(BackArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int j = (t + i * nt) * 8;
-    if (j < a.d) {
-      const size_t at = (size_t)blockIdx.x * a.stride + j;
-      if (a.dw) store8<T_F32, false>(reinterpret_cast<char*>(a.dw + at), sw[i], a.d - j);
-      if (CENTER && a.db) store8<T_F32, false>(reinterpret_cast<char*>(a.db + at), sb[i], a.d - j);
-    }
+    if (skip[i] == 8) continue;
+    const size_t at = (size_t)blockIdx.x * a.stride + js[i];
+    if (a.dw) store8<T_F32, false>(reinterpret_cast<char*>(a.dw + at), sw[i], 8);
+    if (CENTER && a.db) store8<T_F32, false>(reinterpret_cast<char*>(a.db + at), sb[i], 8);
   }
 }
 
-// Rows too wide for that (above 16384 columns): a workgroup takes a row at a
+// Rows of other widths (up to 7, or above 16384 columns): a workgroup takes a row at a
 // time, reads it again for each step, and keeps the sums for the weights in its
 // part of the workspace.
 template <int IN, bool CENTER>
 __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(BackArgs a) {
-  __shared__ float part[2][80];
+  __shared__ __attribute__((aligned(16))) float part[2][80];
   const int t = threadIdx.x, nt = blockDim.x, nw = nt >> 6;
   constexpr int IB = IN == T_F32 ? 4 : 2;
-  const float n = (float)a.d;
+  const float inv = 1.0f / (float)a.d;
   float* dw = a.dw ? a.dw + (size_t)blockIdx.x * a.stride : nullptr;
   float* db = a.db ? a.db + (size_t)blockIdx.x * a.stride : nullptr;
   int turn = 0;
@@ -426,9 +451,12 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(BackArgs a) {
         for (int k = 0; k < 8; ++k) sum[0] += h[k];
       }
       group_sum(sum, part[turn], nw);
-      mean = sum[0] / n;
+      mean = sum[0] * inv;
     }
-    float mom[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int S = CENTER ? 4 : 2;
+    float mom[S];
+#pragma unroll
+    for (int k = 0; k < S; ++k) mom[k] = 0.0f;
     float h[8], dy[8], w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) w[k] = 1.0f;
@@ -439,15 +467,14 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(BackArgs a) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float c = j + k < a.d ? h[k] - mean : 0.0f, g = dy[k] * w[k];
-        mom[0] += c;
-        mom[1] += c * c;
-        mom[2] += g;
-        mom[3] += g * c;
+        mom[0] += c * c;
+        mom[1] += g * c;
+        if (CENTER) mom[S - 2] += c, mom[S - 1] += g;
       }
     }
     group_sum(mom, part[turn] + 16, nw);
     RowBack f;
-    f.template set<CENTER>(mom, n, a.eps);
+    f.template set<CENTER>(mom, inv, a.eps);
     for (int j = t * 8; j < a.d; j += nt * 8) {
       float o[8], sw[8], sb[8];
       load8<IN, false>(hp + (size_t)j * IB, h, a.d - j);
@@ -461,10 +488,9 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(BackArgs a) {
       if (begun && db) load8<T_F32, false>(reinterpret_cast<char*>(db + j), sb, a.d - j);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float v = (h[k] - mean - f.left) * f.r, g = dy[k] * w[k];
-        const float dh = f.r * (g - f.gm - v * f.gn);
+        const float v = f.unit(h[k] - mean), dh = f.grad(dy[k] * w[k], v);
         o[k] = a.dres ? dh + o[k] : dh;
-        sw[k] += dy[k] * v;
+        sw[k] = __builtin_fmaf(dy[k], v, sw[k]);
         sb[k] += dy[k];
       }
       store8<IN, false>(static_cast<char*>(a.dh) + (base + j) * IB, o, a.d - j);
@@ -485,6 +511,7 @@ __global__ void __launch_bounds__(1024) norm_backward_sum_kernel(const float* wp
   const int q = threadIdx.x & 15, at = threadIdx.x >> 4, j = blockIdx.x * 64 + q * 4;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (j < d)
+#pragma unroll 4
     for (int g = at; g < groups; g += 64) {
       const float4 v = *reinterpret_cast<const float4*>(p + (size_t)g * stride + j);
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
@@ -510,12 +537,13 @@ struct BackPlan {
   bool wide;
   BackPlan(int rows, int d) {
     const int nv = (d + 7) / 8;
-    wide = nv > 2048;
+    wide = d < 8 || nv > 2048;
     vpt = nv > 1024 ? 2 : 1;
     nt = std::min(1024, ((nv + vpt - 1) / vpt + 63) / 64 * 64);
     ny = wide || nt >= 512 ? 1 : std::min(8, 512 / nt);
     const int turns = (rows + ny - 1) / ny;
-    groups = turns <= 4 ? std::min(turns, 1) : std::min(turns, 512);
+    const int each = std::max(turns <= 2 ? turns : 1, (turns + 255) / 256);
+    groups = turns == 0 ? 0 : (turns + each - 1) / each;
     stride = (d + 3) / 4 * 4;
   }
   size_t lds() const { return ((size_t)ny * 160 + (ny > 1 ? (size_t)nt * vpt * 16 : 0)) * 4; }
@@ -528,16 +556,10 @@ hipError_t launch_back(const BackArgs& a, const BackPlan& l, hipStream_t s) {
     hipLaunchKernelGGL((norm_backward_wide_kernel<IN, CENTER>), grid, wg, 0, s, a);
     return hipGetLastError();
   }
-  const bool al = a.d % 8 == 0 && is_aligned(a.dy, 16) && is_aligned(a.h, 16) && is_aligned(a.w, 16) &&
-                  is_aligned(a.dres, 16) && is_aligned(a.dh, 16);
-  auto go = [&](auto vpt, auto aligned, auto res) {
-    hipLaunchKernelGGL((norm_backward_kernel<IN, CENTER, decltype(vpt)::value, decltype(aligned)::value, decltype(res)::value>),
-                       grid, wg, l.lds(), s, a);
+  auto go = [&](auto vpt, auto res) {
+    hipLaunchKernelGGL((norm_backward_kernel<IN, CENTER, decltype(vpt)::value, decltype(res)::value>), grid, wg, l.lds(), s, a);
   };
-  auto pick = [&](auto vpt, auto aligned) {
-    a.dres ? go(vpt, aligned, std::true_type{}) : go(vpt, aligned, std::false_type{});
-  };
-  auto width = [&](auto vpt) { al ? pick(vpt, std::true_type{}) : pick(vpt, std::false_type{}); };
+  auto width = [&](auto vpt) { a.dres ? go(vpt, std::true_type{}) : go(vpt, std::false_type{}); };
   l.vpt == 1 ? width(std::integral_constant<int, 1>{}) : width(std::integral_constant<int, 2>{});
   return hipGetLastError();
 }
