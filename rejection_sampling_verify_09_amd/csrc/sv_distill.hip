@@ -10,12 +10,15 @@
 //   grad_v = w / T (q_v - p_v)            v listed
 //          = w / T (q_v / R) (R - r)      v not listed
 //
-// One workgroup takes a row.  The listed tokens are marked in a bitmap in LDS
-// and the streaming passes see the others alone, so that R is a sum of its
-// own and never a difference; q_v / R comes from the rest's own maximum and
-// sum, which no list can underflow.  What is done once an entry is done in 64
-// bits: there are few, and the loss is a difference of numbers close to each
-// other.
+// One workgroup takes a row and keeps it in registers, as it lies in memory,
+// between the sums and the gradient: every logit is read once and written once
+// (rows above 256 KiB: what lies behind that is read twice).  The listed tokens
+// are marked in a bitmap in LDS and set to -inf in the registers, so that R is a
+// sum of its own and never a difference, and q_v / R comes from the rest's own
+// maximum and sum, which no list can underflow.  The sums are formed as the
+// loads arrive, with a running maximum a thread.  What is done once an entry is
+// done in 64 bits: there are few, and the loss is a difference of numbers close
+// to each other.
 #include "sv_ops.hpp"
 #include "specverify.h"
 
@@ -42,100 +45,240 @@ struct DistillArgs {
 };
 
 // In LDS: probabilities, the student's logits and the tokens of the list, [k]
-// each, and the bitmap [ceil(V / 32)].
+// each, and the bitmap.
 inline size_t distill_lds(int V, int k) { return (size_t)k * 16 + (size_t)((V + 31) / 32) * 4; }
 
+// E logits as they lie in memory.
 template <int IN>
+struct Run {
+  static constexpr int E = IN == T_F32 ? 4 : 8, B = IN == T_F32 ? 4 : 2;
+  static constexpr uint32_t NINF = IN == T_F32 ? 0xFF800000u : 0xFF80FF80u;
+  uint32_t v[4];
+  // the run that begins at column j >= 0 of a row of V >= E columns, whether it lies in the row or not
+  __device__ __forceinline__ void load(const char* row, int j, int V) {
+    __builtin_memcpy(v, row + (uint32_t)(min(j, V - E) * B), 16);  // a row is below 2^32 bytes
+  }
+  // takes what lies behind the row for -inf (after load)
+  __device__ __forceinline__ void cut(int j, int V) {
+    const int n = min(j - min(j, V - E), E) * B * 8;  // bits by which load began early
+    uint64_t lo = ((uint64_t)(v[1] ^ NINF) << 32) | (v[0] ^ NINF), hi = ((uint64_t)(v[3] ^ NINF) << 32) | (v[2] ^ NINF);
+    if (n >= 64) lo = hi, hi = 0;
+    const int m = n & 63;
+    if (n == 128) lo = 0;
+    if (m) lo = (lo >> m) | (hi << (64 - m)), hi >>= m;
+    v[0] = (uint32_t)lo ^ NINF, v[1] = (uint32_t)(lo >> 32) ^ NINF;
+    v[2] = (uint32_t)hi ^ NINF, v[3] = (uint32_t)(hi >> 32) ^ NINF;
+  }
+  // element k to -inf for each bit k of mask
+  __device__ __forceinline__ void drop(uint32_t mask) {
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (mask >> k & 1) {
+        if (IN == T_F32)
+          v[k] = NINF;
+        else
+          v[k / 2] = k & 1 ? (v[k / 2] & 0xFFFFu) | 0xFF800000u : (v[k / 2] & 0xFFFF0000u) | 0xFF80u;
+      }
+  }
+  // as if loaded anew: what was formed from it before is formed again, not kept
+  __device__ __forceinline__ void forget() { asm("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])); }
+  __device__ __forceinline__ float operator[](int k) const {
+    return IN == T_F32 ? __uint_as_float(v[k]) : k & 1 ? bf16_hi(v[k / 2]) : bf16_lo(v[k / 2]);
+  }
+};
+
+// A sum of exponentials of scale * (x - m), with its running maximum m (finite,
+// unless an infinity or NaN was added: then the sum is NaN).
+struct RunSum {
+  float m = -FLT_MAX, s = 0.0f;
+  template <int IN>
+  __device__ __forceinline__ void add(const Run<IN>& r, float scale) {
+    constexpr int E = Run<IN>::E;
+    float x = r[0];
+#pragma unroll
+    for (int k = 1; k < E; ++k) x = fmaxf(x, r[k]);
+    const float n = fmaxf(m, x);
+    s *= __builtin_amdgcn_exp2f((m - n) * scale);
+    m = n;
+    float p[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < E; ++k) p[k & 1] += __builtin_amdgcn_exp2f((r[k] - n) * scale);
+    s += p[0] + p[1];
+  }
+};
+
+// NH runs a thread in registers; MORE: rows that go on behind them.
+template <int IN, int NH, bool MORE>
 __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ float fmx[3][16];
-  __shared__ double dsum[4][16];
+  __shared__ float fmx[4][16];
+  __shared__ double dsum[3][16];
   __shared__ int32_t repeated;
+  constexpr int E = Run<IN>::E, IB = Run<IN>::B;
   const int t = threadIdx.x, nt = blockDim.x, nw = nt >> 6, lane = t & 63, wave = t >> 6;
   const int row = blockIdx.x, V = a.V, k = a.k;
-  constexpr int IB = IN == T_F32 ? 4 : 2;
   double* prob = reinterpret_cast<double*>(smem);          // [k] p_j, unnormalised
   float* student = reinterpret_cast<float*>(prob + k);     // [k] s_{i_j}
   int32_t* token = reinterpret_cast<int32_t*>(student + k);  // [k] i_j, -1 where absent
   uint32_t* marks = reinterpret_cast<uint32_t*>(token + k);
+  const uint8_t* bytes = reinterpret_cast<const uint8_t*>(marks);
   const char* x = static_cast<const char*>(a.x) + (size_t)row * V * IB;
   char* grad = a.grad ? static_cast<char*>(a.grad) + (size_t)row * V * IB : nullptr;
+  const int turns = MORE ? ((V + E - 1) / E + nt - 1) / nt : NH;
   const float w = a.weight ? a.weight[row] : 1.0f;
   const float tl = a.top_lse ? a.top_lse[row] : 0.0f;
+  const float scale = LOG2E / a.temperature;
   bool none = w == 0.0f || tl == -INFINITY;  // nothing to learn from this row
   if (!none) {
+    // the list's loads first: those of the row need not be waited for then
+    const int32_t* ip = a.index + (size_t)row * k;
+    const float* vp = a.values + (size_t)row * k;
+    const int32_t iv = ip[min(t, k - 1)];
+    const float tv = vp[min(t, k - 1)];
+    Run<IN> r[NH];
+    if (V >= E) {
+#pragma unroll
+      for (int i = 0; i < NH; ++i) r[i].load(x, (t + i * nt) * E, V);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NH; ++i) r[i].drop(0xFF);
+      if (t == 0)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (e < V) {
+            const float f = load1<IN>(x, e);
+            if (IN == T_F32)
+              r[0].v[e] = __float_as_uint(f);
+            else
+              r[0].v[e / 2] = e & 1 ? (r[0].v[e / 2] & 0xFFFFu) | __float_as_uint(f)
+                                    : (r[0].v[e / 2] & 0xFFFF0000u) | (__float_as_uint(f) >> 16);
+          }
+    }
     for (int i = t; i < (V + 31) / 32; i += nt) marks[i] = 0;
     if (t == 0) repeated = 0;
-    float tm = -INFINITY, sm = -INFINITY;
     __syncthreads();
+    float tm = -INFINITY, sm = -INFINITY;
     for (int j = t; j < k; j += nt) {
-      const int v = a.index[(size_t)row * k + j];
+      const int v = j == t ? iv : ip[j];
+      const float y = j == t ? tv : vp[j];
       const bool here = v >= 0 && v < V;
       token[j] = here ? v : -1;
-      if (here) {
-        const float s = load1<IN>(x, v), tv = a.values[(size_t)row * k + j];
-        student[j] = s;
-        sm = fmaxf(sm, s);
-        tm = fmaxf(tm, tv);
-        if (tv != tv) tm = INFINITY;  // fmaxf would lose it
-        // the first of a token listed more than once stands for its q
-        if (atomicOr(&marks[v >> 5], 1u << (v & 31)) >> (v & 31) & 1) {
-          token[j] = v | 0x40000000;
-          repeated = 1;
-        }
+      if (!here) continue;
+      // the first of a token listed more than once stands for its q
+      if (atomicOr(&marks[v >> 5], 1u << (v & 31)) >> (v & 31) & 1) {
+        token[j] = v | 0x40000000;
+        repeated = 1;
       }
+      const float s = load1<IN>(x, v);
+      student[j] = s;
+      sm = fmaxf(sm, s);
+      tm = y != y ? INFINITY : fmaxf(tm, y);  // fmaxf would lose a NaN
     }
     __syncthreads();
-    float rm = -INFINITY;
-    for (int j = t; j < V; j += nt)
-      if (!(marks[j >> 5] >> (j & 31) & 1)) rm = fmaxf(rm, load1<IN>(x, j));
-    rm = dpp_wave_fmax(rm), tm = dpp_wave_fmax(tm), sm = dpp_wave_fmax(sm);
-    if (lane == 0) fmx[0][wave] = rm, fmx[1][wave] = tm, fmx[2][wave] = sm;
+    // the rest's maximum and sum
+    auto take = [&](Run<IN>& v, int i) {
+      const int j = (t + i * nt) * E;
+      if ((i + 1) * nt * E > V && V >= E) v.cut(j, V);  // some of this turn's runs
+      const int at = min(j, V - 1);
+      uint32_t mask = bytes[at >> 3];
+      if (IN == T_F32) mask = mask >> (at & 4) & 15;
+      if (mask) v.drop(mask);
+    };
+    RunSum acc;
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      take(r[i], i);
+      r[i].forget();
+      acc.add(r[i], scale);
+      __builtin_amdgcn_sched_barrier(0);  // one run at a time: more would not fit the registers
+    }
+    constexpr int AHEAD = 4;
+    auto stream = [&](auto&& f) {
+      for (int i = NH; i < turns; i += AHEAD) {
+        Run<IN> o[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) o[u].load(x, (t + min(i + u, turns - 1) * nt) * E, V);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+          if (i + u < turns) {
+            take(o[u], i + u);
+            f(o[u], i + u);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+      }
+    };
+    if (MORE) stream([&](const Run<IN>& v, int) { acc.add(v, scale); });
+    const float wm = dpp_wave_fmax(acc.m);
+    const float ws = dpp_wave_fsum(acc.s * __builtin_amdgcn_exp2f((acc.m - wm) * scale));
+    tm = dpp_wave_fmax(tm), sm = dpp_wave_fmax(sm);
+    if (lane == 0) fmx[0][wave] = wm, fmx[1][wave] = tm, fmx[2][wave] = sm, fmx[3][wave] = ws;
     __syncthreads();
-    rm = fmx[0][0], tm = fmx[1][0], sm = fmx[2][0];
+    float rm = fmx[0][0];
+    tm = fmx[1][0], sm = fmx[2][0];
     for (int i = 1; i < nw; ++i) rm = fmaxf(rm, fmx[0][i]), tm = fmaxf(tm, fmx[1][i]), sm = fmaxf(sm, fmx[2][i]);
     none = !a.top_lse && tm == -INFINITY;
     if (!none) {
       const double invT = 1.0 / (double)a.temperature;
-      const float scale = LOG2E / a.temperature;
-      const float r0 = rm == -INFINITY ? 0.0f : rm;  // a rest that is all -inf adds exp(-inf)
       const double s0 = sm == -INFINITY ? 0.0 : (double)sm;
-      double acc[4] = {0.0, 0.0, 0.0, 0.0};  // rest, listed, sum of p, sum of p (t - s) / T
-      float sum = 0.0f;
-      for (int j = t; j < V; j += nt)
-        if (!(marks[j >> 5] >> (j & 31) & 1)) sum += __builtin_amdgcn_exp2f((load1<IN>(x, j) - r0) * scale);
-      acc[0] = (double)sum;
+      float rest = 0.0f;
+      for (int i = 0; i < nw; ++i) rest += fmx[3][i] * __builtin_amdgcn_exp2f((fmx[0][i] - rm) * scale);
+      double sum[3] = {0.0, 0.0, 0.0};  // listed, sum of p, sum of p (t - s) / T
       for (int j = t; j < k; j += nt) {
         if (token[j] < 0) continue;
-        const double tv = (double)a.values[(size_t)row * k + j], s = (double)student[j];
-        const double p = exp((tv - (a.top_lse ? 0.0 : (double)tm)) * invT - (a.top_lse ? (double)tl : 0.0));
+        const double y = (double)(j == t ? tv : vp[j]), s = (double)student[j];
+        const double p = exp((y - (a.top_lse ? 0.0 : (double)tm)) * invT - (a.top_lse ? (double)tl : 0.0));
         prob[j] = p;
-        if (!(token[j] & 0x40000000)) acc[1] += exp((s - s0) * invT);
-        acc[2] += p;
-        if (p != 0.0) acc[3] += p * ((tv - s) * invT);
+        if (!(token[j] & 0x40000000)) sum[0] += exp((s - s0) * invT);
+        sum[1] += p;
+        if (p != 0.0) sum[2] += p * ((y - s) * invT);
       }
+      const int lw = (min(k, nt) + 63) >> 6;  // waves that have entries
+      if (wave < lw) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = dpp_wave_sum(acc[i]);
-      if (lane == 0)
+        for (int i = 0; i < 3; ++i) sum[i] = dpp_wave_sum(sum[i]);
+        if (lane == 0)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dsum[i][wave] = acc[i];
+          for (int i = 0; i < 3; ++i) dsum[i][wave] = sum[i];
+      }
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i] = dsum[i][0];
-        for (int o = 1; o < nw; ++o) acc[i] += dsum[i][o];
+      for (int i = 0; i < 3; ++i) {
+        sum[i] = dsum[i][0];
+        for (int o = 1; o < lw; ++o) sum[i] += dsum[i][o];
       }
-      const double total = acc[2], norm = a.top_lse ? 1.0 : 1.0 / total;
+      const double R0 = (double)rest, total = sum[1], norm = a.top_lse ? 1.0 : 1.0 / total;
       // relative to the larger of the two maxima
-      const double top = acc[0] == 0.0 ? s0 : acc[1] == 0.0 ? (double)r0 : fmax((double)r0, s0);
-      const double A = acc[0] == 0.0 ? 0.0 : acc[0] * exp(((double)r0 - top) * invT);
-      const double B = acc[1] == 0.0 ? 0.0 : acc[1] * exp((s0 - top) * invT);
+      const double top = R0 == 0.0 ? s0 : sum[0] == 0.0 ? (double)rm : fmax((double)rm, s0);
+      const double A = R0 == 0.0 ? 0.0 : R0 * exp(((double)rm - top) * invT);
+      const double B = sum[0] == 0.0 ? 0.0 : sum[0] * exp((s0 - top) * invT);
       const double inv = A + B == 0.0 ? 0.0 : 1.0 / (A + B);
-      const double left = a.top_lse && acc[0] != 0.0 ? fmax(0.0, 1.0 - total) : 0.0;
+      const double left = a.top_lse && R0 != 0.0 ? fmax(0.0, 1.0 - total) : 0.0;
       const double gs = (double)w * invT;
       if (grad) {
-        const float coef = acc[0] == 0.0 ? 0.0f : (float)(gs * (A * inv - left) / acc[0]);
-        for (int j = t; j < V; j += nt) store1<IN>(grad, j, __builtin_amdgcn_exp2f((load1<IN>(x, j) - r0) * scale) * coef);
+        const float coef = R0 == 0.0 ? 0.0f : (float)(gs * (A * inv - left) / R0);
+        auto put = [&](const Run<IN>& v, int i) {
+          const int j = (t + i * nt) * E;
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = __builtin_amdgcn_exp2f((v[e] - rm) * scale) * coef;
+          uint32_t u[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u[e] = IN == T_F32 ? __float_as_uint(o[e]) : pack_bf16(o[(2 * e) % E], o[(2 * e + 1) % E]);
+          if ((i + 1) * nt * E <= V || j + E <= V) {
+            __builtin_memcpy(grad + (uint32_t)(j * IB), u, 16);
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if (j + e < V) store1<IN>(grad, j + e, o[e]);
+          }
+        };
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          r[i].forget();
+          put(r[i], i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (MORE) stream(put);
         __syncthreads();  // the listed tokens' own values come after
         for (int j = t; j < k; j += nt) {
           if (token[j] < 0) continue;
@@ -154,9 +297,9 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         // log p_j - log q_j = (t_j - s_j) / T - log of the teacher's sum + log of the student's
         const double ls = top * invT + log(A + B);
         const double lt = a.top_lse ? (double)tl : (double)tm * invT + log(total);
-        double loss = acc[3] * norm;
+        double loss = sum[2] * norm;
         if (total != 0.0 && loss != INFINITY) loss += total * norm * (ls - lt);
-        if (left > 0.0) loss += left * (log(left) - (((double)r0 - top) * invT + log(acc[0]) - log(A + B)));
+        if (left > 0.0) loss += left * (log(left) - (((double)rm - top) * invT + log(R0) - log(A + B)));
         a.loss[row] = (float)((double)w * loss);
       }
     }
@@ -164,20 +307,46 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
   if (none) {
     if (a.loss && t == 0) a.loss[row] = 0.0f;
     if (grad)
-      for (int j = t; j < V; j += nt) store1<IN>(grad, j, 0.0f);
+      for (int j = t * E; j < V; j += nt * E) {
+        if (j + E <= V) {
+          const uint32_t u[4] = {0, 0, 0, 0};
+          __builtin_memcpy(grad + (size_t)j * IB, u, 16);
+        } else {
+          for (int e = j; e < V; ++e) store1<IN>(grad, e, 0.0f);
+        }
+      }
   }
 }
 
-template <int IN>
-hipError_t launch_distill(const DistillArgs& a, int nt, hipStream_t s) {
+// Runs a thread in registers, and whole waves of threads to go with them.
+struct DistillLaunch {
+  int nt, nh;
+  bool more;
+  DistillLaunch(int V, int dtype) {
+    const int e = dtype == SV_F32 ? 4 : 8, runs = (V + e - 1) / e;
+    nh = runs <= 256 ? 2 : runs <= 2048 ? 8 : 16;
+    nt = std::min(1024, ((runs + nh - 1) / nh + 63) / 64 * 64);
+    more = runs > nt * nh;
+  }
+};
+
+template <int IN, int NH, bool MORE>
+hipError_t launch_distill(const DistillArgs& a, const DistillLaunch& l, hipStream_t s) {
   const size_t lds = distill_lds(a.V, a.k);
   if (lds > 48 * 1024) {
-    const hipError_t e = hipFuncSetAttribute((const void*)distill_kernel<IN>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)lds);
+    const hipError_t e = hipFuncSetAttribute((const void*)distill_kernel<IN, NH, MORE>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((distill_kernel<IN>), dim3((unsigned)a.rows), dim3((unsigned)nt), lds, s, a);
+  hipLaunchKernelGGL((distill_kernel<IN, NH, MORE>), dim3((unsigned)a.rows), dim3((unsigned)l.nt), lds, s, a);
   return hipGetLastError();
+}
+
+template <int IN>
+hipError_t launch_distill(const DistillArgs& a, const DistillLaunch& l, hipStream_t s) {
+  if (l.more) return launch_distill<IN, 16, true>(a, l, s);
+  return l.nh == 2 ? launch_distill<IN, 2, false>(a, l, s)
+                   : l.nh == 8 ? launch_distill<IN, 8, false>(a, l, s) : launch_distill<IN, 16, false>(a, l, s);
 }
 
 }  // namespace
@@ -191,8 +360,8 @@ extern "C" int sv_distill_loss(const void* logits, const int32_t* top_index, con
   if (rows < 0 || V < 1 || V > SV_MAX_DISTILL_V || k < 1 || k > SV_MAX_TOP) return SV_ERR_SHAPE;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
   if (!(temperature >= FLT_MIN) || !std::isfinite(temperature)) return SV_ERR_PARAM;
-  const int e = dtype == SV_F32 ? 4 : 8, nt = std::min(1024, ((V + e - 1) / e + 63) / 64 * 64);
-  if ((int64_t)rows * nt > kGridThreads) return SV_ERR_SHAPE;
+  const DistillLaunch l(V, dtype);
+  if ((int64_t)rows * l.nt > kGridThreads) return SV_ERR_SHAPE;
   if (rows == 0) return SV_OK;
   if (!logits || !top_index || !top_values || (!out_loss && !out_grad)) return SV_ERR_NULL;
   const size_t ie = (size_t)type_bytes(dtype), nin = (size_t)rows * (size_t)V * ie, nk = (size_t)rows * (size_t)k * 4;
@@ -212,7 +381,7 @@ extern "C" int sv_distill_loss(const void* logits, const int32_t* top_index, con
   for (const Range& i : lists)
     if (overlaps(out_grad, nin, i.p, i.n) || overlaps(out_loss, nr, i.p, i.n)) return SV_ERR_PARAM;
   const DistillArgs a{logits, top_index, top_values, top_lse, weight, out_loss, out_grad, rows, V, k, temperature};
-  const hipError_t err = dtype == SV_F32 ? launch_distill<T_F32>(a, nt, (hipStream_t)stream)
-                                         : launch_distill<T_BF16>(a, nt, (hipStream_t)stream);
+  const hipError_t err = dtype == SV_F32 ? launch_distill<T_F32>(a, l, (hipStream_t)stream)
+                                         : launch_distill<T_BF16>(a, l, (hipStream_t)stream);
   return err == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
