@@ -58,6 +58,20 @@ struct Run {
   __device__ __forceinline__ void load(const char* row, int j, int V) {
     __builtin_memcpy(v, row + (uint32_t)(min(j, V - E) * B), 16);  // a row is below 2^32 bytes
   }
+  // a row of V < E columns (0: nothing)
+  __device__ __forceinline__ void tiny(const char* row, int V) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = NINF;
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k < V) {
+        const uint32_t u = __float_as_uint(load1<IN>(row, k));
+        if (IN == T_F32)
+          v[k] = u;
+        else
+          v[k / 2] = k & 1 ? (v[k / 2] & 0xFFFFu) | u : (v[k / 2] & 0xFFFF0000u) | (u >> 16);
+      }
+  }
   // takes what lies behind the row for -inf (after load)
   __device__ __forceinline__ void cut(int j, int V) {
     const int n = min(j - min(j, V - E), E) * B * 8;  // bits by which load began early
@@ -87,6 +101,13 @@ struct Run {
   }
 };
 
+// A value that the compiler takes for a new one: what is formed from it is
+// formed again, and not held in a register from one pass to the next.
+__device__ __forceinline__ int fresh(int v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
 // A sum of exponentials of scale * (x - m), with its running maximum m (finite,
 // unless an infinity or NaN was added: then the sum is NaN).
 struct RunSum {
@@ -107,8 +128,9 @@ struct RunSum {
   }
 };
 
-// NH runs a thread in registers; MORE: rows that go on behind them.
-template <int IN, int NH, bool MORE>
+// NH runs a thread in registers; MORE: rows that go on behind them; TINY: rows
+// shorter than a run.
+template <int IN, int NH, bool MORE, bool TINY>
 __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ float fmx[4][16];
@@ -130,55 +152,41 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
   const float scale = LOG2E / a.temperature;
   bool none = w == 0.0f || tl == -INFINITY;  // nothing to learn from this row
   if (!none) {
-    // the list's loads first: those of the row need not be waited for then
+    // The list's loads first: those of the row need not be waited for then.  None
+    // stands in a branch, at whose end the compiler would wait for all of them,
+    // and the student's logits, behind the row in the queue, are looked at last.
     const int32_t* ip = a.index + (size_t)row * k;
     const float* vp = a.values + (size_t)row * k;
     const int32_t iv = ip[min(t, k - 1)];
     const float tv = vp[min(t, k - 1)];
     Run<IN> r[NH];
-    if (V >= E) {
+    int j0 = t * E;  // this thread's column in turn 0
+    if (TINY)
+      r[0].tiny(x, t == 0 ? V : 0);
+    else
 #pragma unroll
-      for (int i = 0; i < NH; ++i) r[i].load(x, (t + i * nt) * E, V);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NH; ++i) r[i].drop(0xFF);
-      if (t == 0)
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (e < V) {
-            const float f = load1<IN>(x, e);
-            if (IN == T_F32)
-              r[0].v[e] = __float_as_uint(f);
-            else
-              r[0].v[e / 2] = e & 1 ? (r[0].v[e / 2] & 0xFFFFu) | __float_as_uint(f)
-                                    : (r[0].v[e / 2] & 0xFFFF0000u) | (__float_as_uint(f) >> 16);
-          }
-    }
+      for (int i = 0; i < NH; ++i) r[i].load(x, j0 + i * (nt * E), V);
     for (int i = t; i < (V + 31) / 32; i += nt) marks[i] = 0;
     if (t == 0) repeated = 0;
     __syncthreads();
-    float tm = -INFINITY, sm = -INFINITY;
-    for (int j = t; j < k; j += nt) {
-      const int v = j == t ? iv : ip[j];
-      const float y = j == t ? tv : vp[j];
-      const bool here = v >= 0 && v < V;
-      token[j] = here ? v : -1;
-      if (!here) continue;
-      // the first of a token listed more than once stands for its q
-      if (atomicOr(&marks[v >> 5], 1u << (v & 31)) >> (v & 31) & 1) {
-        token[j] = v | 0x40000000;
+    // entry j's token, or -1; the first of a token listed more than once stands for its q
+    auto mark = [&](int j, int v) {
+      int to = v >= 0 && v < V ? v : -1;
+      if (to >= 0 && (atomicOr(&marks[v >> 5], 1u << (v & 31)) >> (v & 31) & 1)) {
+        to = v | 0x40000000;
         repeated = 1;
       }
-      const float s = load1<IN>(x, v);
-      student[j] = s;
-      sm = fmaxf(sm, s);
-      tm = y != y ? INFINITY : fmaxf(tm, y);  // fmaxf would lose a NaN
-    }
+      token[j] = to;
+    };
+    const bool here = t < k && iv >= 0 && iv < V;
+    const float sv = load1<IN>(x, here ? iv : 0);
+    if (t < k) mark(t, iv);
+    for (int j = t + nt; j < k; j += nt) mark(j, ip[j]);
     __syncthreads();
     // the rest's maximum and sum
     auto take = [&](Run<IN>& v, int i) {
-      const int j = (t + i * nt) * E;
-      if ((i + 1) * nt * E > V && V >= E) v.cut(j, V);  // some of this turn's runs
+      const int j = j0 + i * (nt * E);
+      if (!TINY && (i + 1) * nt * E > V) v.cut(j, V);  // some of this turn's runs
       const int at = min(j, V - 1);
       uint32_t mask = bytes[at >> 3];
       if (IN == T_F32) mask = mask >> (at & 4) & 15;
@@ -187,6 +195,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
     RunSum acc;
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
+      j0 = fresh(j0);
       take(r[i], i);
       r[i].forget();
       acc.add(r[i], scale);
@@ -197,7 +206,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
       for (int i = NH; i < turns; i += AHEAD) {
         Run<IN> o[AHEAD];
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) o[u].load(x, (t + min(i + u, turns - 1) * nt) * E, V);
+        for (int u = 0; u < AHEAD; ++u) o[u].load(x, j0 + min(i + u, turns - 1) * (nt * E), V);
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
           if (i + u < turns) {
@@ -208,6 +217,16 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
       }
     };
     if (MORE) stream([&](const Run<IN>& v, int) { acc.add(v, scale); });
+    // the list's maxima
+    float tm = -INFINITY, sm = -INFINITY;
+    auto entry = [&](int j, float y, float s) {
+      student[j] = s;
+      sm = fmaxf(sm, s);
+      tm = y != y ? INFINITY : fmaxf(tm, y);  // fmaxf would lose a NaN
+    };
+    if (here) entry(t, tv, sv);
+    for (int j = t + nt; j < k; j += nt)
+      if (token[j] >= 0) entry(j, vp[j], load1<IN>(x, token[j] & 0x3FFFFFFF));
     const float wm = dpp_wave_fmax(acc.m);
     const float ws = dpp_wave_fsum(acc.s * __builtin_amdgcn_exp2f((acc.m - wm) * scale));
     tm = dpp_wave_fmax(tm), sm = dpp_wave_fmax(sm);
@@ -257,7 +276,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
       if (grad) {
         const float coef = R0 == 0.0 ? 0.0f : (float)(gs * (A * inv - left) / R0);
         auto put = [&](const Run<IN>& v, int i) {
-          const int j = (t + i * nt) * E;
+          const int j = j0 + i * (nt * E);
           float o[8];
 #pragma unroll
           for (int e = 0; e < E; ++e) o[e] = __builtin_amdgcn_exp2f((v[e] - rm) * scale) * coef;
@@ -274,6 +293,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         };
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
+          j0 = fresh(j0);
           r[i].forget();
           put(r[i], i);
           __builtin_amdgcn_sched_barrier(0);
@@ -330,23 +350,24 @@ struct DistillLaunch {
   }
 };
 
-template <int IN, int NH, bool MORE>
+template <int IN, int NH, bool MORE, bool TINY>
 hipError_t launch_distill(const DistillArgs& a, const DistillLaunch& l, hipStream_t s) {
   const size_t lds = distill_lds(a.V, a.k);
   if (lds > 48 * 1024) {
-    const hipError_t e = hipFuncSetAttribute((const void*)distill_kernel<IN, NH, MORE>,
+    const hipError_t e = hipFuncSetAttribute((const void*)distill_kernel<IN, NH, MORE, TINY>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((distill_kernel<IN, NH, MORE>), dim3((unsigned)a.rows), dim3((unsigned)l.nt), lds, s, a);
+  hipLaunchKernelGGL((distill_kernel<IN, NH, MORE, TINY>), dim3((unsigned)a.rows), dim3((unsigned)l.nt), lds, s, a);
   return hipGetLastError();
 }
 
 template <int IN>
 hipError_t launch_distill(const DistillArgs& a, const DistillLaunch& l, hipStream_t s) {
-  if (l.more) return launch_distill<IN, 16, true>(a, l, s);
-  return l.nh == 2 ? launch_distill<IN, 2, false>(a, l, s)
-                   : l.nh == 8 ? launch_distill<IN, 8, false>(a, l, s) : launch_distill<IN, 16, false>(a, l, s);
+  if (a.V < Run<IN>::E) return launch_distill<IN, 1, false, true>(a, l, s);
+  if (l.more) return launch_distill<IN, 16, true, false>(a, l, s);
+  return l.nh == 2 ? launch_distill<IN, 2, false, false>(a, l, s)
+                   : l.nh == 8 ? launch_distill<IN, 8, false, false>(a, l, s) : launch_distill<IN, 16, false, false>(a, l, s);
 }
 
 }  // namespace
