@@ -45,8 +45,21 @@ struct DistillArgs {
 };
 
 // In LDS: probabilities, the student's logits and the tokens of the list, [k]
-// each, and the bitmap.
-inline size_t distill_lds(int V, int k) { return (size_t)k * 16 + (size_t)((V + 31) / 32) * 4; }
+// each, and the marks: a bit a token, in the order in which the threads take
+// them.  A thread's runs in registers have theirs next to each other (a byte a
+// run of 8, half a byte a run of 4), the runs behind them turn by turn.
+struct Marks {
+  int e, nt, nh, turns;  // columns a run, threads, runs a thread in registers and in all
+  __host__ __device__ int of(int nruns) const { return e == 8 ? nruns : (nruns + 1) / 2; }
+  __host__ __device__ int bytes() const { return (nt * (of(nh) + of(turns - nh)) + 15) & ~15; }
+  // bit of the token
+  __device__ __forceinline__ uint32_t bit(int token) const {
+    const uint32_t run = (uint32_t)token / (uint32_t)e, i = run / (uint32_t)nt, t = run - i * nt;
+    const uint32_t n = (uint32_t)nh, at = i < n ? i : i - n;
+    const uint32_t byte = i < n ? t * of(nh) + (e == 8 ? at : at / 2) : nt * of(nh) + (e == 8 ? at : at / 2) * nt + t;
+    return byte * 8 + (e == 8 ? 0 : at % 2 * 4) + (uint32_t)token % (uint32_t)e;
+  }
+};
 
 // E logits as they lie in memory.
 template <int IN>
@@ -108,22 +121,29 @@ __device__ __forceinline__ int fresh(int v) {
   return v;
 }
 
-// A sum of exponentials of scale * (x - m), with its running maximum m (finite,
-// unless an infinity or NaN was added: then the sum is NaN).
+// A sum of 2^(scale x - ref).  ref is not the maximum but a value of the scale
+// that lies 8 below it at most: it follows the maximum in steps, so that few
+// runs form the sum so far again.  Where scale x is not finite in float32
+// (logits next to the type's largest or lowest value), the sum comes out as 0 or
+// NaN, and the row takes the slow way below.
 struct RunSum {
-  float m = -FLT_MAX, s = 0.0f;
+  float ref = -FLT_MAX, s = 0.0f;
+  bool any = false;  // something above -inf was added
   template <int IN>
   __device__ __forceinline__ void add(const Run<IN>& r, float scale) {
     constexpr int E = Run<IN>::E;
     float x = r[0];
 #pragma unroll
     for (int k = 1; k < E; ++k) x = fmaxf(x, r[k]);
-    const float n = fmaxf(m, x);
-    s *= __builtin_amdgcn_exp2f((m - n) * scale);
-    m = n;
+    any |= x > -INFINITY;
+    x *= scale;
+    if (x > ref + 8.0f) {
+      s *= __builtin_amdgcn_exp2f(ref - x);
+      ref = x;
+    }
     float p[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < E; ++k) p[k & 1] += __builtin_amdgcn_exp2f((r[k] - n) * scale);
+    for (int k = 0; k < E; ++k) p[k & 1] += __builtin_amdgcn_exp2f(__builtin_fmaf(r[k], scale, -ref));
     s += p[0] + p[1];
   }
 };
@@ -133,7 +153,8 @@ struct RunSum {
 template <int IN, int NH, bool MORE, bool TINY>
 __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ float fmx[4][16];
+  __shared__ float4 fmx[16];
+  __shared__ float fany[16];
   __shared__ double dsum[3][16];
   __shared__ int32_t repeated;
   constexpr int E = Run<IN>::E, IB = Run<IN>::B;
@@ -144,9 +165,11 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
   int32_t* token = reinterpret_cast<int32_t*>(student + k);  // [k] i_j, -1 where absent
   uint32_t* marks = reinterpret_cast<uint32_t*>(token + k);
   const uint8_t* bytes = reinterpret_cast<const uint8_t*>(marks);
+  constexpr int MB = E == 8 ? NH : (NH + 1) / 2;  // bytes of marks a thread for its runs in registers
   const char* x = static_cast<const char*>(a.x) + (size_t)row * V * IB;
   char* grad = a.grad ? static_cast<char*>(a.grad) + (size_t)row * V * IB : nullptr;
   const int turns = MORE ? ((V + E - 1) / E + nt - 1) / nt : NH;
+  const Marks at{E, nt, NH, turns};
   const float w = a.weight ? a.weight[row] : 1.0f;
   const float tl = a.top_lse ? a.top_lse[row] : 0.0f;
   const float scale = LOG2E / a.temperature;
@@ -166,15 +189,18 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
     else
 #pragma unroll
       for (int i = 0; i < NH; ++i) r[i].load(x, j0 + i * (nt * E), V);
-    for (int i = t; i < (V + 31) / 32; i += nt) marks[i] = 0;
+    for (int i = t; i < at.bytes() / 16; i += nt) reinterpret_cast<uint4*>(marks)[i] = make_uint4(0, 0, 0, 0);
     if (t == 0) repeated = 0;
     __syncthreads();
     // entry j's token, or -1; the first of a token listed more than once stands for its q
     auto mark = [&](int j, int v) {
       int to = v >= 0 && v < V ? v : -1;
-      if (to >= 0 && (atomicOr(&marks[v >> 5], 1u << (v & 31)) >> (v & 31) & 1)) {
-        to = v | 0x40000000;
-        repeated = 1;
+      if (to >= 0) {
+        const uint32_t b = at.bit(v);
+        if (atomicOr(&marks[b >> 5], 1u << (b & 31)) >> (b & 31) & 1) {
+          to = v | 0x40000000;
+          repeated = 1;
+        }
       }
       token[j] = to;
     };
@@ -184,19 +210,18 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
     for (int j = t + nt; j < k; j += nt) mark(j, ip[j]);
     __syncthreads();
     // the rest's maximum and sum
-    auto take = [&](Run<IN>& v, int i) {
+    auto take = [&](Run<IN>& v, int i, uint32_t mask) {
       const int j = j0 + i * (nt * E);
       if (!TINY && (i + 1) * nt * E > V) v.cut(j, V);  // some of this turn's runs
-      const int at = min(j, V - 1);
-      uint32_t mask = bytes[at >> 3];
-      if (IN == T_F32) mask = mask >> (at & 4) & 15;
       if (mask) v.drop(mask);
     };
+    uint32_t mk[(MB + 3) / 4];
+    __builtin_memcpy(mk, __builtin_assume_aligned(bytes + t * MB, MB & -MB), MB);
     RunSum acc;
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
       j0 = fresh(j0);
-      take(r[i], i);
+      take(r[i], i, E == 8 ? mk[i / 4] >> (i % 4 * 8) & 255 : mk[i / 8] >> (i % 8 * 4) & 15);
       r[i].forget();
       acc.add(r[i], scale);
       __builtin_amdgcn_sched_barrier(0);  // one run at a time: more would not fit the registers
@@ -210,7 +235,9 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
           if (i + u < turns) {
-            take(o[u], i + u);
+            const int n = i + u - NH;
+            const uint32_t b = bytes[nt * MB + (E == 8 ? n : n / 2) * nt + t];
+            take(o[u], i + u, E == 8 ? b : b >> (n % 2 * 4) & 15);
             f(o[u], i + u);
             __builtin_amdgcn_sched_barrier(0);
           }
@@ -227,20 +254,48 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
     if (here) entry(t, tv, sv);
     for (int j = t + nt; j < k; j += nt)
       if (token[j] >= 0) entry(j, vp[j], load1<IN>(x, token[j] & 0x3FFFFFFF));
-    const float wm = dpp_wave_fmax(acc.m);
-    const float ws = dpp_wave_fsum(acc.s * __builtin_amdgcn_exp2f((acc.m - wm) * scale));
+    const float wr = dpp_wave_fmax(acc.ref);
+    const float ws = dpp_wave_fsum(acc.s * __builtin_amdgcn_exp2f(acc.ref - wr));
     tm = dpp_wave_fmax(tm), sm = dpp_wave_fmax(sm);
-    if (lane == 0) fmx[0][wave] = wm, fmx[1][wave] = tm, fmx[2][wave] = sm, fmx[3][wave] = ws;
+    if (lane == 0) fmx[wave] = make_float4(wr, ws, tm, sm);
+    if (lane == 0) fany[wave] = __any(acc.any) ? 1.0f : 0.0f;
     __syncthreads();
-    float rm = fmx[0][0];
-    tm = fmx[1][0], sm = fmx[2][0];
-    for (int i = 1; i < nw; ++i) rm = fmaxf(rm, fmx[0][i]), tm = fmaxf(tm, fmx[1][i]), sm = fmaxf(sm, fmx[2][i]);
+    const int from = min(lane & 15, nw - 1);
+    const float4 wv = fmx[from];
+    const float ref = row16_max(wv.x);
+    float rest = row16_sum((lane & 15) < nw ? wv.y * __builtin_amdgcn_exp2f(wv.x - ref) : 0.0f);
+    tm = row16_max(wv.z), sm = row16_max(wv.w);
+    const bool left_over = row16_max(fany[from]) > 0.0f;  // not all of the rest is -inf
     none = !a.top_lse && tm == -INFINITY;
     if (!none) {
       const double invT = 1.0 / (double)a.temperature;
       const double s0 = sm == -INFINITY ? 0.0 : (double)sm;
-      float rest = 0.0f;
-      for (int i = 0; i < nw; ++i) rest += fmx[3][i] * __builtin_amdgcn_exp2f((fmx[0][i] - rm) * scale);
+      // the logit that the rest's sum is relative to: of ref as the float32 factor takes it there
+      double rm = (double)ref / (double)scale;
+      const bool slow = left_over && !(rest > 0.0f && rest < INFINITY);
+      float far = 0.0f;
+      if (slow) {
+        // relative to the maximum itself, read again, an element at a time
+        auto each = [&](auto&& f) {
+          for (int j = t; j < V; j += nt) {
+            const uint32_t b = at.bit(j);
+            if (!(marks[b >> 5] >> (b & 31) & 1)) f(load1<IN>(x, j));
+          }
+        };
+        float m = -INFINITY, e = 0.0f;
+        each([&](float v) { m = fmaxf(m, v); });
+        m = dpp_wave_fmax(m);
+        __syncthreads();
+        if (lane == 0) fmx[wave].x = m;
+        __syncthreads();
+        far = row16_max(fmx[from].x);
+        each([&](float v) { e += __builtin_amdgcn_exp2f((v - far) * scale); });
+        e = dpp_wave_fsum(e);
+        if (lane == 0) fmx[wave].y = e;
+        __syncthreads();
+        rest = row16_sum((lane & 15) < nw ? fmx[from].y : 0.0f);
+        rm = (double)far;
+      }
       double sum[3] = {0.0, 0.0, 0.0};  // listed, sum of p, sum of p (t - s) / T
       for (int j = t; j < k; j += nt) {
         if (token[j] < 0) continue;
@@ -266,20 +321,24 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         for (int o = 1; o < lw; ++o) sum[i] += dsum[i][o];
       }
       const double R0 = (double)rest, total = sum[1], norm = a.top_lse ? 1.0 : 1.0 / total;
-      // relative to the larger of the two maxima
-      const double top = R0 == 0.0 ? s0 : sum[0] == 0.0 ? (double)rm : fmax((double)rm, s0);
-      const double A = R0 == 0.0 ? 0.0 : R0 * exp(((double)rm - top) * invT);
-      const double B = sum[0] == 0.0 ? 0.0 : sum[0] * exp((s0 - top) * invT);
+      // relative to the larger of the two maxima; lane 0 for the rest, the others for the list
+      const double top = R0 == 0.0 ? s0 : sum[0] == 0.0 ? rm : fmax(rm, s0);
+      const double part = lane == 0 ? R0 : sum[0];
+      const double AB = part == 0.0 ? 0.0 : part * exp(((lane == 0 ? rm : s0) - top) * invT);
+      const double A = __shfl(AB, 0), B = __shfl(AB, 1);
       const double inv = A + B == 0.0 ? 0.0 : 1.0 / (A + B);
       const double left = a.top_lse && R0 != 0.0 ? fmax(0.0, 1.0 - total) : 0.0;
       const double gs = (double)w * invT;
       if (grad) {
         const float coef = R0 == 0.0 ? 0.0f : (float)(gs * (A * inv - left) / R0);
+        if (slow)
+          for (int j = t; j < V; j += nt)
+            store1<IN>(grad, j, __builtin_amdgcn_exp2f((load1<IN>(x, j) - far) * scale) * coef);
         auto put = [&](const Run<IN>& v, int i) {
           const int j = j0 + i * (nt * E);
           float o[8];
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = __builtin_amdgcn_exp2f((v[e] - rm) * scale) * coef;
+          for (int e = 0; e < E; ++e) o[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], scale, -ref)) * coef;
           uint32_t u[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) u[e] = IN == T_F32 ? __float_as_uint(o[e]) : pack_bf16(o[(2 * e) % E], o[(2 * e + 1) % E]);
@@ -291,14 +350,16 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
               if (j + e < V) store1<IN>(grad, j + e, o[e]);
           }
         };
+        if (!slow) {
 #pragma unroll
-        for (int i = 0; i < NH; ++i) {
-          j0 = fresh(j0);
-          r[i].forget();
-          put(r[i], i);
-          __builtin_amdgcn_sched_barrier(0);
+          for (int i = 0; i < NH; ++i) {
+            j0 = fresh(j0);
+            r[i].forget();
+            put(r[i], i);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (MORE) stream(put);
         }
-        if (MORE) stream(put);
         __syncthreads();  // the listed tokens' own values come after
         for (int j = t; j < k; j += nt) {
           if (token[j] < 0) continue;
@@ -313,14 +374,17 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
           store1<IN>(grad, v, (float)(gs * ((student[j] == -INFINITY ? 0.0 : q) - p * norm)));
         }
       }
-      if (a.loss && t == 0) {
+      if (a.loss && wave == nw - 1) {
+        // four logarithms at once, a lane each
+        const double of = lane == 0 ? A + B : lane == 1 ? total : lane == 2 ? left : R0;
+        const double lg = log(of);
+        const double lAB = __shfl(lg, 0), lP = __shfl(lg, 1), lr = __shfl(lg, 2), lR = __shfl(lg, 3);
         // log p_j - log q_j = (t_j - s_j) / T - log of the teacher's sum + log of the student's
-        const double ls = top * invT + log(A + B);
-        const double lt = a.top_lse ? (double)tl : (double)tm * invT + log(total);
+        const double ls = top * invT + lAB, lt = a.top_lse ? (double)tl : (double)tm * invT + lP;
         double loss = sum[2] * norm;
         if (total != 0.0 && loss != INFINITY) loss += total * norm * (ls - lt);
-        if (left > 0.0) loss += left * (log(left) - (((double)rm - top) * invT + log(R0) - log(A + B)));
-        a.loss[row] = (float)((double)w * loss);
+        if (left > 0.0) loss += left * (lr - ((rm - top) * invT + lR - lAB));
+        if (lane == 0) a.loss[row] = (float)((double)w * loss);
       }
     }
   }
@@ -352,7 +416,8 @@ struct DistillLaunch {
 
 template <int IN, int NH, bool MORE, bool TINY>
 hipError_t launch_distill(const DistillArgs& a, const DistillLaunch& l, hipStream_t s) {
-  const size_t lds = distill_lds(a.V, a.k);
+  const Marks at{Run<IN>::E, l.nt, NH, MORE ? ((a.V + Run<IN>::E - 1) / Run<IN>::E + l.nt - 1) / l.nt : NH};
+  const size_t lds = (size_t)a.k * 16 + (size_t)at.bytes();
   if (lds > 48 * 1024) {
     const hipError_t e = hipFuncSetAttribute((const void*)distill_kernel<IN, NH, MORE, TINY>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);

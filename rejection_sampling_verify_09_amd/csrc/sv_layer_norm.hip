@@ -39,13 +39,6 @@ struct LayerArgs {
 // aligned, which nothing else uses until the next barrier but one), in a fixed order, to all of
 // their threads.  Waves first; then each lane takes one wave's sum and 16 lanes
 // add theirs, instead of every lane adding all of them.
-__device__ __forceinline__ float row16_sum(float v) {
-  v += __uint_as_float(dpp_mov<DPP_QP_1032>(__float_as_uint(v)));
-  v += __uint_as_float(dpp_mov<DPP_QP_2301>(__float_as_uint(v)));
-  v += __uint_as_float(dpp_mov<DPP_HALF_MIRROR>(__float_as_uint(v)));
-  v += __uint_as_float(dpp_mov<DPP_MIRROR>(__float_as_uint(v)));
-  return v;
-}
 template <int A>
 __device__ __forceinline__ void group_sum(float (&v)[A], float* part, int nw) {
 #pragma unroll

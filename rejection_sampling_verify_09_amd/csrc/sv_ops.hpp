@@ -47,6 +47,23 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(clamp_e4m3(c), clamp_e4m3(d), w, true);
 }
 
+// Over the 16 lanes that hold a value for each of up to 16 waves.
+__device__ __forceinline__ float row16_max(float v) {
+  v = fmaxf(v, __uint_as_float(dpp_mov<DPP_QP_1032>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp_mov<DPP_QP_2301>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp_mov<DPP_HALF_MIRROR>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp_mov<DPP_MIRROR>(__float_as_uint(v))));
+  return v;
+}
+
+__device__ __forceinline__ float row16_sum(float v) {
+  v += __uint_as_float(dpp_mov<DPP_QP_1032>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_mov<DPP_QP_2301>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_mov<DPP_HALF_MIRROR>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_mov<DPP_MIRROR>(__float_as_uint(v)));
+  return v;
+}
+
 // Element j of a row.
 template <int T>
 __device__ __forceinline__ float load1(const char* p, int j) {
