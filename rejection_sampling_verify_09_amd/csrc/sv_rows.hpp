@@ -1,0 +1,103 @@
+// Rows of logits, 16 bytes a load, for the operators that take a row a workgroup
+// (sv_top.hip, sv_distill.hip).
+#pragma once
+
+#include "sv_ops.hpp"
+
+#include <cfloat>
+#include <cmath>
+
+namespace sv {
+
+constexpr float LOG2E = 1.4426950408889634f;
+
+// E logits as they lie in memory.
+template <int IN>
+struct Run {
+  static constexpr int E = IN == T_F32 ? 4 : 8, B = IN == T_F32 ? 4 : 2;
+  static constexpr uint32_t NINF = IN == T_F32 ? 0xFF800000u : 0xFF80FF80u;
+  uint32_t v[4];
+  // the run that begins at column j >= 0 of a row of V >= E columns, whether it lies in the row or not
+  __device__ __forceinline__ void load(const char* row, int j, int V) {
+    __builtin_memcpy(v, row + (uint32_t)(min(j, V - E) * B), 16);  // a row is below 2^32 bytes
+  }
+  // a row of V < E columns (0: nothing)
+  __device__ __forceinline__ void tiny(const char* row, int V) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = NINF;
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k < V) {
+        const uint32_t u = __float_as_uint(load1<IN>(row, k));
+        if (IN == T_F32)
+          v[k] = u;
+        else
+          v[k / 2] = k & 1 ? (v[k / 2] & 0xFFFFu) | u : (v[k / 2] & 0xFFFF0000u) | (u >> 16);
+      }
+  }
+  // takes what lies behind the row for -inf (after load)
+  __device__ __forceinline__ void cut(int j, int V) {
+    const int n = min(j - min(j, V - E), E) * B * 8;  // bits by which load began early
+    uint64_t lo = ((uint64_t)(v[1] ^ NINF) << 32) | (v[0] ^ NINF), hi = ((uint64_t)(v[3] ^ NINF) << 32) | (v[2] ^ NINF);
+    if (n >= 64) lo = hi, hi = 0;
+    const int m = n & 63;
+    if (n == 128) lo = 0;
+    if (m) lo = (lo >> m) | (hi << (64 - m)), hi >>= m;
+    v[0] = (uint32_t)lo ^ NINF, v[1] = (uint32_t)(lo >> 32) ^ NINF;
+    v[2] = (uint32_t)hi ^ NINF, v[3] = (uint32_t)(hi >> 32) ^ NINF;
+  }
+  // element k to -inf for each bit k of mask
+  __device__ __forceinline__ void drop(uint32_t mask) {
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (mask >> k & 1) {
+        if (IN == T_F32)
+          v[k] = NINF;
+        else
+          v[k / 2] = k & 1 ? (v[k / 2] & 0xFFFFu) | 0xFF800000u : (v[k / 2] & 0xFFFF0000u) | 0xFF80u;
+      }
+  }
+  // as if loaded anew: what was formed from it before is formed again, not kept
+  __device__ __forceinline__ void forget() { asm("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])); }
+  __device__ __forceinline__ float operator[](int k) const {
+    return IN == T_F32 ? __uint_as_float(v[k]) : k & 1 ? bf16_hi(v[k / 2]) : bf16_lo(v[k / 2]);
+  }
+};
+
+// A value that the compiler takes for a new one: what is formed from it is
+// formed again, and not held in a register from one pass to the next.
+__device__ __forceinline__ int fresh(int v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
+// A sum of 2^(scale x - ref).  ref is not the maximum but a value of the scale
+// that lies 8 below it at most: it follows the maximum in steps, so that few
+// runs form the sum so far again.  Where scale x is not finite in float32
+// (logits next to the type's largest or lowest value), the sum comes out as 0 or
+// NaN, and the row takes the slow way below.
+struct RunSum {
+  float ref = -FLT_MAX, s = 0.0f;
+  bool any = false;  // something above -inf was added
+  // returns the run's maximum (NaN apart)
+  template <int IN>
+  __device__ __forceinline__ float add(const Run<IN>& r, float scale) {
+    constexpr int E = Run<IN>::E;
+    float x = r[0];
+#pragma unroll
+    for (int k = 1; k < E; ++k) x = fmaxf(x, r[k]);
+    any |= x > -INFINITY;
+    const float y = x * scale;
+    if (y > ref + 8.0f) {
+      s *= __builtin_amdgcn_exp2f(ref - y);
+      ref = y;
+    }
+    float p[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < E; ++k) p[k & 1] += __builtin_amdgcn_exp2f(__builtin_fmaf(r[k], scale, -ref));
+    s += p[0] + p[1];
+    return x;
+  }
+};
+
+}  // namespace sv

@@ -2,16 +2,21 @@
 // a temperature.
 //
 // Order: larger value first, among equal ones (-0 equals +0) the lower token;
-// NaN above +infinity.  One workgroup takes a row.  A lower bound of the k-th
-// largest value comes from the threads' own maxima: of each wave's 64 maxima
-// the ceil(k / waves)-th largest, and of those the smallest, has at least k
-// maxima at or above it.  What is at or above it goes to an LDS list, and each
-// entry's place is the number of entries before it in the order: all keys are
-// unlike (value, then token), so no order of arrival shows.  Where the list is
-// too short (rows in order of their tokens, many equal values), the k-th
-// largest value itself is found by digits and the equal ones are taken in the
-// order of their tokens.
-#include "sv_ops.hpp"
+// NaN above +infinity.
+//
+// One workgroup takes a row, in one pass: the sum of exponentials with a running
+// reference, and the maximum of each of a thread's slots (four runs of 16 bytes,
+// or a multiple).  A lower bound of the k-th largest value comes from the
+// threads' maxima: of each wave's 64 the ceil(k / waves)-th largest, and of those
+// the smallest, has at least k maxima at or above it.  The slots that reach it
+// are read again, a few hundred runs, and what is at or above it goes to a list
+// in LDS, where each entry's place is the number of entries before it in the
+// order: all keys are unlike (value, then token), so no order of arrival shows.
+// Where more reach the bound than the lists hold, because many equal it, those
+// above it and the first equal ones are enough, if these lie among the row's
+// first tokens (masked rows); otherwise (rows in order of their tokens) the k-th
+// largest value itself is found by digits, reading the row for each.
+#include "sv_rows.hpp"
 #include "specverify.h"
 
 #include <algorithm>
@@ -22,16 +27,17 @@ namespace sv {
 
 namespace {
 
-constexpr int TOP_CAP = 2048;    // entries of the list; at least SV_MAX_TOP
-constexpr int TOP_TURNS = 512;   // runs a thread, at most: SV_MAX_V / 4 runs on 1024 threads
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr int TOP_CAP = 2048;   // entries of the list; at least 2 SV_MAX_TOP
+constexpr int TOP_HITS = 2048;  // slots read again
+constexpr int TOP_SLOTS = 16;   // slots a thread, at most
+constexpr int TOP_TURNS = 512;  // runs a thread, at most: SV_MAX_V / 4 runs on 1024 threads
 
 struct TopArgs {
   const void* x;
   float* values;
   int32_t* index;
   float* lse;
-  int32_t rows, V, k;
+  int32_t rows, V, k, turns, each;
   float temperature;
 };
 
@@ -54,147 +60,274 @@ __device__ __forceinline__ uint32_t wave_sort_desc(uint32_t v) {
   return v;
 }
 
-template <int IN>
-struct TopRow {
-  static constexpr int E = IN == T_F32 ? 4 : 8;  // elements of a 16-byte run
-  const char* p;
-  int V, nt;
-  // f(key, token) for each element of this thread's run of turn i
-  template <typename F>
-  __device__ __forceinline__ void run(int i, F&& f) const {
-    const int j = (threadIdx.x + i * nt) * E;
-    for (int k = 0; k < E; ++k)
-      if (j + k < V) f(top_key(load1<IN>(p, j + k)), j + k);
+// A row's launch: threads, runs a thread, and runs a slot.
+struct TopShape {
+  int nt, turns, each;
+  TopShape(int V, int k, int e) {
+    // four runs a thread, as many as are on their way at a time; more threads for long lists, whose bound is the
+    // better the more maxima there are, but none without a run
+    const int runs = (V + e - 1) / e, full = std::max(64, runs / 64 * 64);
+    nt = std::min({1024, full, std::max((runs / 4 + 63) / 64 * 64, (4 * k + 63) / 64 * 64)});
+    nt = std::max(nt, 64);
+    turns = (runs + nt - 1) / nt;
+    each = ((turns + 3) / 4 + TOP_SLOTS - 1) / TOP_SLOTS * 4;
   }
+  int slots() const { return (turns + each - 1) / each; }
 };
 
-template <int IN>
+// TINY: rows shorter than a run.
+template <int IN, bool TINY>
 __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
-  constexpr int E = TopRow<IN>::E;
+  constexpr int E = Run<IN>::E;
+  extern __shared__ uint32_t slot[];  // [slots][nt] the slot's largest key
   __shared__ uint64_t list[TOP_CAP];
-  __shared__ float fsum[16];
+  // slots above the bound, then those at it; later the number of equal logits of each turn
+  __shared__ uint32_t hits[TOP_HITS];
   __shared__ uint32_t bound[2][16];
-  __shared__ int32_t count[TOP_TURNS];
+  __shared__ float2 fsum[16];
   __shared__ int32_t hist[256];
   __shared__ int32_t wcount[16];
-  __shared__ int32_t nlist, nabove, pick, need;
+  __shared__ int32_t nlist, nabove, nat, pick, need, nans;
   const int t = threadIdx.x, nt = blockDim.x, nw = nt >> 6, lane = t & 63, wave = t >> 6;
-  const int row = blockIdx.x, V = a.V, k = a.k;
-  const TopRow<IN> r{static_cast<const char*>(a.x) + (size_t)row * V * (IN == T_F32 ? 4 : 2), V, nt};
-  const int turns = ((V + E - 1) / E + nt - 1) / nt;
-  if (t == 0) nlist = 0, nabove = 0;
+  const int row = blockIdx.x, V = a.V, k = a.k, turns = a.turns, each = a.each, nslots = (turns + each - 1) / each;
+  const char* x = static_cast<const char*>(a.x) + (size_t)row * V * Run<IN>::B;
+  const float scale = LOG2E / a.temperature;
+  // f(key, token) for the elements of thread `by`'s run of turn i
+  auto again = [&](int i, int by, auto&& f) {
+    const int j = (by + i * nt) * E;
+    if (j >= V) return;
+    Run<IN> r;
+    if (TINY) {
+      r.tiny(x, V);
+    } else {
+      r.load(x, j, V);
+      r.cut(j, V);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (j + e < V) f(r[e], j + e);
+  };
+  if (t == 0) nlist = nabove = nat = nans = 0;
 
-  uint32_t m = 0;
-  for (int i = 0; i < turns; ++i) r.run(i, [&](uint32_t key, int) { m = max(m, key); });
-  const uint32_t wm = dpp_wave_umax(m);
+  // one pass, four runs ahead
+  RunSum sum;
+  float sm = -INFINITY, m = -INFINITY;
+  Run<IN> r[4];
+  auto fetch = [&](Run<IN>& o, int i) {
+    if (!TINY) o.load(x, (t + i * nt) * E, V);
+  };
+#pragma unroll
+  for (int u = 0; u < 4; ++u) fetch(r[u], u);
+  if (TINY) r[0].tiny(x, t == 0 ? V : 0);
+  for (int i = 0; i < turns; i += 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (i + u < turns) {
+        if (!TINY && (i + u + 1) * nt * E > V) r[u].cut((t + (i + u) * nt) * E, V);
+        sm = fmaxf(sm, sum.add(r[u], scale));
+      }
+      fetch(r[u], i + 4 + u);
+    }
+    if ((i + 4) % each == 0 || i + 4 >= turns) {
+      slot[i / each * nt + t] = top_key(sm);
+      m = fmaxf(m, sm);
+      sm = -INFINITY;
+    }
+  }
+  // NaN (or an infinity) somewhere: the maxima know nothing of it, so all of the thread's slots are looked at
+  if (sum.s != sum.s)
+    for (int s = 0; s < nslots; ++s) slot[s * nt + t] = 0xFFFFFFFFu;
+
+  // the bound
+  const uint32_t mk = top_key(m), wm = dpp_wave_umax(mk);
   const int c = (k + nw - 1) / nw;
-  const uint32_t sorted = wave_sort_desc(m);
-  // fewer maxima than k: no bound
-  if (lane == 0) bound[0][wave] = wm;
-  if (lane == min(c, 64) - 1) bound[1][wave] = c <= 64 ? sorted : 0;
+  const uint32_t sorted = wave_sort_desc(mk);
+  const float wr = dpp_wave_fmax(sum.ref);
+  const float ws = dpp_wave_fsum(sum.s * __builtin_amdgcn_exp2f(sum.ref - wr));
+  if (lane == 0) {
+    bound[0][wave] = wm;
+    fsum[wave] = make_float2(wr, ws);
+  }
+  if (lane == min(c, 64) - 1) bound[1][wave] = c <= 64 ? sorted : KEY_NEG_INF;  // fewer maxima than k: no bound
   __syncthreads();
   uint32_t rowmax = 0, tau = 0xFFFFFFFFu;
   for (int i = 0; i < nw; ++i) {
     rowmax = max(rowmax, bound[0][i]);
     tau = min(tau, bound[1][i]);
   }
+  const float2 fs = fsum[min(lane & 15, nw - 1)];
+  const float ref = row16_max(fs.x);
+  float total = row16_sum((lane & 15) < nw ? fs.y * __builtin_amdgcn_exp2f(fs.x - ref) : 0.0f);
 
-  // the list, how many lie above the bound, and the sum of exponentials
-  const float mv = rowmax == KEY_NEG_INF ? 0.0f : key_val(rowmax), scale = LOG2E / a.temperature;
-  float sum = 0.0f;
-  int above = 0;
-  for (int i = 0; i < turns; ++i)
-    r.run(i, [&](uint32_t key, int token) {
-      sum += __builtin_amdgcn_exp2f((key_val(key) - mv) * scale);
-      if (key >= tau) {
-        above += key > tau;
-        const int at = atomicAdd(&nlist, 1);
-        if (at < TOP_CAP) list[at] = ((uint64_t)key << 32) | (uint32_t)~token;
-      }
-    });
-  sum = dpp_wave_fsum(sum);
-  if (lane == 0) fsum[wave] = sum;
-  if (above) atomicAdd(&nabove, above);
+  // the slots that reach it
+  for (int s = 0; s < nslots; ++s)
+    if (slot[s * nt + t] > tau) {
+      const int at = atomicAdd(&nabove, 1);
+      if (at < TOP_HITS) hits[at] = (uint32_t)(s * nt + t);
+    }
   __syncthreads();
-  if (a.lse && t == 0) {
-    double s = 0.0;
-    for (int i = 0; i < nw; ++i) s += (double)fsum[i];
-    float lse = (float)((double)mv / (double)a.temperature + log(s));
-    if (rowmax == 0xFFFFFFFFu) lse = NAN;
-    else if (mv == INFINITY) lse = INFINITY;
-    a.lse[row] = lse;
+  const int above = nabove;
+  for (int s = 0; s < nslots; ++s)
+    if (slot[s * nt + t] == tau) {
+      const int at = above + atomicAdd(&nat, 1);
+      if (at < TOP_HITS) hits[at] = (uint32_t)(s * nt + t);
+    }
+  __syncthreads();
+  const int reach = above + nat;
+  auto push = [&](uint32_t key, int token) {
+    const int at = atomicAdd(&nlist, 1);
+    if (at < TOP_CAP) list[at] = ((uint64_t)key << 32) | (uint32_t)~token;
+  };
+  auto collect = [&](int n, uint32_t over) {  // logits above `over`
+    for (int h = t; h < n * each; h += nt) {
+      const int id = (int)hits[h / each], s = id / nt, i = s * each + h % each;
+      if (i < turns)
+        again(i, id - s * nt, [&](float v, int token) {
+          if (top_key(v) > over) push(top_key(v), token);
+        });
+    }
+    __syncthreads();
+  };
+  int n = TOP_CAP + 1;
+  if (reach <= TOP_HITS) {
+    collect(reach, tau - 1);  // no key is below that of -inf
+    n = nlist;
   }
-  int n = nlist;
+  if (n > TOP_CAP && above <= TOP_HITS) {
+    __syncthreads();
+    if (t == 0) nlist = 0;
+    __syncthreads();
+    collect(above, tau);
+    n = nlist;
+    if (n < k) {
+      // and those at the bound, among the first tokens
+      __syncthreads();
+      for (int j = t; j < min(V, TOP_CAP - n); j += nt)
+        if (top_key(load1<IN>(x, j)) == tau) push(tau, j);
+      __syncthreads();
+      n = nlist < k ? TOP_CAP + 1 : nlist;
+    }
+  }
   if (n > TOP_CAP) {
-    // the k-th largest key: the bound itself, or by digits
-    if (nabove >= k) {
-      uint32_t known = 0;
-      int left = k;  // the place of the key among those that begin with the known digits
-      for (int s = 24; s >= 0; s -= 8) {
-        __syncthreads();
-        for (int i = t; i < 256; i += nt) hist[i] = 0;
-        __syncthreads();
-        for (int i = 0; i < turns; ++i)
-          r.run(i, [&](uint32_t key, int) {
-            if (key >= tau && (s == 24 || (key >> (s + 8)) == (known >> (s + 8)))) atomicAdd(&hist[(key >> s) & 255], 1);
-          });
-        __syncthreads();
-        if (t == 0) {
-          int d = 255, over = 0;
-          while (d > 0 && over + hist[d] < left) over += hist[d--];
-          pick = d;
-          need = left - over;
-        }
-        __syncthreads();
-        known |= (uint32_t)pick << s;
-        left = need;
+    // the k-th largest key, by digits
+    uint32_t known = 0;
+    int left = k;  // its place among those that begin with the known digits
+    for (int s = 24; s >= 0; s -= 8) {
+      __syncthreads();
+      for (int i = t; i < 256; i += nt) hist[i] = 0;
+      __syncthreads();
+      for (int i = 0; i < turns; ++i)
+        again(i, t, [&](float v, int) {
+          const uint32_t key = top_key(v);
+          if (key >= tau && (s == 24 || (key >> (s + 8)) == (known >> (s + 8)))) atomicAdd(&hist[(key >> s) & 255], 1);
+        });
+      __syncthreads();
+      if (t == 0) {
+        int d = 255, over = 0;
+        while (d > 0 && over + hist[d] < left) over += hist[d--];
+        pick = d;
+        need = left - over;
       }
-      tau = known;
+      __syncthreads();
+      known |= (uint32_t)pick << s;
+      left = need;
     }
     // what is above it, and as many of the equal ones as k leaves, by token
-    __syncthreads();
+    int32_t* count = reinterpret_cast<int32_t*>(hits);
+    static_assert(TOP_HITS >= TOP_TURNS, "a count for each turn");
     for (int i = t; i < turns; i += nt) count[i] = 0;
     if (t == 0) nlist = 0;
     __syncthreads();
     for (int i = 0; i < turns; ++i) {
       int eq = 0;
-      r.run(i, [&](uint32_t key, int token) {
-        if (key > tau) list[atomicAdd(&nlist, 1)] = ((uint64_t)key << 32) | (uint32_t)~token;
-        eq += key == tau;
+      again(i, t, [&](float v, int token) {
+        const uint32_t key = top_key(v);
+        if (key > known) push(key, token);
+        eq += key == known;
       });
       if (eq) atomicAdd(&count[i], eq);
     }
     __syncthreads();
-    int left = k - nlist, last = 0;  // the turn in which the equal ones reach k
+    left = k - nlist;
+    int last = 0;  // the turn in which the equal ones reach k
     while (left > count[last]) left -= count[last++];
     __syncthreads();
     for (int i = 0; i < last; ++i)
-      r.run(i, [&](uint32_t key, int token) {
-        if (key == tau) list[atomicAdd(&nlist, 1)] = ((uint64_t)key << 32) | (uint32_t)~token;
+      again(i, t, [&](float v, int token) {
+        if (top_key(v) == known) push(known, token);
       });
     int eq = 0;
-    r.run(last, [&](uint32_t key, int) { eq += key == tau; });
+    again(last, t, [&](float v, int) { eq += top_key(v) == known; });
     const int before = (int)wave_scan_u32((uint32_t)eq) - eq;
     if (lane == 63) wcount[wave] = before + eq;
     __syncthreads();
     int at = before;
     for (int i = 0; i < wave; ++i) at += wcount[i];
-    r.run(last, [&](uint32_t key, int token) {
-      if (key == tau && at++ < left) list[atomicAdd(&nlist, 1)] = ((uint64_t)key << 32) | (uint32_t)~token;
+    again(last, t, [&](float v, int token) {
+      if (top_key(v) == known && at++ < left) push(known, token);
     });
     __syncthreads();
     n = nlist;
   }
-  for (int i = t; i < n; i += nt) {
+  // each entry's place, by as many lanes as there are for it
+  int lg = 0;
+  while (lg < 4 && (n << (lg + 1)) <= nt) ++lg;
+  const int by = 1 << lg;
+  for (int i = t >> lg; i < n; i += nt >> lg) {
     const uint64_t mine = list[i];
     int place = 0;
-    for (int o = 0; o < n; ++o) place += list[o] > mine;
-    if (place < k) {
+    for (int o = t & (by - 1); o < n; o += by) place += list[o] > mine;
+    for (int o = 1; o < by; o <<= 1) place += __shfl_xor(place, o);
+    if ((t & (by - 1)) == 0 && place < k) {
       const int token = (int)~(uint32_t)mine;
       a.index[(size_t)row * k + place] = token;
-      a.values[(size_t)row * k + place] = load1<IN>(r.p, token);
+      a.values[(size_t)row * k + place] = load1<IN>(x, token);
     }
   }
+  if (!a.lse) return;
+  const float top = key_val(rowmax);
+  double base = (double)ref / (double)scale;
+  const bool slow = !(total > 0.0f && total < INFINITY) && !(rowmax == KEY_NEG_INF && total == 0.0f);
+  if (slow) {
+    // NaN, infinities, or logits next to the type's largest or lowest value: relative to the maximum itself
+    float e = 0.0f;
+    int nan = 0;
+    for (int i = 0; i < turns; ++i)
+      again(i, t, [&](float v, int) {
+        e += __builtin_amdgcn_exp2f((v - top) * scale);
+        nan |= v != v;
+      });
+    e = dpp_wave_fsum(e);
+    if (nan) nans = 1;
+    __syncthreads();
+    if (lane == 0) fsum[wave].y = e;
+    __syncthreads();
+    total = row16_sum((lane & 15) < nw ? fsum[min(lane & 15, nw - 1)].y : 0.0f);
+    base = (double)top;
+  }
+  if (t == 0) {
+    float lse = (float)(base / (double)a.temperature + log((double)total));
+    if (rowmax == KEY_NEG_INF || top == INFINITY) lse = top;
+    if (slow && nans) lse = NAN;
+    a.lse[row] = lse;
+  }
+}
+
+template <int IN, bool TINY>
+hipError_t launch_top(const TopArgs& a, const TopShape& l, hipStream_t s) {
+  const size_t lds = (size_t)l.slots() * (size_t)l.nt * 4;
+  if (lds > 32 * 1024) {
+    const hipError_t e =
+        hipFuncSetAttribute((const void*)top_kernel<IN, TINY>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((top_kernel<IN, TINY>), dim3((unsigned)a.rows), dim3((unsigned)l.nt), lds, s, a);
+  return hipGetLastError();
+}
+
+template <int IN>
+hipError_t launch_top(const TopArgs& a, const TopShape& l, hipStream_t s) {
+  return a.V < Run<IN>::E ? launch_top<IN, true>(a, l, s) : launch_top<IN, false>(a, l, s);
 }
 
 }  // namespace
@@ -207,9 +340,8 @@ extern "C" int sv_top_logits(const void* logits, int32_t k, float temperature, f
   if (rows < 0 || V < 1 || V > SV_MAX_V || k < 1 || k > SV_MAX_TOP || k > V) return SV_ERR_SHAPE;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
   if (!(temperature >= FLT_MIN) || !std::isfinite(temperature)) return SV_ERR_PARAM;
-  // whole waves of threads that all have a run, where there are as many
-  const int e = dtype == SV_F32 ? 4 : 8, nt = std::min(1024, std::max(64, (V + e - 1) / e / 64 * 64));
-  if ((int64_t)rows * nt > kGridThreads) return SV_ERR_SHAPE;
+  const TopShape l(V, k, dtype == SV_F32 ? 4 : 8);
+  if ((int64_t)rows * l.nt > kGridThreads) return SV_ERR_SHAPE;
   if (rows == 0) return SV_OK;
   if (!logits || !out_values || !out_index) return SV_ERR_NULL;
   const size_t ie = (size_t)type_bytes(dtype), nin = (size_t)rows * (size_t)V * ie, no = (size_t)rows * (size_t)k * 4;
@@ -219,11 +351,8 @@ extern "C" int sv_top_logits(const void* logits, int32_t k, float temperature, f
   if (overlaps(out_values, no, logits, nin) || overlaps(out_index, no, logits, nin) || overlaps(out_lse, nl, logits, nin) ||
       overlaps(out_values, no, out_index, no) || overlaps(out_values, no, out_lse, nl) || overlaps(out_index, no, out_lse, nl))
     return SV_ERR_PARAM;
-  const TopArgs a{logits, out_values, out_index, out_lse, rows, V, k, temperature};
-  const dim3 grid((unsigned)rows), wg((unsigned)nt);
-  if (dtype == SV_F32)
-    hipLaunchKernelGGL((top_kernel<T_F32>), grid, wg, 0, (hipStream_t)stream, a);
-  else
-    hipLaunchKernelGGL((top_kernel<T_BF16>), grid, wg, 0, (hipStream_t)stream, a);
-  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+  const TopArgs a{logits, out_values, out_index, out_lse, rows, V, k, l.turns, l.each, temperature};
+  const hipError_t err =
+      dtype == SV_F32 ? launch_top<T_F32>(a, l, (hipStream_t)stream) : launch_top<T_BF16>(a, l, (hipStream_t)stream);
+  return err == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
