@@ -129,12 +129,13 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
     uint32_t mk[(MB + 3) / 4];
     __builtin_memcpy(mk, __builtin_assume_aligned(bytes + t * MB, MB & -MB), MB);
     RunSum acc;
+    float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
       j0 = fresh(j0);
       take(r[i], i, E == 8 ? mk[i / 4] >> (i % 4 * 8) & 255 : mk[i / 8] >> (i % 8 * 4) & 15);
       r[i].forget();
-      acc.add(r[i], scale);
+      acc.add<false>(r[i], scale, mx);
       __builtin_amdgcn_sched_barrier(0);  // one run at a time: more would not fit the registers
     }
     constexpr int AHEAD = 4;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
           }
       }
     };
-    if (MORE) stream([&](const Run<IN>& v, int) { acc.add(v, scale); });
+    if (MORE) stream([&](const Run<IN>& v, int) { acc.add<false>(v, scale, mx); });
     // the list's maxima
     float tm = -INFINITY, sm = -INFINITY;
     auto entry = [&](int j, float y, float s) {
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
     const float ws = dpp_wave_fsum(acc.s * __builtin_amdgcn_exp2f(acc.ref - wr));
     tm = dpp_wave_fmax(tm), sm = dpp_wave_fmax(sm);
     if (lane == 0) fmx[wave] = make_float4(wr, ws, tm, sm);
-    if (lane == 0) fany[wave] = __any(acc.any) ? 1.0f : 0.0f;
+    if (lane == 0) fany[wave] = __any(mx > -INFINITY) ? 1.0f : 0.0f;
     __syncthreads();
     const int from = min(lane & 15, nw - 1);
     const float4 wv = fmx[from];

@@ -78,25 +78,26 @@ __device__ __forceinline__ int fresh(int v) {
 // NaN, and the row takes the slow way below.
 struct RunSum {
   float ref = -FLT_MAX, s = 0.0f;
-  bool any = false;  // something above -inf was added
-  // returns the run's maximum (NaN apart)
-  template <int IN>
-  __device__ __forceinline__ float add(const Run<IN>& r, float scale) {
+  // mx: the running maximum (NaN apart).  BRANCH: pass over the new reference where no lane of the wave has one
+  // (few times a row one has; it costs registers)
+  template <bool BRANCH, int IN>
+  __device__ __forceinline__ void add(const Run<IN>& r, float scale, float& mx) {
     constexpr int E = Run<IN>::E;
-    float x = r[0];
 #pragma unroll
-    for (int k = 1; k < E; ++k) x = fmaxf(x, r[k]);
-    any |= x > -INFINITY;
-    const float y = x * scale;
-    if (y > ref + 8.0f) {
-      s *= __builtin_amdgcn_exp2f(ref - y);
-      ref = y;
+    for (int k = 0; k < E; ++k) mx = fmaxf(mx, r[k]);
+    const float y = mx * scale;
+    if (!BRANCH || __any(y > ref + 8.0f)) {
+      const float n = y > ref + 8.0f ? y : ref;
+      s *= __builtin_amdgcn_exp2f(ref - n);
+      ref = n;
     }
-    float p[2] = {0.0f, 0.0f};
+    float p[2];
 #pragma unroll
-    for (int k = 0; k < E; ++k) p[k & 1] += __builtin_amdgcn_exp2f(__builtin_fmaf(r[k], scale, -ref));
+    for (int k = 0; k < E; ++k) {
+      const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(r[k], scale, -ref));
+      p[k & 1] = k < 2 ? e : p[k & 1] + e;
+    }
     s += p[0] + p[1];
-    return x;
   }
 };
 

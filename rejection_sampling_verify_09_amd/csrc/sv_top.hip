@@ -27,23 +27,32 @@ namespace sv {
 
 namespace {
 
-constexpr int TOP_CAP = 2048;   // entries of the list; at least 2 SV_MAX_TOP
-constexpr int TOP_HITS = 2048;  // slots read again
+constexpr int TOP_CAP = 2048;   // entries of the list, at most; at least 2 SV_MAX_TOP
+constexpr int TOP_HITS = 2048;  // slots read again, at most
 constexpr int TOP_SLOTS = 16;   // slots a thread, at most
 constexpr int TOP_TURNS = 512;  // runs a thread, at most: SV_MAX_V / 4 runs on 1024 threads
+constexpr int TOP_BINS = 512;
+constexpr int TOP_RANK = 128;  // lists up to sqrt(128 threads) entries are ranked
 
 struct TopArgs {
   const void* x;
   float* values;
   int32_t* index;
   float* lse;
-  int32_t rows, V, k, turns, each;
+  int32_t rows, V, k, turns, each, cap, hits;
   float temperature;
 };
 
 // ord_key with -0 as +0 and NaN above everything.
 __device__ __forceinline__ uint32_t top_key(float x) {
   return x != x ? 0xFFFFFFFFu : ord_key(x + 0.0f);
+}
+
+// What this wave has written to LDS is there for what it reads next: its LDS
+// instructions are carried out in their order, which the compiler has to keep.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // Largest first: a wave's 64 keys.
@@ -60,6 +69,29 @@ __device__ __forceinline__ uint32_t wave_sort_desc(uint32_t v) {
   return v;
 }
 
+// The list's first n entries, largest first, by nt threads: a bitonic sort.
+// Pairs 64 b .. 64 b + 63 of a stage lie within 128 entries up to a distance of
+// 64, and are one wave's in every such stage, which then needs no barrier.
+__device__ __forceinline__ void sort_list(uint64_t* list, int n, int nt) {
+  int all = 2;
+  while (all < n) all <<= 1;
+  for (int i = n + threadIdx.x; i < all; i += nt) list[i] = 0;
+  __syncthreads();
+  for (int len = 2; len <= all; len <<= 1)
+    for (int j = len >> 1; j > 0; j >>= 1) {
+      for (int p = threadIdx.x; p < all >> 1; p += nt) {
+        const int i = ((p & -j) << 1) | (p & (j - 1));
+        const uint64_t x = list[i], y = list[i + j];
+        if ((i & len) == 0 ? x < y : x > y) list[i] = y, list[i + j] = x;
+      }
+      if (j > 64 || (j == 1 && len >= 128))
+        __syncthreads();
+      else
+        wave_order();
+    }
+  __syncthreads();
+}
+
 // A row's launch: threads, runs a thread, and runs a slot.
 struct TopShape {
   int nt, turns, each;
@@ -73,21 +105,68 @@ struct TopShape {
     each = ((turns + 3) / 4 + TOP_SLOTS - 1) / TOP_SLOTS * 4;
   }
   int slots() const { return (turns + each - 1) / each; }
+  // what a short row cannot fill is not set aside: more workgroups a compute unit
+  int cap(int V) const {
+    int n = 64;
+    while (n < V && n < TOP_CAP) n <<= 1;
+    return n;
+  }
+  int hits() const { return std::min(TOP_HITS, slots() * nt); }
+  size_t lds(int V) const { return (size_t)cap(V) * 8 + (size_t)(hits() + slots() * nt) * 4; }
 };
+
+// Of keys at or above tau, a value that at least k of them reach and few more do
+// (tau where they are fewer than k): from a histogram over [tau, rowmax].  each(f): f(key) for each of
+// this thread's; hist: TOP_BINS counts, found: one word.
+template <typename F>
+__device__ __forceinline__ uint32_t narrow(uint32_t tau, uint32_t rowmax, int k, int32_t* hist, uint32_t* found, int nt, F&& each) {
+  const int t = threadIdx.x;
+  const uint32_t range = rowmax > tau ? rowmax - tau : 0;
+  int sh = 0;
+  while (range >> sh >= TOP_BINS) ++sh;
+  __syncthreads();
+  for (int i = t; i < TOP_BINS; i += nt) hist[i] = 0;
+  if (t == 0) *found = tau;
+  __syncthreads();
+  each([&](uint32_t key) {
+    if (key >= tau) atomicAdd(&hist[min((key - tau) >> sh, (uint32_t)TOP_BINS - 1)], 1);
+  });
+  __syncthreads();
+  if (t < 64) {
+    // from the top: lane l the bins below TOP_BINS - 8 l
+    constexpr int PER = TOP_BINS / 64;
+    int n[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += n[i] = hist[TOP_BINS - 1 - t * PER - i];
+    int over = (int)wave_scan_u32((uint32_t)sum) - sum;
+    if (over < k && over + sum >= k) {
+      int i = 0;
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        over += n[u];
+        if (over < k) i = u + 1;
+      }
+      *found = tau + ((uint32_t)(TOP_BINS - 1 - t * PER - i) << sh);
+    }
+  }
+  __syncthreads();
+  return *found;
+}
 
 // TINY: rows shorter than a run.
 template <int IN, bool TINY>
 __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
   constexpr int E = Run<IN>::E;
-  extern __shared__ uint32_t slot[];  // [slots][nt] the slot's largest key
-  __shared__ uint64_t list[TOP_CAP];
-  // slots above the bound, then those at it; later the number of equal logits of each turn
-  __shared__ uint32_t hits[TOP_HITS];
+  extern __shared__ uint64_t list[];  // [cap]
   __shared__ uint32_t bound[2][16];
   __shared__ float2 fsum[16];
-  __shared__ int32_t hist[256];
+  __shared__ int32_t hist[TOP_BINS];
   __shared__ int32_t wcount[16];
   __shared__ int32_t nlist, nabove, nat, pick, need, nans;
+  __shared__ uint32_t found;
+  const int cap = a.cap, mhits = a.hits;
+  uint32_t* hits = reinterpret_cast<uint32_t*>(list + cap);  // [mhits] slots above the bound, then those at it
+  uint32_t* slot = hits + mhits;                             // [slots][nt] the slot's largest key
   const int t = threadIdx.x, nt = blockDim.x, nw = nt >> 6, lane = t & 63, wave = t >> 6;
   const int row = blockIdx.x, V = a.V, k = a.k, turns = a.turns, each = a.each, nslots = (turns + each - 1) / each;
   const char* x = static_cast<const char*>(a.x) + (size_t)row * V * Run<IN>::B;
@@ -117,14 +196,17 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
     if (!TINY) o.load(x, (t + i * nt) * E, V);
   };
 #pragma unroll
-  for (int u = 0; u < 4; ++u) fetch(r[u], u);
+  for (int u = 0; u < 4; ++u) {
+    fetch(r[u], u);
+    __builtin_amdgcn_sched_barrier(0);  // in the order of the loop, whose waits count on it
+  }
   if (TINY) r[0].tiny(x, t == 0 ? V : 0);
   for (int i = 0; i < turns; i += 4) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       if (i + u < turns) {
         if (!TINY && (i + u + 1) * nt * E > V) r[u].cut((t + (i + u) * nt) * E, V);
-        sm = fmaxf(sm, sum.add(r[u], scale));
+        sum.add<true>(r[u], scale, sm);
       }
       fetch(r[u], i + 4 + u);
     }
@@ -163,20 +245,20 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
   for (int s = 0; s < nslots; ++s)
     if (slot[s * nt + t] > tau) {
       const int at = atomicAdd(&nabove, 1);
-      if (at < TOP_HITS) hits[at] = (uint32_t)(s * nt + t);
+      if (at < mhits) hits[at] = (uint32_t)(s * nt + t);
     }
   __syncthreads();
   const int above = nabove;
   for (int s = 0; s < nslots; ++s)
     if (slot[s * nt + t] == tau) {
       const int at = above + atomicAdd(&nat, 1);
-      if (at < TOP_HITS) hits[at] = (uint32_t)(s * nt + t);
+      if (at < mhits) hits[at] = (uint32_t)(s * nt + t);
     }
   __syncthreads();
   const int reach = above + nat;
   auto push = [&](uint32_t key, int token) {
     const int at = atomicAdd(&nlist, 1);
-    if (at < TOP_CAP) list[at] = ((uint64_t)key << 32) | (uint32_t)~token;
+    if (at < cap) list[at] = ((uint64_t)key << 32) | (uint32_t)~token;
   };
   auto collect = [&](int n, uint32_t over) {  // logits above `over`
     for (int h = t; h < n * each; h += nt) {
@@ -188,12 +270,12 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
     }
     __syncthreads();
   };
-  int n = TOP_CAP + 1;
-  if (reach <= TOP_HITS) {
+  int n = cap + 1;
+  if (reach <= mhits) {
     collect(reach, tau - 1);  // no key is below that of -inf
     n = nlist;
   }
-  if (n > TOP_CAP && above <= TOP_HITS) {
+  if (n > cap && above <= mhits) {
     __syncthreads();
     if (t == 0) nlist = 0;
     __syncthreads();
@@ -202,13 +284,13 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
     if (n < k) {
       // and those at the bound, among the first tokens
       __syncthreads();
-      for (int j = t; j < min(V, TOP_CAP - n); j += nt)
+      for (int j = t; j < min(V, cap - n); j += nt)
         if (top_key(load1<IN>(x, j)) == tau) push(tau, j);
       __syncthreads();
-      n = nlist < k ? TOP_CAP + 1 : nlist;
+      n = nlist < k ? cap + 1 : nlist;
     }
   }
-  if (n > TOP_CAP) {
+  if (n > cap) {
     // the k-th largest key, by digits
     uint32_t known = 0;
     int left = k;  // its place among those that begin with the known digits
@@ -233,8 +315,9 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
       left = need;
     }
     // what is above it, and as many of the equal ones as k leaves, by token
-    int32_t* count = reinterpret_cast<int32_t*>(hits);
-    static_assert(TOP_HITS >= TOP_TURNS, "a count for each turn");
+    int32_t* count = reinterpret_cast<int32_t*>(slot);  // the equal ones of each turn: at most 4 slots of 64 threads
+    static_assert(TOP_TURNS <= 64 * TOP_SLOTS, "a word for each turn");
+    __syncthreads();
     for (int i = t; i < turns; i += nt) count[i] = 0;
     if (t == 0) nlist = 0;
     __syncthreads();
@@ -269,20 +352,42 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
     __syncthreads();
     n = nlist;
   }
-  // each entry's place, by as many lanes as there are for it
-  int lg = 0;
-  while (lg < 4 && (n << (lg + 1)) <= nt) ++lg;
-  const int by = 1 << lg;
-  for (int i = t >> lg; i < n; i += nt >> lg) {
-    const uint64_t mine = list[i];
-    int place = 0;
-    for (int o = t & (by - 1); o < n; o += by) place += list[o] > mine;
-    for (int o = 1; o < by; o <<= 1) place += __shfl_xor(place, o);
-    if ((t & (by - 1)) == 0 && place < k) {
-      const int token = (int)~(uint32_t)mine;
-      a.index[(size_t)row * k + place] = token;
-      a.values[(size_t)row * k + place] = load1<IN>(x, token);
+  auto put = [&](uint64_t entry, int place) {
+    const int token = (int)~(uint32_t)entry;
+    a.index[(size_t)row * k + place] = token;
+    a.values[(size_t)row * k + place] = load1<IN>(x, token);
+  };
+  // what is ranked or sorted is not much longer than k
+  if (n * n > TOP_RANK * nt && n > k + k / 4) {
+    const uint32_t low = narrow(tau, rowmax, k, hist, &found, nt, [&](auto&& f) {
+      for (int i = t; i < n; i += nt) f((uint32_t)(list[i] >> 32));
+    });
+    __syncthreads();
+    if (t == 0) nlist = 0;
+    for (int i = 0; i < n; i += nt) {
+      // entries go to places that have been read
+      const uint64_t e = i + t < n ? list[i + t] : 0;
+      __syncthreads();
+      if ((uint32_t)(e >> 32) >= low) list[atomicAdd(&nlist, 1)] = e;
+      __syncthreads();
     }
+    n = nlist;
+  }
+  if (n * n <= TOP_RANK * nt) {
+    // each entry's place, by as many lanes as there are for it
+    int lg = 0;
+    while (lg < 4 && (n << (lg + 1)) <= nt) ++lg;
+    const int by = 1 << lg;
+    for (int i = t >> lg; i < n; i += nt >> lg) {
+      const uint64_t mine = list[i];
+      int place = 0;
+      for (int o = t & (by - 1); o < n; o += by) place += list[o] > mine;
+      for (int o = 1; o < by; o <<= 1) place += __shfl_xor(place, o);
+      if ((t & (by - 1)) == 0 && place < k) put(mine, place);
+    }
+  } else {
+    sort_list(list, n, nt);
+    for (int i = t; i < k; i += nt) put(list[i], i);
   }
   if (!a.lse) return;
   const float top = key_val(rowmax);
@@ -315,7 +420,7 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
 
 template <int IN, bool TINY>
 hipError_t launch_top(const TopArgs& a, const TopShape& l, hipStream_t s) {
-  const size_t lds = (size_t)l.slots() * (size_t)l.nt * 4;
+  const size_t lds = l.lds(a.V);
   if (lds > 32 * 1024) {
     const hipError_t e =
         hipFuncSetAttribute((const void*)top_kernel<IN, TINY>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -351,7 +456,7 @@ extern "C" int sv_top_logits(const void* logits, int32_t k, float temperature, f
   if (overlaps(out_values, no, logits, nin) || overlaps(out_index, no, logits, nin) || overlaps(out_lse, nl, logits, nin) ||
       overlaps(out_values, no, out_index, no) || overlaps(out_values, no, out_lse, nl) || overlaps(out_index, no, out_lse, nl))
     return SV_ERR_PARAM;
-  const TopArgs a{logits, out_values, out_index, out_lse, rows, V, k, l.turns, l.each, temperature};
+  const TopArgs a{logits, out_values, out_index, out_lse, rows, V, k, l.turns, l.each, l.cap(V), l.hits(), temperature};
   const hipError_t err =
       dtype == SV_F32 ? launch_top<T_F32>(a, l, (hipStream_t)stream) : launch_top<T_BF16>(a, l, (hipStream_t)stream);
   return err == hipSuccess ? SV_OK : SV_ERR_HIP;
