@@ -32,7 +32,8 @@ constexpr int TOP_HITS = 2048;  // slots read again, at most
 constexpr int TOP_SLOTS = 16;   // slots a thread, at most
 constexpr int TOP_TURNS = 512;  // runs a thread, at most: SV_MAX_V / 4 runs on 1024 threads
 constexpr int TOP_BINS = 512;
-constexpr int TOP_RANK = 128;  // lists up to sqrt(128 threads) entries are ranked
+constexpr int TOP_TAKE = 8;
+constexpr int TOP_RANK = 16;  // lists up to sqrt(16 threads) entries are ranked one against all
 
 struct TopArgs {
   const void* x;
@@ -48,13 +49,6 @@ __device__ __forceinline__ uint32_t top_key(float x) {
   return x != x ? 0xFFFFFFFFu : ord_key(x + 0.0f);
 }
 
-// What this wave has written to LDS is there for what it reads next: its LDS
-// instructions are carried out in their order, which the compiler has to keep.
-__device__ __forceinline__ void wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // Largest first: a wave's 64 keys.
 __device__ __forceinline__ uint32_t wave_sort_desc(uint32_t v) {
   const int l = threadIdx.x & 63;
@@ -67,29 +61,6 @@ __device__ __forceinline__ uint32_t wave_sort_desc(uint32_t v) {
       v = up ? max(v, o) : min(v, o);
     }
   return v;
-}
-
-// The list's first n entries, largest first, by nt threads: a bitonic sort.
-// Pairs 64 b .. 64 b + 63 of a stage lie within 128 entries up to a distance of
-// 64, and are one wave's in every such stage, which then needs no barrier.
-__device__ __forceinline__ void sort_list(uint64_t* list, int n, int nt) {
-  int all = 2;
-  while (all < n) all <<= 1;
-  for (int i = n + threadIdx.x; i < all; i += nt) list[i] = 0;
-  __syncthreads();
-  for (int len = 2; len <= all; len <<= 1)
-    for (int j = len >> 1; j > 0; j >>= 1) {
-      for (int p = threadIdx.x; p < all >> 1; p += nt) {
-        const int i = ((p & -j) << 1) | (p & (j - 1));
-        const uint64_t x = list[i], y = list[i + j];
-        if ((i & len) == 0 ? x < y : x > y) list[i] = y, list[i + j] = x;
-      }
-      if (j > 64 || (j == 1 && len >= 128))
-        __syncthreads();
-      else
-        wave_order();
-    }
-  __syncthreads();
 }
 
 // A row's launch: threads, runs a thread, and runs a slot.
@@ -111,47 +82,30 @@ struct TopShape {
     while (n < V && n < TOP_CAP) n <<= 1;
     return n;
   }
-  int hits() const { return std::min(TOP_HITS, slots() * nt); }
-  size_t lds(int V) const { return (size_t)cap(V) * 8 + (size_t)(hits() + slots() * nt) * 4; }
+  int hits(int V) const { return std::max(std::min(TOP_HITS, slots() * nt), cap(V) / 2); }
+  size_t lds(int V) const { return (size_t)cap(V) * 8 + (size_t)(hits(V) + slots() * nt) * 4; }
 };
 
-// Of keys at or above tau, a value that at least k of them reach and few more do
-// (tau where they are fewer than k): from a histogram over [tau, rowmax].  each(f): f(key) for each of
-// this thread's; hist: TOP_BINS counts, found: one word.
-template <typename F>
-__device__ __forceinline__ uint32_t narrow(uint32_t tau, uint32_t rowmax, int k, int32_t* hist, uint32_t* found, int nt, F&& each) {
-  const int t = threadIdx.x;
-  const uint32_t range = rowmax > tau ? rowmax - tau : 0;
-  int sh = 0;
-  while (range >> sh >= TOP_BINS) ++sh;
-  __syncthreads();
-  for (int i = t; i < TOP_BINS; i += nt) hist[i] = 0;
-  if (t == 0) *found = tau;
-  __syncthreads();
-  each([&](uint32_t key) {
-    if (key >= tau) atomicAdd(&hist[min((key - tau) >> sh, (uint32_t)TOP_BINS - 1)], 1);
-  });
-  __syncthreads();
-  if (t < 64) {
-    // from the top: lane l the bins below TOP_BINS - 8 l
-    constexpr int PER = TOP_BINS / 64;
-    int n[PER], sum = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) sum += n[i] = hist[TOP_BINS - 1 - t * PER - i];
-    int over = (int)wave_scan_u32((uint32_t)sum) - sum;
-    if (over < k && over + sum >= k) {
-      int i = 0;
-#pragma unroll
-      for (int u = 0; u < PER; ++u) {
-        over += n[u];
-        if (over < k) i = u + 1;
-      }
-      *found = tau + ((uint32_t)(TOP_BINS - 1 - t * PER - i) << sh);
-    }
+// A key's bin, of TOP_BINS: rising with the key from tau to rowmax, in equal
+// steps of the value where both are finite, else of the key.
+struct TopBins {
+  uint32_t tau;
+  float lo, mul;
+  int sh;
+  __device__ __forceinline__ TopBins(uint32_t tau, uint32_t rowmax) : tau(tau) {
+    lo = key_val(tau);
+    const float width = key_val(rowmax) - lo;
+    mul = width > 0.0f && width < INFINITY ? (float)TOP_BINS / width : 0.0f;
+    if (!(mul > 0.0f && mul < INFINITY)) mul = 0.0f;
+    sh = 0;
+    while (rowmax > tau && (rowmax - tau) >> sh >= TOP_BINS) ++sh;
   }
-  __syncthreads();
-  return *found;
-}
+  __device__ __forceinline__ int operator()(uint32_t key) const {
+    if (key == 0xFFFFFFFFu) return TOP_BINS - 1;  // NaN
+    if (mul > 0.0f) return (int)fminf((key_val(key) - lo) * mul, (float)(TOP_BINS - 1));
+    return (int)min((key - tau) >> sh, (uint32_t)TOP_BINS - 1);
+  }
+};
 
 // TINY: rows shorter than a run.
 template <int IN, bool TINY>
@@ -163,9 +117,9 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
   __shared__ int32_t hist[TOP_BINS];
   __shared__ int32_t wcount[16];
   __shared__ int32_t nlist, nabove, nat, pick, need, nans;
-  __shared__ uint32_t found;
   const int cap = a.cap, mhits = a.hits;
-  uint32_t* hits = reinterpret_cast<uint32_t*>(list + cap);  // [mhits] slots above the bound, then those at it
+  // [mhits] slots above the bound, then those at it; later the list's order
+  uint32_t* hits = reinterpret_cast<uint32_t*>(list + cap);
   uint32_t* slot = hits + mhits;                             // [slots][nt] the slot's largest key
   const int t = threadIdx.x, nt = blockDim.x, nw = nt >> 6, lane = t & 63, wave = t >> 6;
   const int row = blockIdx.x, V = a.V, k = a.k, turns = a.turns, each = a.each, nslots = (turns + each - 1) / each;
@@ -223,14 +177,25 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
   // the bound
   const uint32_t mk = top_key(m), wm = dpp_wave_umax(mk);
   const int c = (k + nw - 1) / nw;
-  const uint32_t sorted = wave_sort_desc(mk);
+  // the c-th largest of the wave's 64: the larger ones taken out one by one, or all put in order
+  uint32_t cth = mk;
+  if (c <= TOP_TAKE) {
+    uint32_t v = mk;
+    for (int i = 1; i < c; ++i) {
+      const uint64_t same = __ballot(v == dpp_wave_umax(v));
+      if (lane == __ffsll((long long)same) - 1) v = 0;
+    }
+    cth = dpp_wave_umax(v);
+  } else {
+    cth = __shfl(wave_sort_desc(mk), min(c, 64) - 1);
+  }
   const float wr = dpp_wave_fmax(sum.ref);
   const float ws = dpp_wave_fsum(sum.s * __builtin_amdgcn_exp2f(sum.ref - wr));
   if (lane == 0) {
     bound[0][wave] = wm;
+    bound[1][wave] = c <= 64 ? cth : KEY_NEG_INF;  // fewer maxima than k: no bound
     fsum[wave] = make_float2(wr, ws);
   }
-  if (lane == min(c, 64) - 1) bound[1][wave] = c <= 64 ? sorted : KEY_NEG_INF;  // fewer maxima than k: no bound
   __syncthreads();
   uint32_t rowmax = 0, tau = 0xFFFFFFFFu;
   for (int i = 0; i < nw; ++i) {
@@ -357,22 +322,6 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
     a.index[(size_t)row * k + place] = token;
     a.values[(size_t)row * k + place] = load1<IN>(x, token);
   };
-  // what is ranked or sorted is not much longer than k
-  if (n * n > TOP_RANK * nt && n > k + k / 4) {
-    const uint32_t low = narrow(tau, rowmax, k, hist, &found, nt, [&](auto&& f) {
-      for (int i = t; i < n; i += nt) f((uint32_t)(list[i] >> 32));
-    });
-    __syncthreads();
-    if (t == 0) nlist = 0;
-    for (int i = 0; i < n; i += nt) {
-      // entries go to places that have been read
-      const uint64_t e = i + t < n ? list[i + t] : 0;
-      __syncthreads();
-      if ((uint32_t)(e >> 32) >= low) list[atomicAdd(&nlist, 1)] = e;
-      __syncthreads();
-    }
-    n = nlist;
-  }
   if (n * n <= TOP_RANK * nt) {
     // each entry's place, by as many lanes as there are for it
     int lg = 0;
@@ -386,8 +335,39 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
       if ((t & (by - 1)) == 0 && place < k) put(mine, place);
     }
   } else {
-    sort_list(list, n, nt);
-    for (int i = t; i < k; i += nt) put(list[i], i);
+    // by bins, the largest values first: an entry's place is where its bin begins, and the place within
+    const TopBins bin(tau, rowmax);
+    uint16_t* order = reinterpret_cast<uint16_t*>(hits);  // [cap]
+    __syncthreads();
+    for (int i = t; i < TOP_BINS; i += nt) hist[i] = 0;
+    __syncthreads();
+    for (int i = t; i < n; i += nt) atomicAdd(&hist[bin((uint32_t)(list[i] >> 32))], 1);
+    __syncthreads();
+    if (t < 64) {
+      // how many stand before each bin: lane l has the bins below TOP_BINS - 8 l
+      constexpr int PER = TOP_BINS / 64;
+      int c[PER], sum = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) sum += c[i] = hist[TOP_BINS - 1 - t * PER - i];
+      int before = (int)wave_scan_u32((uint32_t)sum) - sum;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        hist[TOP_BINS - 1 - t * PER - i] = before;
+        before += c[i];
+      }
+    }
+    __syncthreads();
+    for (int i = t; i < n; i += nt) order[atomicAdd(&hist[bin((uint32_t)(list[i] >> 32))], 1)] = (uint16_t)i;
+    __syncthreads();
+    // each bin's count has moved on to where it ends
+    for (int i = t; i < n; i += nt) {
+      const uint64_t mine = list[order[i]];
+      const int b = bin((uint32_t)(mine >> 32)), from = b == TOP_BINS - 1 ? 0 : hist[b + 1], to = hist[b];
+      if (from >= k) continue;
+      int place = from;
+      for (int o = from; o < to; ++o) place += list[order[o]] > mine;
+      if (place < k) put(mine, place);
+    }
   }
   if (!a.lse) return;
   const float top = key_val(rowmax);
@@ -456,7 +436,7 @@ extern "C" int sv_top_logits(const void* logits, int32_t k, float temperature, f
   if (overlaps(out_values, no, logits, nin) || overlaps(out_index, no, logits, nin) || overlaps(out_lse, nl, logits, nin) ||
       overlaps(out_values, no, out_index, no) || overlaps(out_values, no, out_lse, nl) || overlaps(out_index, no, out_lse, nl))
     return SV_ERR_PARAM;
-  const TopArgs a{logits, out_values, out_index, out_lse, rows, V, k, l.turns, l.each, l.cap(V), l.hits(), temperature};
+  const TopArgs a{logits, out_values, out_index, out_lse, rows, V, k, l.turns, l.each, l.cap(V), l.hits(V), temperature};
   const hipError_t err =
       dtype == SV_F32 ? launch_top<T_F32>(a, l, (hipStream_t)stream) : launch_top<T_BF16>(a, l, (hipStream_t)stream);
   return err == hipSuccess ? SV_OK : SV_ERR_HIP;
