@@ -67,23 +67,25 @@ __device__ __forceinline__ uint32_t wave_sort_desc(uint32_t v) {
 struct TopShape {
   int nt, turns, each;
   TopShape(int V, int k, int e) {
-    // four runs a thread, as many as are on their way at a time; more threads for long lists, whose bound is the
-    // better the more maxima there are, but none without a run
+    // Eight runs a thread: with four, a compute unit holds fewer rows (2048 x 32000 bfloat16, k = 64: 56 us against 41),
+    // with sixteen a row takes longer (64 x 32000 13.7 against 11.7); of short rows fewer.  More threads for long lists,
+    // whose bound is the better the more maxima there are (8192 x 4096, k = 64: 121 us with 64 threads, 59 with 256, 81
+    // with 512), but none without a run.
     const int runs = (V + e - 1) / e, full = std::max(64, runs / 64 * 64);
-    nt = std::min({1024, full, std::max((runs / 4 + 63) / 64 * 64, (4 * k + 63) / 64 * 64)});
+    nt = std::min({1024, full, std::max({(runs / 8 + 63) / 64 * 64, (4 * k + 63) / 64 * 64, 128})});
     nt = std::max(nt, 64);
     turns = (runs + nt - 1) / nt;
     each = ((turns + 3) / 4 + TOP_SLOTS - 1) / TOP_SLOTS * 4;
   }
   int slots() const { return (turns + each - 1) / each; }
-  // what a short row cannot fill is not set aside: more workgroups a compute unit
-  int cap(int V) const {
+  // entries that the list holds: a few times k, which is what reaches the bound as a rule, and no more than a row has
+  int cap(int V, int k) const {
     int n = 64;
-    while (n < V && n < TOP_CAP) n <<= 1;
+    while (n < V && n < TOP_CAP && (n < 512 || n < 4 * k)) n <<= 1;
     return n;
   }
-  int hits(int V) const { return std::max(std::min(TOP_HITS, slots() * nt), cap(V) / 2); }
-  size_t lds(int V) const { return (size_t)cap(V) * 8 + (size_t)(hits(V) + slots() * nt) * 4; }
+  int hits(int V, int k) const { return std::max(std::min(TOP_HITS, slots() * nt), cap(V, k) / 2); }
+  size_t lds(int V, int k) const { return (size_t)cap(V, k) * 8 + (size_t)(hits(V, k) + slots() * nt) * 4; }
 };
 
 // A key's bin, of TOP_BINS: rising with the key from tau to rowmax, in equal
@@ -107,6 +109,22 @@ struct TopBins {
   }
 };
 
+// Counts of bins into how many stand in the bins above.
+__device__ __forceinline__ void bins_before(int32_t* hist) {
+  const int t = threadIdx.x;
+  if (t >= 64) return;
+  constexpr int PER = TOP_BINS / 64;  // lane l: the bins below TOP_BINS - PER l
+  int c[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) sum += c[i] = hist[TOP_BINS - 1 - t * PER - i];
+  int before = (int)wave_scan_u32((uint32_t)sum) - sum;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    hist[TOP_BINS - 1 - t * PER - i] = before;
+    before += c[i];
+  }
+}
+
 // TINY: rows shorter than a run.
 template <int IN, bool TINY>
 __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
@@ -117,6 +135,7 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
   __shared__ int32_t hist[TOP_BINS];
   __shared__ int32_t wcount[16];
   __shared__ int32_t nlist, nabove, nat, pick, need, nans;
+  __shared__ uint32_t found;
   const int cap = a.cap, mhits = a.hits;
   // [mhits] slots above the bound, then those at it; later the list's order
   uint32_t* hits = reinterpret_cast<uint32_t*>(list + cap);
@@ -125,8 +144,8 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
   const int row = blockIdx.x, V = a.V, k = a.k, turns = a.turns, each = a.each, nslots = (turns + each - 1) / each;
   const char* x = static_cast<const char*>(a.x) + (size_t)row * V * Run<IN>::B;
   const float scale = LOG2E / a.temperature;
-  // f(key, token) for the elements of thread `by`'s run of turn i
-  auto again = [&](int i, int by, auto&& f) {
+  // thread `by`'s run of turn i: f(the run, its first token, how many of its elements are the row's)
+  auto rerun = [&](int i, int by, auto&& f) {
     const int j = (by + i * nt) * E;
     if (j >= V) return;
     Run<IN> r;
@@ -136,9 +155,15 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
       r.load(x, j, V);
       r.cut(j, V);
     }
+    f(r, j, min(V - j, E));
+  };
+  // the same, f(logit, token) for each
+  auto again = [&](int i, int by, auto&& f) {
+    rerun(i, by, [&](const Run<IN>& r, int j, int len) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (j + e < V) f(r[e], j + e);
+      for (int e = 0; e < E; ++e)
+        if (e < len) f(r[e], j + e);
+    });
   };
   if (t == 0) nlist = nabove = nat = nans = 0;
 
@@ -206,39 +231,108 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
   const float ref = row16_max(fs.x);
   float total = row16_sum((lane & 15) < nw ? fs.y * __builtin_amdgcn_exp2f(fs.x - ref) : 0.0f);
 
-  // the slots that reach it
-  for (int s = 0; s < nslots; ++s)
-    if (slot[s * nt + t] > tau) {
-      const int at = atomicAdd(&nabove, 1);
-      if (at < mhits) hits[at] = (uint32_t)(s * nt + t);
+  if (a.lse) {
+    const float top = key_val(rowmax);
+    double base = (double)ref / (double)scale;
+    const bool slow = !(total > 0.0f && total < INFINITY) && !(rowmax == KEY_NEG_INF && total == 0.0f);
+    if (slow) {
+      // NaN, infinities, or logits next to the type's largest or lowest value: relative to the maximum itself
+      float e = 0.0f;
+      int nan = 0;
+      for (int i = 0; i < turns; ++i)
+        again(i, t, [&](float v, int) {
+          e += __builtin_amdgcn_exp2f((v - top) * scale);
+          nan |= v != v;
+        });
+      e = dpp_wave_fsum(e);
+      if (nan) nans = 1;
+      __syncthreads();
+      if (lane == 0) fsum[wave].y = e;
+      __syncthreads();
+      total = row16_sum((lane & 15) < nw ? fsum[min(lane & 15, nw - 1)].y : 0.0f);
+      base = (double)top;
     }
-  __syncthreads();
-  const int above = nabove;
-  for (int s = 0; s < nslots; ++s)
-    if (slot[s * nt + t] == tau) {
-      const int at = above + atomicAdd(&nat, 1);
-      if (at < mhits) hits[at] = (uint32_t)(s * nt + t);
+    if (t == nt - 1) {  // beside the others' search
+      float lse = (float)(base / (double)a.temperature + log((double)total));
+      if (rowmax == KEY_NEG_INF || top == INFINITY) lse = top;
+      if (slow && nans) lse = NAN;
+      a.lse[row] = lse;
     }
-  __syncthreads();
-  const int reach = above + nat;
+  }
   auto push = [&](uint32_t key, int token) {
     const int at = atomicAdd(&nlist, 1);
     if (at < cap) list[at] = ((uint64_t)key << 32) | (uint32_t)~token;
   };
-  auto collect = [&](int n, uint32_t over) {  // logits above `over`
+  auto collect = [&](int n, uint32_t over) {  // logits above `over` in the first n hits
     for (int h = t; h < n * each; h += nt) {
       const int id = (int)hits[h / each], s = id / nt, i = s * each + h % each;
       if (i < turns)
-        again(i, id - s * nt, [&](float v, int token) {
-          if (top_key(v) > over) push(top_key(v), token);
+        rerun(i, id - s * nt, [&](const Run<IN>& r, int j, int len) {
+          uint32_t key[E];
+          int mine = 0;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            key[e] = e < len ? top_key(r[e]) : 0;
+            mine += key[e] > over;
+          }
+          if (mine == 0) return;
+          int at = atomicAdd(&nlist, mine);
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (key[e] > over) {
+              if (at < cap) list[at] = ((uint64_t)key[e] << 32) | (uint32_t)~(j + e);
+              ++at;
+            }
         });
     }
     __syncthreads();
   };
-  int n = cap + 1;
-  if (reach <= mhits) {
+  // the slots that reach tau, those above it first, and their logits that do: how many, or more than cap
+  int above = 0;
+  auto gather = [&]() {
+    for (int s = 0; s < nslots; ++s)
+      if (slot[s * nt + t] > tau) {
+        const int at = atomicAdd(&nabove, 1);
+        if (at < mhits) hits[at] = (uint32_t)(s * nt + t);
+      }
+    __syncthreads();
+    above = nabove;
+    for (int s = 0; s < nslots; ++s)
+      if (slot[s * nt + t] == tau) {
+        const int at = above + atomicAdd(&nat, 1);
+        if (at < mhits) hits[at] = (uint32_t)(s * nt + t);
+      }
+    __syncthreads();
+    const int reach = above + nat;
+    if (reach > mhits) return cap + 1;
     collect(reach, tau - 1);  // no key is below that of -inf
-    n = nlist;
+    return (int)nlist;
+  };
+  int n = gather();
+  if (n > cap && c <= 64) {
+    // a better bound: k of the slots' maxima reach it too
+    const TopBins bin(tau, rowmax);
+    auto each_slot = [&](auto&& f) {
+      for (int s = 0; s < nslots; ++s) {
+        const uint32_t key = slot[s * nt + t];
+        if (key >= tau && key != 0xFFFFFFFFu) f(key);
+      }
+    };
+    __syncthreads();
+    if (t == 0) nlist = nabove = nat = 0, found = 0xFFFFFFFFu;
+    for (int i = t; i < TOP_BINS; i += nt) hist[i] = 0;
+    __syncthreads();
+    each_slot([&](uint32_t key) { atomicAdd(&hist[bin(key)], 1); });
+    __syncthreads();
+    bins_before(hist);
+    __syncthreads();
+    // bins before which fewer than k stand: of the last one that is not empty, all of it
+    each_slot([&](uint32_t key) {
+      if (hist[bin(key)] < k) atomicMin(&found, key);
+    });
+    __syncthreads();
+    if (found != 0xFFFFFFFFu) tau = found;
+    n = gather();
   }
   if (n > cap && above <= mhits) {
     __syncthreads();
@@ -319,8 +413,10 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
   }
   auto put = [&](uint64_t entry, int place) {
     const int token = (int)~(uint32_t)entry;
+    const uint32_t key = (uint32_t)(entry >> 32);
     a.index[(size_t)row * k + place] = token;
-    a.values[(size_t)row * k + place] = load1<IN>(x, token);
+    // a key is its logit, but for the sign of 0 and what a NaN holds
+    a.values[(size_t)row * k + place] = key == ord_key(0.0f) || key == 0xFFFFFFFFu ? load1<IN>(x, token) : key_val(key);
   };
   if (n * n <= TOP_RANK * nt) {
     // each entry's place, by as many lanes as there are for it
@@ -343,19 +439,7 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
     __syncthreads();
     for (int i = t; i < n; i += nt) atomicAdd(&hist[bin((uint32_t)(list[i] >> 32))], 1);
     __syncthreads();
-    if (t < 64) {
-      // how many stand before each bin: lane l has the bins below TOP_BINS - 8 l
-      constexpr int PER = TOP_BINS / 64;
-      int c[PER], sum = 0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) sum += c[i] = hist[TOP_BINS - 1 - t * PER - i];
-      int before = (int)wave_scan_u32((uint32_t)sum) - sum;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        hist[TOP_BINS - 1 - t * PER - i] = before;
-        before += c[i];
-      }
-    }
+    bins_before(hist);
     __syncthreads();
     for (int i = t; i < n; i += nt) order[atomicAdd(&hist[bin((uint32_t)(list[i] >> 32))], 1)] = (uint16_t)i;
     __syncthreads();
@@ -369,38 +453,11 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
       if (place < k) put(mine, place);
     }
   }
-  if (!a.lse) return;
-  const float top = key_val(rowmax);
-  double base = (double)ref / (double)scale;
-  const bool slow = !(total > 0.0f && total < INFINITY) && !(rowmax == KEY_NEG_INF && total == 0.0f);
-  if (slow) {
-    // NaN, infinities, or logits next to the type's largest or lowest value: relative to the maximum itself
-    float e = 0.0f;
-    int nan = 0;
-    for (int i = 0; i < turns; ++i)
-      again(i, t, [&](float v, int) {
-        e += __builtin_amdgcn_exp2f((v - top) * scale);
-        nan |= v != v;
-      });
-    e = dpp_wave_fsum(e);
-    if (nan) nans = 1;
-    __syncthreads();
-    if (lane == 0) fsum[wave].y = e;
-    __syncthreads();
-    total = row16_sum((lane & 15) < nw ? fsum[min(lane & 15, nw - 1)].y : 0.0f);
-    base = (double)top;
-  }
-  if (t == 0) {
-    float lse = (float)(base / (double)a.temperature + log((double)total));
-    if (rowmax == KEY_NEG_INF || top == INFINITY) lse = top;
-    if (slow && nans) lse = NAN;
-    a.lse[row] = lse;
-  }
 }
 
 template <int IN, bool TINY>
 hipError_t launch_top(const TopArgs& a, const TopShape& l, hipStream_t s) {
-  const size_t lds = l.lds(a.V);
+  const size_t lds = l.lds(a.V, a.k);
   if (lds > 32 * 1024) {
     const hipError_t e =
         hipFuncSetAttribute((const void*)top_kernel<IN, TINY>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -436,7 +493,7 @@ extern "C" int sv_top_logits(const void* logits, int32_t k, float temperature, f
   if (overlaps(out_values, no, logits, nin) || overlaps(out_index, no, logits, nin) || overlaps(out_lse, nl, logits, nin) ||
       overlaps(out_values, no, out_index, no) || overlaps(out_values, no, out_lse, nl) || overlaps(out_index, no, out_lse, nl))
     return SV_ERR_PARAM;
-  const TopArgs a{logits, out_values, out_index, out_lse, rows, V, k, l.turns, l.each, l.cap(V), l.hits(V), temperature};
+  const TopArgs a{logits, out_values, out_index, out_lse, rows, V, k, l.turns, l.each, l.cap(V, k), l.hits(V, k), temperature};
   const hipError_t err =
       dtype == SV_F32 ? launch_top<T_F32>(a, l, (hipStream_t)stream) : launch_top<T_BF16>(a, l, (hipStream_t)stream);
   return err == hipSuccess ? SV_OK : SV_ERR_HIP;
