@@ -78,10 +78,11 @@ struct TopShape {
     each = ((turns + 3) / 4 + TOP_SLOTS - 1) / TOP_SLOTS * 4;
   }
   int slots() const { return (turns + each - 1) / each; }
-  // entries that the list holds: a few times k, which is what reaches the bound as a rule, and no more than a row has
+  // entries that the list holds: several times k, which is more than what reaches the bound as a rule, and no more than a
+  // row has
   int cap(int V, int k) const {
     int n = 64;
-    while (n < V && n < TOP_CAP && (n < 512 || n < 4 * k)) n <<= 1;
+    while (n < V && n < TOP_CAP && (n < 512 || n < 16 * k)) n <<= 1;
     return n;
   }
   int hits(int V, int k) const { return std::max(std::min(TOP_HITS, slots() * nt), cap(V, k) / 2); }
@@ -94,6 +95,7 @@ struct TopBins {
   uint32_t tau;
   float lo, mul;
   int sh;
+  // (lower keys are in the first bin)
   __device__ __forceinline__ TopBins(uint32_t tau, uint32_t rowmax) : tau(tau) {
     lo = key_val(tau);
     const float width = key_val(rowmax) - lo;
@@ -104,8 +106,8 @@ struct TopBins {
   }
   __device__ __forceinline__ int operator()(uint32_t key) const {
     if (key == 0xFFFFFFFFu) return TOP_BINS - 1;  // NaN
-    if (mul > 0.0f) return (int)fminf((key_val(key) - lo) * mul, (float)(TOP_BINS - 1));
-    return (int)min((key - tau) >> sh, (uint32_t)TOP_BINS - 1);
+    if (mul > 0.0f) return (int)fminf(fmaxf((key_val(key) - lo) * mul, 0.0f), (float)(TOP_BINS - 1));
+    return key < tau ? 0 : (int)min((key - tau) >> sh, (uint32_t)TOP_BINS - 1);
   }
 };
 
@@ -211,6 +213,13 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
       if (lane == __ffsll((long long)same) - 1) v = 0;
     }
     cth = dpp_wave_umax(v);
+  } else if (c <= 64 && c > 64 - TOP_TAKE) {
+    uint32_t v = ~mk;  // from the other end
+    for (int i = 64; i > c; --i) {
+      const uint64_t same = __ballot(v == dpp_wave_umax(v));
+      if (lane == __ffsll((long long)same) - 1) v = 0;
+    }
+    cth = ~dpp_wave_umax(v);
   } else {
     cth = __shfl(wave_sort_desc(mk), min(c, 64) - 1);
   }
@@ -432,11 +441,21 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
     }
   } else {
     // by bins, the largest values first: an entry's place is where its bin begins, and the place within
-    const TopBins bin(tau, rowmax);
     uint16_t* order = reinterpret_cast<uint16_t*>(hits);  // [cap]
     __syncthreads();
     for (int i = t; i < TOP_BINS; i += nt) hist[i] = 0;
+    if (t == 0) found = rowmax;
     __syncthreads();
+    // from the smallest one above -inf
+    uint32_t least = 0xFFFFFFFFu;
+    for (int i = t; i < n; i += nt) {
+      const uint32_t key = (uint32_t)(list[i] >> 32);
+      if (key > KEY_NEG_INF) least = min(least, key);
+    }
+    least = ~dpp_wave_umax(~least);
+    if (lane == 0) atomicMin(&found, least);
+    __syncthreads();
+    const TopBins bin(found, rowmax);
     for (int i = t; i < n; i += nt) atomicAdd(&hist[bin((uint32_t)(list[i] >> 32))], 1);
     __syncthreads();
     bins_before(hist);
