@@ -68,6 +68,13 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
   __shared__ float fany[16];
   __shared__ double dsum[3][16];
   __shared__ int32_t repeated;
+  struct Row {
+    // mass: of the student's logits relative to top, inv its reciprocal; total: of the list, norm its reciprocal (1 with
+    // the teacher's log-sum-exp); dot: sum of p (t - s) / T; left: the teacher's rest; coef: of the gradient there
+    double mass, inv, top, total, norm, dot, left;
+    float coef;
+  };
+  __shared__ Row fin;
   constexpr int E = Run<IN>::E, IB = Run<IN>::B;
   const int t = threadIdx.x, nt = blockDim.x, nw = nt >> 6, lane = t & 63, wave = t >> 6;
   const int row = blockIdx.x, V = a.V, k = a.k;
@@ -138,21 +145,27 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
       acc.add<false>(r[i], scale, mx);
       __builtin_amdgcn_sched_barrier(0);  // one run at a time: more would not fit the registers
     }
-    constexpr int AHEAD = 4;
+    // the runs behind those in registers, four on their way at a time
     auto stream = [&](auto&& f) {
+      constexpr int AHEAD = 4;
+      Run<IN> o[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        o[u].load(x, j0 + (NH + u) * (nt * E), V);
+        __builtin_amdgcn_sched_barrier(0);  // in the order of the loop, whose waits count on it
+      }
       for (int i = NH; i < turns; i += AHEAD) {
-        Run<IN> o[AHEAD];
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) o[u].load(x, j0 + min(i + u, turns - 1) * (nt * E), V);
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
+        for (int u = 0; u < AHEAD; ++u) {
           if (i + u < turns) {
             const int n = i + u - NH;
             const uint32_t b = bytes[nt * MB + (E == 8 ? n : n / 2) * nt + t];
             take(o[u], i + u, E == 8 ? b : b >> (n % 2 * 4) & 15);
             f(o[u], i + u);
-            __builtin_amdgcn_sched_barrier(0);
           }
+          o[u].load(x, j0 + (i + u + AHEAD) * (nt * E), V);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     };
     if (MORE) stream([&](const Run<IN>& v, int) { acc.add<false>(v, scale, mx); });
@@ -227,22 +240,32 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
           for (int i = 0; i < 3; ++i) dsum[i][wave] = sum[i];
       }
       __syncthreads();
+      // what the row comes to: formed by one wave
+      if (wave == 0) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        sum[i] = dsum[i][0];
-        for (int o = 1; o < lw; ++o) sum[i] += dsum[i][o];
+        for (int i = 0; i < 3; ++i) {
+          sum[i] = dsum[i][0];
+          for (int o = 1; o < lw; ++o) sum[i] += dsum[i][o];
+        }
+        const double R0 = (double)rest;
+        Row f;
+        f.total = sum[1];
+        f.dot = sum[2];
+        f.norm = a.top_lse ? 1.0 : 1.0 / sum[1];
+        // relative to the larger of the two maxima; lane 0 for the rest, the others for the list
+        f.top = R0 == 0.0 ? s0 : sum[0] == 0.0 ? rm : fmax(rm, s0);
+        const double part = lane == 0 ? R0 : sum[0];
+        const double AB = part == 0.0 ? 0.0 : part * exp(((lane == 0 ? rm : s0) - f.top) * invT);
+        const double A = __shfl(AB, 0);
+        f.mass = A + __shfl(AB, 1);
+        f.inv = f.mass == 0.0 ? 0.0 : 1.0 / f.mass;
+        f.left = a.top_lse && R0 != 0.0 ? fmax(0.0, 1.0 - sum[1]) : 0.0;
+        f.coef = R0 == 0.0 ? 0.0f : (float)((double)w * invT * (A * f.inv - f.left) / R0);
+        if (lane == 0) fin = f;
       }
-      const double R0 = (double)rest, total = sum[1], norm = a.top_lse ? 1.0 : 1.0 / total;
-      // relative to the larger of the two maxima; lane 0 for the rest, the others for the list
-      const double top = R0 == 0.0 ? s0 : sum[0] == 0.0 ? rm : fmax(rm, s0);
-      const double part = lane == 0 ? R0 : sum[0];
-      const double AB = part == 0.0 ? 0.0 : part * exp(((lane == 0 ? rm : s0) - top) * invT);
-      const double A = __shfl(AB, 0), B = __shfl(AB, 1);
-      const double inv = A + B == 0.0 ? 0.0 : 1.0 / (A + B);
-      const double left = a.top_lse && R0 != 0.0 ? fmax(0.0, 1.0 - total) : 0.0;
-      const double gs = (double)w * invT;
+      __syncthreads();
       if (grad) {
-        const float coef = R0 == 0.0 ? 0.0f : (float)(gs * (A * inv - left) / R0);
+        const float coef = fin.coef;
         if (slow)
           for (int j = t; j < V; j += nt)
             store1<IN>(grad, j, __builtin_amdgcn_exp2f((load1<IN>(x, j) - far) * scale) * coef);
@@ -255,7 +278,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) u[e] = IN == T_F32 ? __float_as_uint(o[e]) : pack_bf16(o[(2 * e) % E], o[(2 * e + 1) % E]);
           if ((i + 1) * nt * E <= V || j + E <= V) {
-            __builtin_memcpy(grad + (uint32_t)(j * IB), u, 16);
+            store_through(grad + (uint32_t)(j * IB), u);
           } else {
 #pragma unroll
             for (int e = 0; e < E; ++e)
@@ -282,20 +305,20 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
             for (int o = 0; o < k; ++o)
               if (token[o] >= 0 && (token[o] & 0x3FFFFFFF) == v) p += prob[o];
           }
-          const double q = exp(((double)student[j] - top) * invT) * inv;
-          store1<IN>(grad, v, (float)(gs * ((student[j] == -INFINITY ? 0.0 : q) - p * norm)));
+          const double q = exp(((double)student[j] - fin.top) * invT) * fin.inv;
+          store1<IN>(grad, v, (float)((double)w * invT * ((student[j] == -INFINITY ? 0.0 : q) - p * fin.norm)));
         }
       }
       if (a.loss && wave == nw - 1) {
         // four logarithms at once, a lane each
-        const double of = lane == 0 ? A + B : lane == 1 ? total : lane == 2 ? left : R0;
+        const double of = lane == 0 ? fin.mass : lane == 1 ? fin.total : lane == 2 ? fin.left : (double)rest;
         const double lg = log(of);
-        const double lAB = __shfl(lg, 0), lP = __shfl(lg, 1), lr = __shfl(lg, 2), lR = __shfl(lg, 3);
+        const double lm = __shfl(lg, 0), lp = __shfl(lg, 1), lr = __shfl(lg, 2), lR = __shfl(lg, 3);
         // log p_j - log q_j = (t_j - s_j) / T - log of the teacher's sum + log of the student's
-        const double ls = top * invT + lAB, lt = a.top_lse ? (double)tl : (double)tm * invT + lP;
-        double loss = sum[2] * norm;
-        if (total != 0.0 && loss != INFINITY) loss += total * norm * (ls - lt);
-        if (left > 0.0) loss += left * (lr - ((rm - top) * invT + lR - lAB));
+        const double ls = fin.top * invT + lm, lt = a.top_lse ? (double)tl : (double)tm * invT + lp;
+        double loss = fin.dot * fin.norm;
+        if (fin.total != 0.0 && loss != INFINITY) loss += fin.total * fin.norm * (ls - lt);
+        if (fin.left > 0.0) loss += fin.left * (lr - ((rm - fin.top) * invT + lR - lm));
         if (lane == 0) a.loss[row] = (float)((double)w * loss);
       }
     }
@@ -306,7 +329,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
       for (int j = t * E; j < V; j += nt * E) {
         if (j + E <= V) {
           const uint32_t u[4] = {0, 0, 0, 0};
-          __builtin_memcpy(grad + (size_t)j * IB, u, 16);
+          store_through(grad + (size_t)j * IB, u);
         } else {
           for (int e = j; e < V; ++e) store1<IN>(grad, e, 0.0f);
         }

@@ -11,6 +11,14 @@ namespace sv {
 
 constexpr float LOG2E = 1.4426950408889634f;
 
+// 16 bytes at any alignment of their elements, past the caches: nobody reads them
+// before the row's end, and what is read a second time keeps its place there.
+__device__ __forceinline__ void store_through(char* p, const uint32_t (&v)[4]) {
+  typedef uint32_t words __attribute__((ext_vector_type(4), aligned(2)));
+  const words w = {v[0], v[1], v[2], v[3]};
+  __builtin_nontemporal_store(w, reinterpret_cast<words*>(p));
+}
+
 // E logits as they lie in memory.
 template <int IN>
 struct Run {
