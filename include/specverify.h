@@ -602,8 +602,8 @@ int sv_layer_norm(const void* x, const void* residual, const void* weight, const
  * bits.  grad_h may be grad, h or grad_residual itself (in place); any other
  * overlap of what is written with another argument is SV_ERR_PARAM.  A row
  * whose statistics are not finite gives NaN in its grad_h and in grad_weight.
- * rows == 0 writes zeros to grad_weight and grad_bias.  1 <= d <= SV_MAX_NORM_D
- * (else SV_ERR_SHAPE).  A workspace that is too small is SV_ERR_WORKSPACE.
+ * rows == 0 writes zeros to grad_weight and grad_bias.  1 <= d <= SV_MAX_NORM_D,
+ * at most 2^30 rows (else SV_ERR_SHAPE).  A workspace that is too small is SV_ERR_WORKSPACE.
  * Nothing is allocated; calls may be captured.
  *
  * sv_norm_backward_workspace returns bytes, or SV_ERR_SHAPE.

@@ -8,6 +8,7 @@ implementation: if the library is missing it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch  # loaded first so the library binds to the HIP runtime torch uses
@@ -749,6 +750,11 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     return out, out_scale, out_residual
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_backward_bytes(rows: int, d: int) -> int:
+    return max(lib().sv_norm_backward_workspace(rows, d), 0)
+
+
 def _norm_backward(center: bool, grad, h, weight, grad_residual, eps, with_weight, with_bias, out, out_weight, out_bias,
                    stream):
     code = _code(h.dtype, "h", _FLOATS)
@@ -779,7 +785,7 @@ def _norm_backward(center: bool, grad, h, weight, grad_residual, eps, with_weigh
         out_bias = _new(stream, dev, h.new_empty, (d,), dtype=torch.float32)
         obp = out_bias.data_ptr()
     L = lib()
-    nbytes = max(L.sv_norm_backward_workspace(rows, d), 0) * ((1 if with_weight else 0) + (1 if with_bias else 0)) // 2
+    nbytes = _norm_backward_bytes(rows, d) * (int(bool(with_weight)) + int(bool(with_bias))) // 2
     ws = None
     if nbytes:
         # on the call's own stream: handed out again only behind the call

@@ -236,6 +236,10 @@ template <int IN>
 struct Raw8 {
   uint4 v[IN == T_F32 ? 2 : 1];
   __device__ __forceinline__ void load(const char* p) { __builtin_memcpy(v, p, sizeof(v)); }
+  __device__ __forceinline__ void arrived() {
+#pragma unroll
+    for (uint4& q : v) asm volatile("" : "+v"(q.x), "+v"(q.y), "+v"(q.z), "+v"(q.w));
+  }
   __device__ __forceinline__ void ones() {
     const uint32_t u = IN == T_F32 ? 0x3F800000u : 0x3F803F80u;
     v[0] = make_uint4(u, u, u, u);
@@ -349,7 +353,10 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(BackArgs a) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       dyc[i] = dy[i];
-      if (RES) drc[i] = dr[i];
+      if (RES) {
+        drc[i] = dr[i];
+        drc[i].arrived();  // before the barrier behind which a neighbour may write over it (in place)
+      }
     }
     if (AHEAD) fetch(row + step);
     group_sum(mom, part + turn * 80 + 16, nw);
@@ -523,6 +530,8 @@ __global__ void __launch_bounds__(1024) norm_backward_sum_kernel(const float* wp
   out[col] = v;
 }
 
+constexpr int BACK_ROWS = 1 << 30;  // a workgroup's next row stays within 32 bits
+
 // A row's threads and runs, rows a workgroup, and workgroups: what the workspace
 // holds a part for.
 struct BackPlan {
@@ -560,7 +569,7 @@ hipError_t launch_back(const BackArgs& a, const BackPlan& l, hipStream_t s) {
 int norm_backward(bool center, const void* grad, const void* h, const void* weight, const void* grad_residual, float eps,
                   void* grad_h, float* grad_weight, float* grad_bias, void* workspace, int64_t workspace_bytes,
                   int32_t rows, int32_t d, int32_t dtype, hipStream_t s) {
-  if (rows < 0 || d < 1 || d > SV_MAX_NORM_D) return SV_ERR_SHAPE;
+  if (rows < 0 || rows > BACK_ROWS || d < 1 || d > SV_MAX_NORM_D) return SV_ERR_SHAPE;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
   if (!(eps > 0.0f) || !std::isfinite(eps)) return SV_ERR_PARAM;
   const BackPlan l(rows, d);
@@ -669,7 +678,7 @@ extern "C" int sv_layer_norm(const void* x, const void* residual, const void* we
 }
 
 extern "C" int64_t sv_norm_backward_workspace(int32_t rows, int32_t d) {
-  if (rows < 0 || d < 1 || d > SV_MAX_NORM_D) return SV_ERR_SHAPE;
+  if (rows < 0 || rows > BACK_ROWS || d < 1 || d > SV_MAX_NORM_D) return SV_ERR_SHAPE;
   const BackPlan l(rows, d);
   return l.groups > 1 ? (int64_t)l.groups * l.stride * 8 : 0;
 }

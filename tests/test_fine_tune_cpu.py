@@ -54,6 +54,7 @@ def back(center=True, dy=P(0), h=P(1), w=P(2), dres=P(3), eps=1e-6, dh=P(4), dw=
 @pytest.mark.parametrize("center", [True, False])
 @pytest.mark.parametrize("kw,code", [
     (dict(rows=-1), L.SV_ERR_SHAPE), (dict(d=0), L.SV_ERR_SHAPE), (dict(d=65537), L.SV_ERR_SHAPE),
+    (dict(rows=2 ** 30 + 1, d=1), L.SV_ERR_SHAPE),
     (dict(dt=L.SV_E4M3), L.SV_ERR_DTYPE), (dict(eps=0.0), L.SV_ERR_PARAM), (dict(eps=math.nan), L.SV_ERR_PARAM),
     (dict(dy=None), L.SV_ERR_NULL), (dict(h=None), L.SV_ERR_NULL), (dict(dh=None), L.SV_ERR_NULL),
     (dict(ws=None), L.SV_ERR_NULL), (dict(nbytes=16), L.SV_ERR_WORKSPACE), (dict(nbytes=-1), L.SV_ERR_WORKSPACE),
@@ -74,8 +75,8 @@ def test_the_bias_gradient_has_its_own_memory():
 def test_workspace_sizes():
     f = L.lib().sv_norm_backward_workspace
     assert f(0, 64) == 0 and f(1, 65536) == 0
-    assert f(-1, 64) == L.SV_ERR_SHAPE and f(4, 0) == L.SV_ERR_SHAPE and f(4, 65537) == L.SV_ERR_SHAPE
-    for rows, d in ((2, 1), (448, 4096), (2 ** 31 - 1, 65536)):
+    assert f(2 ** 30 + 1, 1) == L.SV_ERR_SHAPE and f(-1, 64) == L.SV_ERR_SHAPE and f(4, 0) == L.SV_ERR_SHAPE and f(4, 65537) == L.SV_ERR_SHAPE
+    for rows, d in ((2, 1), (448, 4096), (2 ** 30, 65536)):
         assert 0 <= f(rows, d) <= 2048 * 8 * d and f(rows, d) % 16 == 0
 
 
