@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
       take(r[i], i, E == 8 ? mk[i / 4] >> (i % 4 * 8) & 255 : mk[i / 8] >> (i % 8 * 4) & 15);
       r[i].forget();
       acc.add<false>(r[i], scale, mx);
+      acc.now(mx);
       __builtin_amdgcn_sched_barrier(0);  // one run at a time: more would not fit the registers
     }
     // the runs behind those in registers, four on their way at a time

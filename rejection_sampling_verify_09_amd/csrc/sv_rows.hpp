@@ -66,7 +66,7 @@ struct Run {
       }
   }
   // as if loaded anew: what was formed from it before is formed again, not kept
-  __device__ __forceinline__ void forget() { asm("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])); }
+  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])); }
   __device__ __forceinline__ float operator[](int k) const {
     return IN == T_F32 ? __uint_as_float(v[k]) : k & 1 ? bf16_hi(v[k / 2]) : bf16_lo(v[k / 2]);
   }
@@ -86,6 +86,8 @@ __device__ __forceinline__ int fresh(int v) {
 // NaN, and the row takes the slow way below.
 struct RunSum {
   float ref = -FLT_MAX, s = 0.0f;
+  // formed by here: the compiler would put all of a row's sums behind the last of its loads
+  __device__ __forceinline__ void now(float& mx) { asm volatile("" : "+v"(ref), "+v"(s), "+v"(mx)); }
   // mx: the running maximum (NaN apart).  BRANCH: pass over the new reference where no lane of the wave has one
   // (few times a row one has; it costs registers)
   template <bool BRANCH, int IN>
