@@ -136,14 +136,19 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
     uint32_t mk[(MB + 3) / 4];
     __builtin_memcpy(mk, __builtin_assume_aligned(bytes + t * MB, MB & -MB), MB);
     RunSum acc;
-    float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
       j0 = fresh(j0);
       take(r[i], i, E == 8 ? mk[i / 4] >> (i % 4 * 8) & 255 : mk[i / 8] >> (i % 8 * 4) & 15);
       r[i].forget();
-      acc.add<false>(r[i], scale, mx);
-      acc.now(mx);
+      if (i == 0) {
+        float first = r[0][0];
+#pragma unroll
+        for (int e = 1; e < E; ++e) first = fmaxf(first, r[0][e]);
+        acc.ref = fmaxf(first * scale, -FLT_MAX);
+      }
+      acc.s += acc.sum(r[i], scale);
+      acc.now();
       __builtin_amdgcn_sched_barrier(0);  // one run at a time: more would not fit the registers
     }
     // the runs behind those in registers, four on their way at a time
@@ -169,7 +174,24 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         }
       }
     };
-    if (MORE) stream([&](const Run<IN>& v, int) { acc.add<false>(v, scale, mx); });
+    if (MORE) stream([&](const Run<IN>& v, int) { acc.s += acc.sum(v, scale); });
+    if (__any(!(acc.s < 0x1p40f))) {
+      // a thread whose first run lies far below its others (masked, for one): once more, with a reference that follows
+      acc = RunSum();
+      float mx = -INFINITY;
+      for (int i = 0; i < turns; ++i) {
+        Run<IN> o;
+        if (TINY) {
+          o.tiny(x, t == 0 ? V : 0);
+        } else {
+          o.load(x, j0 + i * (nt * E), V);
+        }
+        const int n = i < NH ? i : i - NH, b = E == 8 ? n : n / 2;
+        const uint32_t m = bytes[i < NH ? t * MB + b : nt * MB + b * nt + t];
+        take(o, i, E == 8 ? m : m >> (n % 2 * 4) & 15);
+        acc.add(o, scale, mx);
+      }
+    }
     // the list's maxima
     float tm = -INFINITY, sm = -INFINITY;
     auto entry = [&](int j, float y, float s) {
@@ -184,21 +206,30 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
     const float ws = dpp_wave_fsum(acc.s * __builtin_amdgcn_exp2f(acc.ref - wr));
     tm = dpp_wave_fmax(tm), sm = dpp_wave_fmax(sm);
     if (lane == 0) fmx[wave] = make_float4(wr, ws, tm, sm);
-    if (lane == 0) fany[wave] = __any(mx > -INFINITY) ? 1.0f : 0.0f;
     __syncthreads();
     const int from = min(lane & 15, nw - 1);
     const float4 wv = fmx[from];
     const float ref = row16_max(wv.x);
     float rest = row16_sum((lane & 15) < nw ? wv.y * __builtin_amdgcn_exp2f(wv.x - ref) : 0.0f);
     tm = row16_max(wv.z), sm = row16_max(wv.w);
-    const bool left_over = row16_max(fany[from]) > 0.0f;  // not all of the rest is -inf
     none = !a.top_lse && tm == -INFINITY;
     if (!none) {
       const double invT = 1.0 / (double)a.temperature;
       const double s0 = sm == -INFINITY ? 0.0 : (double)sm;
       // the logit that the rest's sum is relative to: of ref as the float32 factor takes it there
       double rm = (double)ref / (double)scale;
-      const bool slow = left_over && !(rest > 0.0f && rest < INFINITY);
+      bool slow = !(rest > 0.0f && rest < INFINITY);
+      if (rest == 0.0f) {
+        // nothing, or all of the rest is -inf
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) any |= r[i].any();
+        if (MORE) stream([&](const Run<IN>& v, int) { any |= v.any(); });
+        if (lane == 0) fany[wave] = 0.0f;
+        if (__any(any) && lane == 0) fany[wave] = 1.0f;
+        __syncthreads();
+        slow = row16_max(fany[from]) > 0.0f;
+      }
       float far = 0.0f;
       if (slow) {
         // relative to the maximum itself, read again, an element at a time

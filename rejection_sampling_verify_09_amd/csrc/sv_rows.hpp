@@ -54,6 +54,8 @@ struct Run {
     v[0] = (uint32_t)lo ^ NINF, v[1] = (uint32_t)(lo >> 32) ^ NINF;
     v[2] = (uint32_t)hi ^ NINF, v[3] = (uint32_t)(hi >> 32) ^ NINF;
   }
+  // something above -inf (or NaN) among the elements
+  __device__ __forceinline__ bool any() const { return ((v[0] ^ NINF) | (v[1] ^ NINF) | (v[2] ^ NINF) | (v[3] ^ NINF)) != 0; }
   // element k to -inf for each bit k of mask
   __device__ __forceinline__ void drop(uint32_t mask) {
 #pragma unroll
@@ -87,27 +89,31 @@ __device__ __forceinline__ int fresh(int v) {
 struct RunSum {
   float ref = -FLT_MAX, s = 0.0f;
   // formed by here: the compiler would put all of a row's sums behind the last of its loads
-  __device__ __forceinline__ void now(float& mx) { asm volatile("" : "+v"(ref), "+v"(s), "+v"(mx)); }
-  // mx: the running maximum (NaN apart).  BRANCH: pass over the new reference where no lane of the wave has one
-  // (few times a row one has; it costs registers)
-  template <bool BRANCH, int IN>
-  __device__ __forceinline__ void add(const Run<IN>& r, float scale, float& mx) {
+  __device__ __forceinline__ void now() { asm volatile("" : "+v"(ref), "+v"(s)); }
+  template <int IN>
+  __device__ __forceinline__ float sum(const Run<IN>& r, float scale) const {
     constexpr int E = Run<IN>::E;
-#pragma unroll
-    for (int k = 0; k < E; ++k) mx = fmaxf(mx, r[k]);
-    const float y = mx * scale;
-    if (!BRANCH || __any(y > ref + 8.0f)) {
-      const float n = y > ref + 8.0f ? y : ref;
-      s *= __builtin_amdgcn_exp2f(ref - n);
-      ref = n;
-    }
     float p[2];
 #pragma unroll
     for (int k = 0; k < E; ++k) {
       const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(r[k], scale, -ref));
       p[k & 1] = k < 2 ? e : p[k & 1] + e;
     }
-    s += p[0] + p[1];
+    return p[0] + p[1];
+  }
+  // mx: the running maximum (NaN apart)
+  template <int IN>
+  __device__ __forceinline__ void add(const Run<IN>& r, float scale, float& mx) {
+    constexpr int E = Run<IN>::E;
+#pragma unroll
+    for (int k = 0; k < E; ++k) mx = fmaxf(mx, r[k]);
+    const float y = mx * scale;
+    if (__any(y > ref + 8.0f)) {  // few times a row
+      const float n = y > ref + 8.0f ? y : ref;
+      s *= __builtin_amdgcn_exp2f(ref - n);
+      ref = n;
+    }
+    s += sum(r, scale);
   }
 };
 

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
     for (int u = 0; u < 4; ++u) {
       if (i + u < turns) {
         if (!TINY && (i + u + 1) * nt * E > V) r[u].cut((t + (i + u) * nt) * E, V);
-        sum.add<true>(r[u], scale, sm);
+        sum.add(r[u], scale, sm);
       }
       fetch(r[u], i + 4 + u);
     }
