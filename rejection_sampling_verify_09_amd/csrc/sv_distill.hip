@@ -13,12 +13,29 @@
 // One workgroup takes a row and keeps it in registers, as it lies in memory,
 // between the sums and the gradient: every logit is read once and written once
 // (rows above 256 KiB: what lies behind that is read twice).  The listed tokens
-// are marked in a bitmap in LDS and set to -inf in the registers, so that R is a
-// sum of its own and never a difference, and q_v / R comes from the rest's own
-// maximum and sum, which no list can underflow.  The sums are formed as the
-// loads arrive, with a running maximum a thread.  What is done once an entry is
-// done in 64 bits: there are few, and the loss is a difference of numbers close
-// to each other.
+// are marked in LDS and set to -inf in the registers, so that R is a sum of its
+// own and never a difference, and q_v / R is formed from the rest alone, which
+// no list can underflow.  The sums are formed as the loads arrive, relative to
+// the largest logit of a thread's first run; what lies far above that (masked
+// first runs, small temperatures) has the thread's wave form its sums once more.
+// What is done once an entry is done in 64 bits: there are few, and the loss is
+// a difference of numbers close to each other.
+//
+// 448 x 128256 bfloat16 with an eighth of the rows left out and lists of 64: 53 us
+// (4.1 TB/s of what must be read and written; a large copy reaches 5.0), of
+// which the vector units are busy for half: two exponentials a logit at a
+// quarter of the rate, and the 256 compute units hold 256 rows at a time, in
+// step, so that loads, sums, gradient and stores take turns.  2304 x 152064
+// float32: 607 us (4.6 TB/s).  A single row takes 19 us, 12 of them instructions.
+// What made the difference (448 x 128256): registers instead of three reads
+// (185 -> 82 us); loads outside branches, at whose ends the compiler waits for
+// all of them, and columns formed anew in each pass instead of being kept
+// (82 -> 73); marks that a thread reads in one load (73 -> 71); the gradient
+// stored past the caches (67 -> 60; 2304 x 152064 691 -> 614); one wave for what
+// is done once a row (60 -> 57.5); a reference from the first run instead of a
+// running maximum (57 -> 55).  Not kept: two rows a compute unit whose second
+// pass reads them again (79 against 67, 2304 x 152064 925 against 692); a check
+// of each run's sum instead of its maximum (61 against 57: a wait a run).
 #include "sv_rows.hpp"
 #include "specverify.h"
 
@@ -369,7 +386,11 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
   }
 }
 
-// Runs a thread in registers, and whole waves of threads to go with them.
+// Runs a thread in registers, and whole waves of threads to go with them.  Few
+// runs and many threads make a row quick, many runs and few threads let a
+// compute unit hold more rows (2, 4, 8 and 16 runs, bfloat16, lists of 64: 16384 x
+// 1000 35, 41, 53, 79 us; 8192 x 4096 47, 39, 36, 50; 4096 x 11000 76, 63, 45, 53;
+// 2048 x 32000 from 4 on 83, 59, 59, float32 104 with 16, 118 with 8).
 struct DistillLaunch {
   int nt, nh;
   bool more;

@@ -11,6 +11,16 @@
 // ([mean g]: layer norm only).  The row's statistics are formed again from h:
 // the row has to be read in any case, and nothing else is kept from the
 // forward pass.
+//
+// Bound by memory from a few MB on: 16384 x 8192 bfloat16 take 190 to 200 us
+// forward with a residual (5.4 to 5.6 TB/s; a large copy reaches 5.0) and 195 to
+// 200 us backward with a residual's gradient (5.4 TB/s); below that by the
+// launches and by a row's two reductions one after the other: one row of 4096
+// takes 2.5 us forward, 448 rows backward 9.4 + 3.8 us.  What holds the backward
+// pass back elsewhere is instructions: at first 56 a column (separate products
+// and sums, divisions, masks for columns past the row), 74% of the cycles, now
+// with fused multiply-adds and the masks in the one wave that needs them about
+// 30, and the same 16384 x 8192 went from 247 to 200 us.
 #include "sv_ops.hpp"
 #include "specverify.h"
 
@@ -156,14 +166,17 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(LayerArgs a) {
   }
 }
 
-// As many threads a row as it has runs of 8, up to 1024; the rows of one wave
-// go four to a workgroup.
+// A thread a run up to 4096 columns, two runs up to 16384: the waves share the
+// two reductions' instructions out over more columns (16384 x 8192 bfloat16 with
+// one, two and four runs a thread 204, 196 and 207 us, to e4m3 245, 198 and 196;
+// one row of 8192 4.2, 4.6 and 5.7; x 4096 one and two 99 and 99).  The rows of
+// one wave go four to a workgroup.
 struct LayerLaunch {
   int nt, ny, vpt;  // threads a row, rows a workgroup, runs a thread
   int64_t wgs;
   LayerLaunch(int64_t rows, int d) {
-    const int nv = (d + 7) / 8;
-    nt = std::min(1024, (nv + 63) / 64 * 64);
+    const int nv = (d + 7) / 8, runs = nv > 512 ? 2 : 1;
+    nt = std::min(1024, ((nv + runs - 1) / runs + 63) / 64 * 64);
     ny = nt == 64 ? 4 : 1;
     vpt = (nv + nt - 1) / nt;
     wgs = (rows + ny - 1) / ny;
@@ -424,9 +437,10 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(BackArgs a) {
   }
 }
 
-// Rows of other widths (up to 7, or above 16384 columns): a workgroup takes a row at a
-// time, reads it again for each step, and keeps the sums for the weights in its
-// part of the workspace.
+// Rows of other widths (up to 7, or above 16384 columns, whose sums the registers
+// do not hold): a workgroup takes a row at a time, reads it again for each step,
+// and keeps the sums for the weights in its part of the workspace (1024 x 40000
+// bfloat16 218 us, a third of the rate of the other kernel).
 template <int IN, bool CENTER>
 __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(BackArgs a) {
   __shared__ __attribute__((aligned(16))) float part[2][80];
@@ -533,7 +547,12 @@ __global__ void __launch_bounds__(1024) norm_backward_sum_kernel(const float* wp
 constexpr int BACK_ROWS = 1 << 30;  // a workgroup's next row stays within 32 bits
 
 // A row's threads and runs, rows a workgroup, and workgroups: what the workspace
-// holds a part for.
+// holds a part for.  One compute unit a workgroup, with equal turns (16384 x 8192
+// bfloat16 with 128, 224, 256, 384 and 512 workgroups 430, 215, 202, over 300 and
+// 213 us; 448 x 4096, where the parts count, 13.1 with 112, 13.4 with 224, 16.3
+// with 448), of at least 512 threads (16384 x 1024 with 256, 512 and 1024 threads
+// 45, 34 and 35 us).  One workgroup without parts to join up to two turns (2 rows
+// of 4096 5.7 us against 6.7, 4 rows 8.3 against 6.7).
 struct BackPlan {
   int nt, ny, vpt, groups, stride;
   bool wide;

@@ -81,14 +81,16 @@ __device__ __forceinline__ int fresh(int v) {
   return v;
 }
 
-// A sum of 2^(scale x - ref).  ref is not the maximum but a value of the scale
-// that lies 8 below it at most: it follows the maximum in steps, so that few
-// runs form the sum so far again.  Where scale x is not finite in float32
-// (logits next to the type's largest or lowest value), the sum comes out as 0 or
-// NaN, and the row takes the slow way below.
+// A sum of 2^(scale x - ref): one fused multiply-add and one exponential an
+// element.  ref is not the maximum but a value that lies some powers of two below
+// it (add: 8 at most, following the maximum in steps), which costs a float32 sum
+// nothing.  Where scale x is not finite in float32 (logits next to the type's
+// largest or lowest value), the sum comes out as 0, infinite or NaN, which its
+// user has to look for.
 struct RunSum {
   float ref = -FLT_MAX, s = 0.0f;
-  // formed by here: the compiler would put all of a row's sums behind the last of its loads
+  // formed by here: the compiler would put all of a row's sums behind the last of its loads (448 x 128256 bfloat16
+  // without a gradient 42.9 us, 42.5 so)
   __device__ __forceinline__ void now() { asm volatile("" : "+v"(ref), "+v"(s)); }
   template <int IN>
   __device__ __forceinline__ float sum(const Run<IN>& r, float scale) const {

@@ -16,6 +16,18 @@
 // above it and the first equal ones are enough, if these lie among the row's
 // first tokens (masked rows); otherwise (rows in order of their tokens) the k-th
 // largest value itself is found by digits, reading the row for each.
+//
+// 2304 x 152064 float32 with k = 256 take 279 us (5.0 TB/s, a large copy's rate);
+// 448 x 128256 bfloat16 with k = 64 31 us (3.7 TB/s), where the vector units are
+// busy for 56% of the cycles (the exponentials above all) and the rest is the
+// steps after the sums, one after another; one row 15 us, of which 7 are
+// instructions.  What made the difference (448 x 128256 with k = 64): slot maxima
+// and reading a few slots again instead of the row (123 -> 38 us); the wave's
+// maxima taken out one by one instead of sorted, and bins in steps of the value
+// instead of comparing all with all or a sort (36 -> 33; with k = 256 55 -> 38,
+// and 70 before the sort); with k = 1000 a second bound instead of digits (215 ->
+// 60).  Rows held in registers were not quicker: the lists' code on eight runs
+// spills (2048 x 32000 198 us against 42).
 #include "sv_rows.hpp"
 #include "specverify.h"
 
@@ -32,8 +44,12 @@ constexpr int TOP_HITS = 2048;  // slots read again, at most
 constexpr int TOP_SLOTS = 16;   // slots a thread, at most
 constexpr int TOP_TURNS = 512;  // runs a thread, at most: SV_MAX_V / 4 runs on 1024 threads
 constexpr int TOP_BINS = 512;
+// Up to here the wave's maxima are taken out one by one (at most 14 instructions each), beyond it they are sorted (about
+// 250): with 0, 8 and 32 448 x 128256 with k = 64 (4 a wave) takes 33.9, 32.9 and 33.3 us, with k = 256 (16) 38.9, 38.5, 39.9.
 constexpr int TOP_TAKE = 8;
-constexpr int TOP_RANK = 16;  // lists up to sqrt(16 threads) entries are ranked one against all
+// Lists up to sqrt(16 threads) entries are ranked one against all, longer ones by bins: 4, 16 and 64 take 32.9, 32.9 and
+// 34.1 us at 448 x 128256 with k = 64, 59, 60 and 66 at 8192 x 4096.
+constexpr int TOP_RANK = 16;
 
 struct TopArgs {
   const void* x;
