@@ -356,8 +356,15 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
       if (hist[bin(key)] < k) atomicMin(&found, key);
     });
     __syncthreads();
+    const uint32_t first = tau;
     if (found != 0xFFFFFFFFu) tau = found;
     n = gather();
+    if (n < k) {
+      // slots of threads with NaN or infinities were left out, and without them fewer than k reach this one
+      tau = first;
+      n = cap + 1;
+      above = mhits + 1;
+    }
   }
   if (n > cap && above <= mhits) {
     __syncthreads();

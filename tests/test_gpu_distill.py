@@ -2,7 +2,10 @@
 
 u = 2^-24.  The list's part is float64 on the device.  The sum S over the
 tokens that are not listed is float32: off by e_S = (4 E + D + 4) u of itself, as
-for top_logits (E: the mean of |x - m| / T over them).  So R is off by R e_S, a
+for top_logits (E: the mean of |x - m| / T over them), and, its exponentials
+being relative to a reference that may lie 40 powers of two below the maximum,
+by another 40 ln 2 (1 + 1.5) u < 70 u: the fused product's rounding, and the
+rounding of log2(e) / T over that distance.  So R is off by R e_S, a
 listed token's q by q e_S, and an unlisted one's share q / R by e_S, its own
 exponential (4 u |x - m| / T + 2 u) and the product's roundings (3 u).  That gives
 for the gradient (times w / T) share (R e_S + |R - r| (e_S + 4 u |x - m| / T + 5 u))
@@ -50,7 +53,7 @@ def check(x, index, values, lse=None, T=1.0, weight=None, rows=None):
             assert li[r] == 0 and not gr[r].any(), r
             continue
         w = abs(ws[r])
-        eS = sum_bound(xs[r][~d["listed"]], T, V, dtype) if d["rest"] > -np.inf else 0.0
+        eS = sum_bound(xs[r][~d["listed"]], T, V, dtype) + 70 * U if d["rest"] > -np.inf else 0.0
         if math.isinf(want):
             assert li[r] == np.sign(ws[r]) * np.inf, (r, li[r])
         else:

@@ -1,12 +1,16 @@
 """GPU parity of top_logits with the float64 oracle: values and tokens equal,
 the log-sum-exp within the bound of its float32 sum.
 
-u = 2^-24.  An exponential's argument has three roundings (the difference, the
-factor, the product): 4 u |x - m| / T of its value, and 2 u from exp2 itself.
-The sum of a thread's V / threads terms, of a wave and of a workgroup is at most
-D = V / threads + 8 + 22 deep, so the sum is off by (4 E + D + 4) u, E being the
-mean of |x - m| / T under the distribution; log turns that into an absolute
-error, and the result is rounded once."""
+u = 2^-24.  An exponential's argument is rounded once (a fused product and
+sum) and carries the rounding of log2(e) / T over its distance from the
+reference, which lies 8 powers of two below the maximum at most: 2.5 u (|x - m| /
+T + 8 ln 2) of its value, within 4 u |x - m| / T + 14 u, and 2 u from exp2 itself.
+The sum of a thread's V / threads terms, of a wave and of a workgroup is less
+than D = V / threads + 8 + 22 deep (a thread's terms are summed in runs of 8,
+two at a time, so that its depth is V / (8 threads) + 5: the 14 u are within D), so
+the sum is off by (4 E + D + 4) u, E being the mean of |x - m| / T under the
+distribution; log turns that into an absolute error, and the result is rounded
+once."""
 import math
 
 import numpy as np
@@ -117,6 +121,30 @@ def test_nan(dtype):
     x[2] = nan
     x[3, 11] = -torch.tensor(nan)
     check(x.to(_t(dtype)), 40)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,k", [(5000, 300), (128256, 1000), (200000, 1024)])
+def test_many_nan_and_infinities_and_long_lists(V, k, dtype):
+    """More reach the bound than the list holds, and threads with NaN or
+    infinities, few to all of them, have no maximum to go by."""
+    import torch
+
+    log(f"[top] many NaN V={V} k={k} {dtype}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    nan, inf = float("nan"), float("inf")
+    x = torch.randn((8, V), device="cuda", generator=g)
+    at = [torch.randperm(V, device="cuda", generator=g) for _ in range(8)]
+    x[0, at[0][:100]], x[0, at[0][100:300]] = nan, inf
+    x[1, at[1][:k + 50]] = nan
+    x[2, at[2][:k - 7]] = inf
+    x[3, :V // 2] = nan
+    x[4, 3::8] = inf
+    x[5] = torch.where(torch.rand(V, device="cuda", generator=g) < 0.9, x[5].round(), inf)
+    x[6, at[6][:5]], x[6, at[6][5:V - 40]] = nan, -inf
+    x[7, at[7][:30]] = torch.finfo(torch.bfloat16).max
+    check(x.to(_t(dtype)), k)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
