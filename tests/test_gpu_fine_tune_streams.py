@@ -176,3 +176,31 @@ def test_a_stream_of_another_device_and_tensors_on_the_host_are_refused():
                      lambda: sv.top_logits(x, 2, stream=other), lambda: sv.distill_loss(x, i, v, stream=other)):
             with pytest.raises(ValueError):
                 call()
+
+
+def test_element_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows come out as in a batch of their own."""
+    import torch
+
+    import rejection_sampling_verify_09_amd as sv
+
+    log("[fine-tune] offsets past 32 bits")
+    b = torch.bfloat16
+    rows, d = (1 << 20) + 3000, 2048
+    x, dy = torch.empty((rows, d), device="cuda", dtype=b).normal_(), torch.empty((rows, d), device="cuda", dtype=b).normal_()
+    w = torch.randn((d,), device="cuda").to(b)
+    last = slice(rows - 5, rows)
+    y, _, _ = sv.layer_norm(x, w, w)
+    assert torch.equal(y[last], sv.layer_norm(x[last], w, w)[0])
+    for back in (sv.layer_norm_backward, sv.rms_norm_backward):
+        got = back(dy, x, w, out=y)
+        assert torch.equal(got[0][last], back(dy[last], x[last], w)[0]) and torch.isfinite(got[1]).all()
+    del x, dy, y, got
+    rows, V, k = 17000, 128256, 8
+    x = torch.empty((rows, V), device="cuda", dtype=b).normal_()
+    index = torch.randint(0, V, (rows, k), device="cuda", dtype=torch.int32)
+    values = torch.randn((rows, k), device="cuda")
+    last = slice(rows - 4, rows)
+    want = sv.distill_loss(x[last].clone(), index[last], values[last], with_grad=True)
+    loss, grad = sv.distill_loss(x, index, values, with_grad=True, out_grad=x)
+    assert torch.equal(loss[last], want[0]) and torch.equal(grad[last], want[1]) and torch.isfinite(loss).all()
