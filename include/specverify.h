@@ -632,8 +632,9 @@ int sv_rms_norm_backward(const void* grad, const void* h, const void* weight, co
  *             (whose list is its first k tokens at -inf)
  * temperature finite, >= FLT_MIN (used for out_lse alone)
  *
- * 1 <= k <= min(V, SV_MAX_TOP), 1 <= V <= SV_MAX_V, and rows * min(1024, V / 8
- * or V / 4 in whole waves) threads within one launch (else SV_ERR_SHAPE).
+ * 1 <= k <= min(V, SV_MAX_TOP), 1 <= V <= SV_MAX_V, and the rows' threads (64 to
+ * 1024 a row, by its length) within one launch: up to 2^22 - 1 rows of any
+ * length (else SV_ERR_SHAPE).
  * Overlap of an output with another argument is SV_ERR_PARAM.  rows == 0 does
  * nothing.  Nothing is allocated and no scratch is used.
  */
