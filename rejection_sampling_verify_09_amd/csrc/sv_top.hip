@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
       sm = -INFINITY;
     }
   }
-  // NaN (or an infinity) somewhere: the maxima know nothing of it, so all of the thread's slots are looked at
+  // NaN (or an infinity, or a run of large finite values, as masks are, ahead of others) somewhere: the maxima may know
+  // nothing of it, so all of the thread's slots are marked, to be looked at
   if (sum.s != sum.s)
     for (int s = 0; s < nslots; ++s) slot[s * nt + t] = 0xFFFFFFFFu;
 
@@ -334,8 +335,10 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
     return (int)nlist;
   };
   int n = gather();
+  const uint32_t sure = tau;  // which at least k logits reach, whatever becomes of tau
   if (n > cap && c <= 64) {
-    // a better bound: k of the slots' maxima reach it too
+    // a better bound: k of the slots' maxima reach it too (as a rule: marked slots are left out, and if fewer than k
+    // others reach sure, all of them are above it)
     const TopBins bin(tau, rowmax);
     auto each_slot = [&](auto&& f) {
       for (int s = 0; s < nslots; ++s) {
@@ -356,12 +359,11 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
       if (hist[bin(key)] < k) atomicMin(&found, key);
     });
     __syncthreads();
-    const uint32_t first = tau;
     if (found != 0xFFFFFFFFu) tau = found;
     n = gather();
     if (n < k) {
-      // slots of threads with NaN or infinities were left out, and without them fewer than k reach this one
-      tau = first;
+      // fewer than k logits reach this one
+      tau = sure;
       n = cap + 1;
       above = mhits + 1;
     }
@@ -382,7 +384,8 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
     }
   }
   if (n > cap) {
-    // the k-th largest key, by digits
+    // The k-th largest key, by digits, of the keys that reach the first bound: the second one may be reached by fewer
+    // than k (its list was never formed where there were too many marked slots).
     uint32_t known = 0;
     int left = k;  // its place among those that begin with the known digits
     for (int s = 24; s >= 0; s -= 8) {
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
       for (int i = 0; i < turns; ++i)
         again(i, t, [&](float v, int) {
           const uint32_t key = top_key(v);
-          if (key >= tau && (s == 24 || (key >> (s + 8)) == (known >> (s + 8)))) atomicAdd(&hist[(key >> s) & 255], 1);
+          if (key >= sure && (s == 24 || (key >> (s + 8)) == (known >> (s + 8)))) atomicAdd(&hist[(key >> s) & 255], 1);
         });
       __syncthreads();
       if (t == 0) {
