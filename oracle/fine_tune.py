@@ -32,8 +32,11 @@ def distill_row(logits, index, values, lse=None, temperature=1.0, weight=1.0):
     """(loss, gradient [V], details) of one row: the definition written out, a
     token listed twice counting with both its probabilities.  details: the
     probabilities of the list and the rest, the student's rest, and so on."""
-    s = np.asarray(logits, dtype=np.float64) / temperature
+    s = np.asarray(logits, dtype=np.float64)
     V = s.size
+    # what all logits have in common changes nothing and takes digits
+    top = np.max(s, initial=-np.inf)
+    s = (s - (top if np.isfinite(top) else 0.0)) / temperature
     entries = [(int(i), float(t)) for i, t in zip(index, values) if 0 <= i < V]
     zero = 0.0, np.zeros(V), None
     if weight == 0.0 or (lse is not None and lse == -np.inf):

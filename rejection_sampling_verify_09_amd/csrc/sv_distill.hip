@@ -87,8 +87,10 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
   __shared__ int32_t repeated;
   struct Row {
     // mass: of the student's logits relative to top, inv its reciprocal; total: of the list, norm its reciprocal (1 with
-    // the teacher's log-sum-exp); dot: sum of p (t - s) / T; left: the teacher's rest; coef: of the gradient there
-    double mass, inv, top, total, norm, dot, left;
+    // the teacher's log-sum-exp); dot: sum of p (t - s) / T, s relative to the list's maximum and t too without the
+    // teacher's log-sum-exp, so that what all of a row's logits have in common (1e20 in a row masked altogether) takes no
+    // digits; base: the rest of log p - log q, but for the sums; left: the teacher's rest; coef: of the gradient there
+    double mass, inv, top, total, norm, dot, base, left;
     float coef;
   };
   __shared__ Row fin;
@@ -273,12 +275,12 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
       double sum[3] = {0.0, 0.0, 0.0};  // listed, sum of p, sum of p (t - s) / T
       for (int j = t; j < k; j += nt) {
         if (token[j] < 0) continue;
-        const double y = (double)(j == t ? tv : vp[j]), s = (double)student[j];
-        const double p = exp((y - (a.top_lse ? 0.0 : (double)tm)) * invT - (a.top_lse ? (double)tl : 0.0));
+        const double y = (double)(j == t ? tv : vp[j]) - (a.top_lse ? 0.0 : (double)tm), d = (double)student[j] - s0;
+        const double p = exp(y * invT - (a.top_lse ? (double)tl : 0.0));
         prob[j] = p;
-        if (!(token[j] & 0x40000000)) sum[0] += exp((s - s0) * invT);
+        if (!(token[j] & 0x40000000)) sum[0] += exp(d * invT);
         sum[1] += p;
-        if (p != 0.0) sum[2] += p * ((y - s) * invT);
+        if (p != 0.0) sum[2] += p * ((y - d) * invT);
       }
       const int lw = (min(k, nt) + 63) >> 6;  // waves that have entries
       if (wave < lw) {
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         const double A = __shfl(AB, 0);
         f.mass = A + __shfl(AB, 1);
         f.inv = f.mass == 0.0 ? 0.0 : 1.0 / f.mass;
+        f.base = (f.top - s0) * invT - (a.top_lse ? (double)tl : 0.0);
         f.left = a.top_lse && R0 != 0.0 ? fmax(0.0, 1.0 - sum[1]) : 0.0;
         f.coef = R0 == 0.0 ? 0.0f : (float)((double)w * invT * (A * f.inv - f.left) / R0);
         if (lane == 0) fin = f;
@@ -364,9 +367,8 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         const double lg = log(of);
         const double lm = __shfl(lg, 0), lp = __shfl(lg, 1), lr = __shfl(lg, 2), lR = __shfl(lg, 3);
         // log p_j - log q_j = (t_j - s_j) / T - log of the teacher's sum + log of the student's
-        const double ls = fin.top * invT + lm, lt = a.top_lse ? (double)tl : (double)tm * invT + lp;
         double loss = fin.dot * fin.norm;
-        if (fin.total != 0.0 && loss != INFINITY) loss += fin.total * fin.norm * (ls - lt);
+        if (fin.total != 0.0 && loss != INFINITY) loss += fin.total * fin.norm * (fin.base + lm - (a.top_lse ? 0.0 : lp));
         if (fin.left > 0.0) loss += fin.left * (lr - ((rm - fin.top) * invT + lR - lm));
         if (lane == 0) a.loss[row] = (float)((double)w * loss);
       }
