@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         float first = r[0][0];
 #pragma unroll
         for (int e = 1; e < E; ++e) first = fmaxf(first, r[0][e]);
-        acc.ref = fmaxf(first * scale, -FLT_MAX);
+        acc.ref = fmaxf(first * scale, RunSum::LOW);
       }
       acc.s += acc.sum(r[i], scale);
       acc.now();

@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
       sm = -INFINITY;
     }
   }
-  // NaN (or an infinity, or a run of large finite values, as masks are, ahead of others) somewhere: the maxima may know
-  // nothing of it, so all of the thread's slots are marked, to be looked at
+  // NaN (or an infinity, or a logit that is as good as one) somewhere: the maxima may know nothing of it, so all of the
+  // thread's slots are marked, to be looked at
   if (sum.s != sum.s)
     for (int s = 0; s < nslots; ++s) slot[s * nt + t] = 0xFFFFFFFFu;
 
