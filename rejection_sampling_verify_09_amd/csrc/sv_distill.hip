@@ -129,17 +129,13 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
     for (int i = t; i < at.bytes() / 16; i += nt) reinterpret_cast<uint4*>(marks)[i] = make_uint4(0, 0, 0, 0);
     if (t == 0) repeated = 0;
     __syncthreads();
-    // entry j's token, or -1; the first of a token listed more than once stands for its q
+    // entry j's token, or -1
     auto mark = [&](int j, int v) {
-      int to = v >= 0 && v < V ? v : -1;
-      if (to >= 0) {
+      token[j] = v >= 0 && v < V ? v : -1;
+      if (v >= 0 && v < V) {
         const uint32_t b = at.bit(v);
-        if (atomicOr(&marks[b >> 5], 1u << (b & 31)) >> (b & 31) & 1) {
-          to = v | 0x40000000;
-          repeated = 1;
-        }
+        if (atomicOr(&marks[b >> 5], 1u << (b & 31)) >> (b & 31) & 1) repeated = 1;
       }
-      token[j] = to;
     };
     const bool here = t < k && iv >= 0 && iv < V;
     const float sv = load1<IN>(x, here ? iv : 0);
@@ -220,7 +216,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
     };
     if (here) entry(t, tv, sv);
     for (int j = t + nt; j < k; j += nt)
-      if (token[j] >= 0) entry(j, vp[j], load1<IN>(x, token[j] & 0x3FFFFFFF));
+      if (token[j] >= 0) entry(j, vp[j], load1<IN>(x, token[j]));
     const float wr = dpp_wave_fmax(acc.ref);
     const float ws = dpp_wave_fsum(acc.s * __builtin_amdgcn_exp2f(acc.ref - wr));
     tm = dpp_wave_fmax(tm), sm = dpp_wave_fmax(sm);
@@ -278,7 +274,11 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         const double y = (double)(j == t ? tv : vp[j]) - (a.top_lse ? 0.0 : (double)tm), d = (double)student[j] - s0;
         const double p = exp(y * invT - (a.top_lse ? (double)tl : 0.0));
         prob[j] = p;
-        if (!(token[j] & 0x40000000)) sum[0] += exp(d * invT);
+        // the first of a token listed more than once stands for its q
+        bool first = true;
+        if (repeated)
+          for (int o = 0; o < j; ++o) first &= token[o] != token[j];
+        if (first) sum[0] += exp(d * invT);
         sum[1] += p;
         if (p != 0.0) sum[2] += p * ((y - d) * invT);
       }
@@ -350,12 +350,12 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         __syncthreads();  // the listed tokens' own values come after
         for (int j = t; j < k; j += nt) {
           if (token[j] < 0) continue;
-          const int v = token[j] & 0x3FFFFFFF;
+          const int v = token[j];
           double p = prob[j];
           if (repeated) {
             p = 0.0;
             for (int o = 0; o < k; ++o)
-              if (token[o] >= 0 && (token[o] & 0x3FFFFFFF) == v) p += prob[o];
+              if (token[o] == v) p += prob[o];
           }
           const double q = exp(((double)student[j] - fin.top) * invT) * fin.inv;
           store1<IN>(grad, v, (float)((double)w * invT * ((student[j] == -INFINITY ? 0.0 : q) - p * fin.norm)));
