@@ -672,7 +672,10 @@ int sv_top_logits(const void* logits, int32_t k, float temperature, float* out_v
  *             be logits itself (in place)
  *
  * A token listed twice counts with both its p, and its q once.  A row without a
- * teacher (no entry above -inf, or a top_lse of -inf) has loss 0 and gradient 0.
+ * teacher (a top_lse of -inf or, without top_lse, no entry above -inf) has loss 0
+ * and gradient 0.  With a finite top_lse a list that has no entry above -inf
+ * leaves the rest all of the teacher's mass (r = 1), by the formula; if no entry
+ * is in [0, V), that comes to exactly 0, loss and gradient.
  * The student's logits may be -inf: q is 0 there, and the loss is +inf where p
  * is not.  Where every token that is not listed is at -inf, their term is left
  * out (r is then no more than the rounding of top_lse).  NaN and +inf logits make

@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         f.inv = f.mass == 0.0 ? 0.0 : 1.0 / f.mass;
         f.base = (f.top - s0) * invT - (a.top_lse ? (double)tl : 0.0);
         f.left = a.top_lse && R0 != 0.0 ? fmax(0.0, 1.0 - sum[1]) : 0.0;
-        f.coef = R0 == 0.0 ? 0.0f : (float)((double)w * invT * (A * f.inv - f.left) / R0);
+        // A / mass, not a product with inv: exactly 1, as left is, for a list without entries
+        f.coef = R0 == 0.0 ? 0.0f : (float)((double)w * invT * (A / f.mass - f.left) / R0);
         if (lane == 0) fin = f;
       }
       __syncthreads();
