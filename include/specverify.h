@@ -678,9 +678,11 @@ int sv_top_logits(const void* logits, int32_t k, float temperature, float* out_v
  * is in [0, V), that comes to exactly 0, loss and gradient.
  * The student's logits may be -inf: q is 0 there, and the loss is +inf where p
  * is not.  Where every token that is not listed is at -inf, their term is left
- * out (r is then no more than the rounding of top_lse).  NaN and +inf logits make
- * the row's loss and gradient NaN.  The list's sums and the loss are float64,
- * the sums over the vocabulary float32; loss and gradient are rounded once.
+ * out (r is then no more than the rounding of top_lse).  NaN and +inf logits, a
+ * NaN top_lse, and a p of NaN (a NaN value, or +inf without a finite top_lse) make
+ * the row's loss and all of its gradient NaN.  The list's sums and the loss are
+ * float64, the sums over the vocabulary float32; loss and gradient are rounded
+ * once.
  * 1 <= k <= SV_MAX_TOP, 1 <= V <= SV_MAX_DISTILL_V, and threads within one
  * launch as for sv_top_logits (else SV_ERR_SHAPE).  Any overlap of an output
  * with another argument but out_grad == logits is SV_ERR_PARAM.  rows == 0 does

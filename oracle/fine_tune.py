@@ -48,6 +48,8 @@ def distill_row(logits, index, values, lse=None, temperature=1.0, weight=1.0):
     p = np.exp(t - (log_sum_exp(t) if lse is None else float(lse)))
     r = 0.0 if lse is None else max(0.0, 1.0 - float(np.sum(p)))
     ls = log_sum_exp(s)
+    if np.isnan(np.sum(p)) or (lse is not None and np.isnan(lse)) or np.isnan(s).any() or top == np.inf:
+        return float("nan"), np.full(V, np.nan), dict(p=p)
     listed = np.zeros(V, dtype=bool)
     listed[at] = True
     rest = log_sum_exp(s[~listed])

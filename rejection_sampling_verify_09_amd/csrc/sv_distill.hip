@@ -314,6 +314,9 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         f.left = a.top_lse && R0 != 0.0 ? fmax(0.0, 1.0 - sum[1]) : 0.0;
         // A / mass, not a product with inv: exactly 1, as left is, for a list without entries
         f.coef = R0 == 0.0 ? 0.0f : (float)((double)w * invT * (A / f.mass - f.left) / R0);
+        // NaN somewhere in the teacher or the student, which the maximum above and a rest of 0 would hide
+        const double all = sum[1] + f.mass + (a.top_lse ? (double)tl : 0.0);
+        if (all != all) f.norm = NAN, f.coef = NAN;
         if (lane == 0) fin = f;
       }
       __syncthreads();
