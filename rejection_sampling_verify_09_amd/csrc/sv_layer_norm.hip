@@ -222,8 +222,15 @@ struct BackArgs {
   float* dw;  // [groups][stride] sums over each workgroup's rows, or NULL
   float* db;
   int32_t rows, d, stride;
+  size_t fold;  // wide rows: floats from a part to where it is folded
   float eps;
 };
+
+// Rows that are added to a sum one after another before it is set aside and
+// begun anew: a workgroup's sum of n rows by itself is off by up to n 2^-24 of
+// the magnitudes' sum (2^30 rows on 256 workgroups: by a fourth), folded by (1024
+// + n / 1024) 2^-24.
+constexpr int BACK_TURNS = 1024;
 
 // What the sums over one row give: the factors of
 // dh = r (g - gm - (c - left) r gn).
@@ -277,7 +284,12 @@ struct Raw8 {
 // that would end past the row begins earlier: it reads, forms and writes some
 // of its neighbour's columns once more, with the same result, and leaves them
 // out of its sums.
-template <int IN, bool CENTER, int VPT, bool RES>
+//
+// FOLD: a workgroup has more than BACK_TURNS turns.  In the other kernels it would
+// cost registers (two runs a thread: 8192 x 16384 bfloat16 with a residual's
+// gradient 236 us, 243 so); where it is needed, 270000 x 16384 takes 6.7 to 6.9 ms,
+// 6.4 without, 1000000 x 1024 1.48 either way.
+template <int IN, bool CENTER, int VPT, bool RES, bool FOLD>
 __global__ void __launch_bounds__(1024) norm_backward_kernel(BackArgs a) {
   extern __shared__ __attribute__((aligned(16))) float smem[];
   const int t = threadIdx.x, nt = blockDim.x, nw = nt >> 6, ny = blockDim.y;
@@ -400,8 +412,35 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(BackArgs a) {
     // all of it: in the loop each wait can then count on the store behind the loads
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   }
-  for (; first + ny <= a.rows; first += step) body(std::true_type{}, true);
-  if (first < a.rows) body(std::false_type{}, row < a.rows);
+  if constexpr (FOLD) {
+    // in LDS, where no load and no store of the rows has to be waited for; addresses anew each time, for their registers
+    bool folded = false;
+    auto each_sum = [&](auto&& f) {
+      const int threads = blockDim.x * blockDim.y;
+      float* fold = smem + blockDim.y * 160 + threadIdx.y * blockDim.x + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          f(sw[i][k], fold[(i * 8 + k) * threads]);
+          if (CENTER) f(sb[i][k], fold[(VPT * 8 + i * 8 + k) * threads]);
+        }
+    };
+    while (true) {
+      for (int n = 0; n < BACK_TURNS && first + ny <= a.rows; ++n, first += step) body(std::true_type{}, true);
+      if (first + ny > a.rows) break;
+      each_sum([&](float& v, float& f) {
+        f = folded ? f + v : v;
+        v = 0.0f;
+      });
+      folded = true;
+    }
+    if (first < a.rows) body(std::false_type{}, row < a.rows);
+    if (folded) each_sum([&](float& v, float& f) { v += f; });
+  } else {
+    for (; first + ny <= a.rows; first += step) body(std::true_type{}, true);
+    if (first < a.rows) body(std::false_type{}, row < a.rows);
+  }
   if (!a.dw && !a.db) return;
   // rows of the workgroup, then the workgroup's part of the workspace
   if (ny > 1) {
@@ -449,8 +488,22 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(BackArgs a) {
   const float inv = 1.0f / (float)a.d;
   float* dw = a.dw ? a.dw + (size_t)blockIdx.x * a.stride : nullptr;
   float* db = a.db ? a.db + (size_t)blockIdx.x * a.stride : nullptr;
-  int turn = 0;
-  for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+  // 8 columns' sums so far, added to what was set aside before; more: there is something
+  auto set_aside = [&](int j, bool more) {
+    for (float* p : {dw, db}) {
+      if (!p) continue;
+      float s[8], f[8];
+      load8<T_F32, false>(reinterpret_cast<char*>(p + j), s, a.d - j);
+      if (more) {
+        load8<T_F32, false>(reinterpret_cast<char*>(p + a.fold + j), f, a.d - j);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[k] += f[k];
+      }
+      store8<T_F32, false>(reinterpret_cast<char*>(p + a.fold + j), s, a.d - j);
+    }
+  };
+  int turn = 0, n = 0;
+  for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1, ++n) {
     const size_t base = (size_t)row * a.d;
     const char* hp = static_cast<const char*>(a.h) + base * IB;
     const char* dyp = static_cast<const char*>(a.dy) + base * IB;
@@ -495,7 +548,8 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(BackArgs a) {
       load8<IN, false>(dyp + (size_t)j * IB, dy, a.d - j);
       if (wp) load8<IN, false>(wp + (size_t)j * IB, w, a.d - j);
       if (a.dres) load8<IN, false>(static_cast<const char*>(a.dres) + (base + j) * IB, o, a.d - j);
-      const bool begun = row >= (int)gridDim.x;
+      const bool begun = n % BACK_TURNS != 0;
+      if (!begun && n > 0) set_aside(j, n > BACK_TURNS);
 #pragma unroll
       for (int k = 0; k < 8; ++k) sw[k] = sb[k] = 0.0f;
       if (begun && dw) load8<T_F32, false>(reinterpret_cast<char*>(dw + j), sw, a.d - j);
@@ -512,6 +566,17 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(BackArgs a) {
       if (db) store8<T_F32, false>(reinterpret_cast<char*>(db + j), sb, a.d - j);
     }
   }
+  if (n <= BACK_TURNS) return;
+  for (int j = t * 8; j < a.d; j += nt * 8)
+    for (float* p : {dw, db}) {
+      if (!p) continue;
+      float s[8], f[8];
+      load8<T_F32, false>(reinterpret_cast<char*>(p + j), s, a.d - j);
+      load8<T_F32, false>(reinterpret_cast<char*>(p + a.fold + j), f, a.d - j);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[k] += f[k];
+      store8<T_F32, false>(reinterpret_cast<char*>(p + j), s, a.d - j);
+    }
 }
 
 // Column sums of the workgroups' parts: 64 columns a workgroup, 16 threads of 4
@@ -544,6 +609,7 @@ __global__ void __launch_bounds__(1024) norm_backward_sum_kernel(const float* wp
   out[col] = v;
 }
 
+constexpr int BACK_LDS = (160 + 1024 * 2 * 16) * 4;  // two runs a thread
 constexpr int BACK_ROWS = 1 << 30;  // a workgroup's next row stays within 32 bits
 
 // A row's threads and runs, rows a workgroup, and workgroups: what the workspace
@@ -555,7 +621,7 @@ constexpr int BACK_ROWS = 1 << 30;  // a workgroup's next row stays within 32 bi
 // of 4096 5.7 us against 6.7, 4 rows 8.3 against 6.7).
 struct BackPlan {
   int nt, ny, vpt, groups, stride;
-  bool wide;
+  bool wide, fold;
   BackPlan(int rows, int d) {
     const int nv = (d + 7) / 8;
     wide = d < 8 || nv > 2048;
@@ -566,8 +632,12 @@ struct BackPlan {
     const int each = std::max(turns <= 2 ? turns : 1, (turns + 255) / 256);
     groups = turns == 0 ? 0 : (turns + each - 1) / each;
     stride = (d + 3) / 4 * 4;
+    fold = each > BACK_TURNS;
   }
-  size_t lds() const { return ((size_t)ny * 160 + (ny > 1 ? (size_t)nt * vpt * 16 : 0)) * 4; }
+  // the reductions', and where sums are folded and, behind the last row, the workgroup's rows joined
+  size_t lds() const { return ((size_t)ny * 160 + (fold ? (size_t)ny : ny > 1 ? 1 : 0) * nt * vpt * 16) * 4; }
+  // floats of a sum's parts
+  int64_t part() const { return groups > 1 ? (int64_t)groups * stride * (wide && fold ? 2 : 1) : 0; }
 };
 
 template <int IN, bool CENTER>
@@ -577,12 +647,16 @@ hipError_t launch_back(const BackArgs& a, const BackPlan& l, hipStream_t s) {
     hipLaunchKernelGGL((norm_backward_wide_kernel<IN, CENTER>), grid, wg, 0, s, a);
     return hipGetLastError();
   }
-  auto go = [&](auto vpt, auto res) {
-    hipLaunchKernelGGL((norm_backward_kernel<IN, CENTER, decltype(vpt)::value, decltype(res)::value>), grid, wg, l.lds(), s, a);
+  hipError_t e = hipSuccess;
+  auto go = [&](auto vpt, auto res, auto fold) {
+    constexpr auto kernel = norm_backward_kernel<IN, CENTER, decltype(vpt)::value, decltype(res)::value, decltype(fold)::value>;
+    if (l.fold) e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, BACK_LDS);
+    if (e == hipSuccess) hipLaunchKernelGGL(kernel, grid, wg, l.lds(), s, a);
   };
-  auto width = [&](auto vpt) { a.dres ? go(vpt, std::true_type{}) : go(vpt, std::false_type{}); };
+  auto sums = [&](auto vpt, auto res) { l.fold ? go(vpt, res, std::true_type{}) : go(vpt, res, std::false_type{}); };
+  auto width = [&](auto vpt) { a.dres ? sums(vpt, std::true_type{}) : sums(vpt, std::false_type{}); };
   l.vpt == 1 ? width(std::integral_constant<int, 1>{}) : width(std::integral_constant<int, 2>{});
-  return hipGetLastError();
+  return e == hipSuccess ? hipGetLastError() : e;
 }
 
 int norm_backward(bool center, const void* grad, const void* h, const void* weight, const void* grad_residual, float eps,
@@ -594,8 +668,8 @@ int norm_backward(bool center, const void* grad, const void* h, const void* weig
   const BackPlan l(rows, d);
   const int groups = l.groups;
   const size_t ie = (size_t)type_bytes(dtype), nin = (size_t)rows * (size_t)d * ie, nw = (size_t)d * ie;
-  const size_t np = (size_t)d * 4, one = (size_t)groups * (size_t)l.stride * 4;
-  const size_t ws = groups > 1 ? one * ((grad_weight ? 1 : 0) + (grad_bias ? 1 : 0)) : 0;
+  const size_t np = (size_t)d * 4, one = (size_t)l.part() * 4;
+  const size_t ws = one * ((grad_weight ? 1 : 0) + (grad_bias ? 1 : 0));
   if (rows > 0 && (!grad || !h || !grad_h)) return SV_ERR_NULL;
   if (ws && !workspace) return SV_ERR_NULL;
   if (ws && workspace_bytes < (int64_t)ws) return SV_ERR_WORKSPACE;
@@ -629,6 +703,7 @@ int norm_backward(bool center, const void* grad, const void* h, const void* weig
   a.dw = !grad_weight ? nullptr : groups > 1 ? reinterpret_cast<float*>(part) : grad_weight;
   a.db = !grad_bias ? nullptr : groups > 1 ? reinterpret_cast<float*>(part + (grad_weight ? one : 0)) : grad_bias;
   a.stride = l.stride;
+  a.fold = (size_t)groups * l.stride;
   if (rows > 0) {
     const hipError_t e = center ? (dtype == SV_F32 ? launch_back<T_F32, true>(a, l, s) : launch_back<T_BF16, true>(a, l, s))
                                 : (dtype == SV_F32 ? launch_back<T_F32, false>(a, l, s) : launch_back<T_BF16, false>(a, l, s));
@@ -699,7 +774,7 @@ extern "C" int sv_layer_norm(const void* x, const void* residual, const void* we
 extern "C" int64_t sv_norm_backward_workspace(int32_t rows, int32_t d) {
   if (rows < 0 || rows > BACK_ROWS || d < 1 || d > SV_MAX_NORM_D) return SV_ERR_SHAPE;
   const BackPlan l(rows, d);
-  return l.groups > 1 ? (int64_t)l.groups * l.stride * 8 : 0;
+  return l.part() * 8;
 }
 
 extern "C" int sv_layer_norm_backward(const void* grad, const void* h, const void* weight, const void* grad_residual,
