@@ -39,13 +39,21 @@ def _run(cmd, verbose: bool) -> None:
         raise RuntimeError(f"hipcc failed with exit code {r.returncode}")
 
 
+def _jobs() -> int:
+    """Compilers at a time: MAX_JOBS if that is a number above 0, else the processors, at most 8 and a source each."""
+    try:
+        n = int(os.environ.get("MAX_JOBS", ""))
+    except ValueError:
+        n = 0
+    return max(1, min(len(SOURCES), n if n > 0 else os.cpu_count() or 1, 8))
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source, side by side, and link them into libspecverify.so; returns its path."""
     tmp = LIB + ".tmp"
     with tempfile.TemporaryDirectory() as d:
         objs = [os.path.join(d, s + ".o") for s in SOURCES]
-        jobs = max(1, min(len(SOURCES), int(os.environ.get("MAX_JOBS", 0)) or os.cpu_count() or 1, 8))
-        with concurrent.futures.ThreadPoolExecutor(jobs) as pool:
+        with concurrent.futures.ThreadPoolExecutor(_jobs()) as pool:
             list(pool.map(lambda so: _run([HIPCC, *FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-c", os.path.join(CSRC, so[0]), "-o",
                                            so[1]], verbose), zip(SOURCES, objs)))
         _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs], verbose)
