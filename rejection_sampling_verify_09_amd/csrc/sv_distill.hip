@@ -408,13 +408,17 @@ struct DistillLaunch {
   }
 };
 
+// What a launch takes at most: the longest list and the longest row, a bit a token.  Calls of several threads set the same
+// limit: one of their own could lower another's between its setting and its launch.
+constexpr int DISTILL_LDS = SV_MAX_TOP * 16 + SV_MAX_DISTILL_V / 8;
+
 template <int IN, int NH, bool MORE, bool TINY>
 hipError_t launch_distill(const DistillArgs& a, const DistillLaunch& l, hipStream_t s) {
   const Marks at{Run<IN>::E, l.nt, NH, MORE ? ((a.V + Run<IN>::E - 1) / Run<IN>::E + l.nt - 1) / l.nt : NH};
   const size_t lds = (size_t)a.k * 16 + (size_t)at.bytes();
   if (lds > 48 * 1024) {
     const hipError_t e = hipFuncSetAttribute((const void*)distill_kernel<IN, NH, MORE, TINY>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, DISTILL_LDS);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((distill_kernel<IN, NH, MORE, TINY>), dim3((unsigned)a.rows), dim3((unsigned)l.nt), lds, s, a);

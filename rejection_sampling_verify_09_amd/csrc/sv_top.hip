@@ -500,12 +500,16 @@ __global__ void __launch_bounds__(1024) top_kernel(TopArgs a) {
   }
 }
 
+// What a launch takes at most.  Calls of several threads set the same limit: one of their own could lower another's
+// between its setting and its launch.
+constexpr int TOP_LDS = TOP_CAP * 8 + (TOP_HITS + TOP_SLOTS * 1024) * 4;
+
 template <int IN, bool TINY>
 hipError_t launch_top(const TopArgs& a, const TopShape& l, hipStream_t s) {
   const size_t lds = l.lds(a.V, a.k);
   if (lds > 32 * 1024) {
     const hipError_t e =
-        hipFuncSetAttribute((const void*)top_kernel<IN, TINY>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        hipFuncSetAttribute((const void*)top_kernel<IN, TINY>, hipFuncAttributeMaxDynamicSharedMemorySize, TOP_LDS);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((top_kernel<IN, TINY>), dim3((unsigned)a.rows), dim3((unsigned)l.nt), lds, s, a);
