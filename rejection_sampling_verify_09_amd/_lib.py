@@ -512,7 +512,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     (then with one float32 scale per row: the row is out * out_scale).
     Returns (out, out_scale [...] or None, h rounded to x's type or None
     without a residual).  out and out_residual may be x or residual (in
-    place)."""
+    place).  The outputs carry no gradient of autograd's: rms_norm_backward is
+    the gradient."""
     code = _code(x.dtype, "x", _FLOATS)
     out_dtype = x.dtype if out_dtype is None else out_dtype
     ocode = _code(out_dtype, "out_dtype", _CODES)
@@ -559,7 +560,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     [..., R] of out_dtype (float32 or bfloat16), R dividing N: output column n
     adds residual column n mod R (several draft heads stacked along N share
     one residual).  activation: "none", "relu", "silu", "gelu" or "gelu_tanh".
-    Returns out [..., N]."""
+    Returns out [..., N], which carries no gradient of autograd's."""
     code = _code(x.dtype, "x", _OPERANDS)
     ocode = _code(out_dtype, "out_dtype", _FLOATS)
     if activation not in ACTIVATIONS:
@@ -713,7 +714,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     (x's type by default) or float8_e4m3fn (then with one float32 scale per
     row: the row is out * out_scale).  Returns (out, out_scale [...] or None, h
     rounded to x's type or None without a residual).  out and out_residual may
-    be x or residual (in place)."""
+    be x or residual (in place).  The outputs carry no gradient of autograd's:
+    layer_norm_backward is the gradient."""
     code = _code(x.dtype, "x", _FLOATS)
     out_dtype = x.dtype if out_dtype is None else out_dtype
     ocode = _code(out_dtype, "out_dtype", _CODES)
@@ -887,7 +889,8 @@ def distill_loss(logits: torch.Tensor, top_index: torch.Tensor, top_values: torc
     (0: the row is left out).  Returns (loss [...] float32 or None, the
     gradient of the sum of loss with respect to logits, of its shape and type,
     or None): both in one pass with with_grad, the gradient alone with
-    with_loss=False.  out_grad may be logits (in place)."""
+    with_loss=False.  out_grad may be logits (in place).  The loss carries no
+    gradient of autograd's: the second output is the gradient."""
     code = _code(logits.dtype, "logits", _FLOATS)
     if logits.dim() < 1 or logits.shape[-1] < 1 or top_index.dim() < 1 or top_index.shape[-1] < 1:
         raise ValueError("logits must be [..., V] and top_index [..., k]")
