@@ -21,12 +21,12 @@
 // What is done once an entry is done in 64 bits: there are few, and the loss is
 // a difference of numbers close to each other.
 //
-// 448 x 128256 bfloat16 with an eighth of the rows left out and lists of 64: 53 us
-// (4.1 TB/s of what must be read and written; a large copy reaches 5.0), of
+// 448 x 128256 bfloat16 with an eighth of the rows left out and lists of 64: 51 us
+// (4.2 TB/s of what must be read and written; a large copy reaches 5.0), of
 // which the vector units are busy for half: two exponentials a logit at a
 // quarter of the rate, and the 256 compute units hold 256 rows at a time, in
 // step, so that loads, sums, gradient and stores take turns.  2304 x 152064
-// float32: 607 us (4.6 TB/s).  A single row takes 19 us, 12 of them instructions.
+// float32: 608 us (4.6 TB/s).  A single row takes 19 us, 12 of them instructions.
 // What made the difference (448 x 128256): registers instead of three reads
 // (185 -> 82 us); loads outside branches, at whose ends the compiler waits for
 // all of them, and columns formed anew in each pass instead of being kept

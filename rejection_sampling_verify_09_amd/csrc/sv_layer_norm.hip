@@ -12,15 +12,16 @@
 // the row has to be read in any case, and nothing else is kept from the
 // forward pass.
 //
-// Bound by memory from a few MB on: 16384 x 8192 bfloat16 take 190 to 200 us
-// forward with a residual (5.4 to 5.6 TB/s; a large copy reaches 5.0) and 195 to
-// 200 us backward with a residual's gradient (5.4 TB/s); below that by the
-// launches and by a row's two reductions one after the other: one row of 4096
-// takes 2.5 us forward, 448 rows backward 9.4 + 3.8 us.  What holds the backward
-// pass back elsewhere is instructions: at first 56 a column (separate products
-// and sums, divisions, masks for columns past the row), 74% of the cycles, now
-// with fused multiply-adds and the masks in the one wave that needs them about
-// 30, and the same 16384 x 8192 went from 247 to 200 us.
+// Bound by memory from a few MB on: 16384 x 8192 bfloat16 take 187 us a call and
+// 195 traced alone forward with a residual (5.7 and 5.5 TB/s; a large copy
+// reaches 5.0), 196 and 204 backward with a residual's gradient (5.5 and 5.3);
+// below that by the launches and by a row's two reductions one after the other:
+// one row of 4096 takes 2.4 us forward, 448 rows backward 9 to 10 + 3.8 us.  What
+// holds the backward pass back elsewhere is instructions: at first 56 a column
+// (separate products and sums, divisions, masks for columns past the row), 74% of
+// the cycles, now with fused multiply-adds and the masks in the one wave that
+// needs them about 30, and the same 16384 x 8192 went from 247 to 200 us in a
+// graph.
 #include "sv_ops.hpp"
 #include "specverify.h"
 
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(BackArgs a) {
 // Rows of other widths (up to 7, or above 16384 columns, whose sums the registers
 // do not hold): a workgroup takes a row at a time, reads it again for each step,
 // and keeps the sums for the weights in its part of the workspace (1024 x 40000
-// bfloat16 218 us, a third of the rate of the other kernel).
+// bfloat16 199 us, with a residual's gradient 224, a fourth of the other kernel's rate).
 template <int IN, bool CENTER>
 __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(BackArgs a) {
   __shared__ __attribute__((aligned(16))) float part[2][80];
@@ -616,8 +617,8 @@ constexpr int BACK_ROWS = 1 << 30;  // a workgroup's next row stays within 32 bi
 // holds a part for.  One compute unit a workgroup, with equal turns (16384 x 8192
 // bfloat16 with 128, 224, 256, 384 and 512 workgroups 430, 215, 202, over 300 and
 // 213 us; 448 x 4096, where the parts count, 13.1 with 112, 13.4 with 224, 16.3
-// with 448), of at least 512 threads (16384 x 1024 with 256, 512 and 1024 threads
-// 45, 34 and 35 us).  One workgroup without parts to join up to two turns (2 rows
+// with 448), of at least 512 threads (16384 x 1024 with a residual's gradient
+// with 256, 512 and 1024 threads 45, 34 and 35 us).  One workgroup without parts to join up to two turns (2 rows
 // of 4096 5.7 us against 6.7, 4 rows 8.3 against 6.7).
 struct BackPlan {
   int nt, ny, vpt, groups, stride;
