@@ -74,3 +74,33 @@ def test_roundings_do_not_add_up(rows, d):
         if gb is not None:
             assert ((gb.double() - want).abs() <= tol * want).all(), (name, gb / want)
         del out
+
+
+@pytest.mark.parametrize("rows,d,dtype", [(2200001, 24, "bf16"), (600001, 4, "f32"), (266001, 16400, "bf16"), (264001, 10000, "bf16")])
+def test_one_sum_alone_in_place_and_in_a_graph(rows, d, dtype):
+    """Folded sums: one of the two alone, grad_h over its inputs, and captured and replayed, give the same bits."""
+    import torch
+
+    import rejection_sampling_verify_09_amd as sv
+
+    log(f"[norm sums] forms rows={rows} d={d} {dtype}")
+    t = _t(dtype)
+    h, dy = torch.empty((rows, d), device="cuda", dtype=t).normal_(), torch.empty((rows, d), device="cuda", dtype=t).normal_()
+    dres = torch.empty((rows, d), device="cuda", dtype=t).normal_()
+    want = sv.layer_norm_backward(dy, h, grad_residual=dres)
+    dh = want[0]
+    for kw in (dict(with_bias=False), dict(with_weight=False)):
+        _, dw, db = sv.layer_norm_backward(dy, h, grad_residual=dres, out=dh, **kw)
+        assert (dw is None or torch.equal(dw, want[1])) and (db is None or torch.equal(db, want[2]))
+    keep = dh.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = sv.layer_norm_backward(dy, h, grad_residual=dres, out=dh)
+    for _ in range(3):
+        dh.zero_(), got[1].zero_(), got[2].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dh, keep) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    del graph, dh
+    got = sv.layer_norm_backward(dy, h, grad_residual=dres, out=dres)
+    assert torch.equal(got[0], keep) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
