@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
     if (t < k) mark(t, iv);
     for (int j = t + nt; j < k; j += nt) mark(j, ip[j]);
     __syncthreads();
+    const int twice = __builtin_amdgcn_readfirstlane(repeated);  // some token is listed more than once
     // the rest's maximum and sum
     auto take = [&](Run<IN>& v, int i, uint32_t mask) {
       const int j = j0 + i * (nt * E);
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         prob[j] = p;
         // the first of a token listed more than once stands for its q
         bool first = true;
-        if (repeated)
+        if (twice)
           for (int o = 0; o < j; ++o) first &= token[o] != token[j];
         if (first) sum[0] += exp(d * invT);
         sum[1] += p;
@@ -312,8 +313,8 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
         f.inv = f.mass == 0.0 ? 0.0 : 1.0 / f.mass;
         f.base = (f.top - s0) * invT - (a.top_lse ? (double)tl : 0.0);
         f.left = a.top_lse && R0 != 0.0 ? fmax(0.0, 1.0 - sum[1]) : 0.0;
-        // A / mass, not a product with inv: exactly 1, as left is, for a list without entries
-        f.coef = R0 == 0.0 ? 0.0f : (float)((double)w * invT * (A / f.mass - f.left) / R0);
+        const double R = A == f.mass ? 1.0 : A * f.inv;  // exactly 1, as left is, for a list without entries
+        f.coef = R0 == 0.0 ? 0.0f : (float)((double)w * invT * (R - f.left) / R0);
         // NaN somewhere in the teacher or the student, which the maximum above and a rest of 0 would hide
         const double all = sum[1] + f.mass + (a.top_lse ? (double)tl : 0.0);
         if (all != all) f.norm = NAN, f.coef = NAN;
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(1024) distill_kernel(DistillArgs a) {
           if (token[j] < 0) continue;
           const int v = token[j];
           double p = prob[j];
-          if (repeated) {
+          if (twice) {
             p = 0.0;
             for (int o = 0; o < k; ++o)
               if (token[o] == v) p += prob[o];
