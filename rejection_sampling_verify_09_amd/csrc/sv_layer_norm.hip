@@ -13,10 +13,10 @@
 // forward pass.
 //
 // Bound by memory from a few MB on: 16384 x 8192 bfloat16 take 187 us a call and
-// 195 traced alone forward with a residual (5.7 and 5.5 TB/s; a large copy
+// 196 traced alone forward with a residual (5.7 and 5.5 TB/s; a large copy
 // reaches 5.0), 196 and 204 backward with a residual's gradient (5.5 and 5.3);
 // below that by the launches and by a row's two reductions one after the other:
-// one row of 4096 takes 2.4 us forward, 448 rows backward 9 to 10 + 3.8 us.  What
+// one row of 4096 takes 2.5 us forward, 448 rows backward 9 to 10 + 3.6 us.  What
 // holds the backward pass back elsewhere is instructions: at first 56 a column
 // (separate products and sums, divisions, masks for columns past the row), 74% of
 // the cycles, now with fused multiply-adds and the masks in the one wave that

@@ -19,7 +19,7 @@
 //
 // 2304 x 152064 float32 with k = 256 take 278 us (5.0 TB/s, a large copy's rate);
 // 448 x 128256 bfloat16 with k = 64 31 us (3.7 TB/s), where the vector units are
-// busy for 56% of the cycles (the exponentials above all) and the rest is the
+// busy for 55% of the cycles (the exponentials above all) and the rest is the
 // steps after the sums, one after another; one row 16 us, of which 7 are
 // instructions.  What made the difference (448 x 128256 with k = 64): slot maxima
 // and reading a few slots again instead of the row (123 -> 38 us); the wave's
